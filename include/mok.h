@@ -287,6 +287,112 @@ mok_status_t mok_moe_fwd_noalloc(const mok_desc_t* desc, const void* x, const in
                                  const uint8_t* s_down, void* y, uint32_t* dev_status,
                                  void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Row operators: tokens to expert order and back, for expert functions that are not the
+ * layer's own ([L] section 01: keep one expert's rows contiguous; [L] section 03: the
+ * final weighted sum).  They read one table, pos [T, k] int32 as mok_schedule writes it
+ * (mok_schedule_tables, or in place: mok_schedule_layout): pos[t*k+j] is the routed row
+ * of pair (t, j), or -1.  Every routed row has one pair.
+ *
+ * Common rules.  `type` is the element type of every row operand (MOK_TYPE_*); sums run
+ * in fp32 and are rounded once.  A row operand is `ld` elements from row to row; cols a
+ * multiple of 8, 8..65536; ld a multiple of 8, at least cols (a read operand may also have
+ * ld 0: every row the same); bases 16-byte aligned.  tokens 0..2^24, top_k 1..64,
+ * tokens*top_k at most 2^24.  topk_w, d_topk_w: [T, k] fp32.  A pair whose pos lies
+ * outside [0, max_rows) has no row and is skipped, its weight unread; rows without a pair
+ * are neither read nor written, so max_rows may exceed the routed rows (their number
+ * stays on the device).  Outputs must not overlap inputs.  With tokens 0 nothing is done
+ * (the pointers may be NULL); with max_rows 0 the rows pointer may be NULL.  Errors:
+ * MOK_E_NULL, MOK_E_SHAPE, MOK_E_UNSUPPORTED (type), MOK_E_LAUNCH.  Asynchronous on
+ * stream, one launch each, no workspace; fixed-order sums, bitwise repeatable. */
+#define MOK_TYPE_BF16 0
+#define MOK_TYPE_FP16 1
+#define MOK_TYPE_FP32 2
+
+/* Where the schedule's tables lie in the workspace (host only): byte offsets from the
+ * workspace start of offsets [E_loc + 1] and pos [T*k], both int32, for the operators
+ * that read them in place on the schedule's stream.  Either may be NULL.  Errors:
+ * MOK_E_NULL (desc), the descriptor's errors. */
+mok_status_t mok_schedule_layout(const mok_desc_t* desc, size_t* offsets_bytes,
+                                 size_t* pos_bytes);
+
+/* rows[pos[t,j]] = x[t] for every pair with a row.  x [T, cols] (ld_x), rows
+ * [max_rows, cols] (ld_rows). */
+mok_status_t mok_permute(int32_t type, const void* x, int64_t ld_x, const int32_t* pos,
+                         int64_t tokens, int32_t top_k, int32_t cols, void* rows,
+                         int64_t ld_rows, int64_t max_rows, void* stream);
+
+/* Gradient of mok_permute: dx[t] = sum over j in ascending order of d_rows[pos[t,j]];
+ * 0 for a token without rows. */
+mok_status_t mok_permute_bwd(int32_t type, const void* d_rows, int64_t ld_rows,
+                             int64_t max_rows, const int32_t* pos, int64_t tokens,
+                             int32_t top_k, int32_t cols, void* dx, int64_t ld_x,
+                             void* stream);
+
+/* y[t] = sum over j in ascending order of topk_w[t,j] * rows[pos[t,j]]; 0 for a token
+ * without rows. */
+mok_status_t mok_unpermute(int32_t type, const void* rows, int64_t ld_rows, int64_t max_rows,
+                           const int32_t* pos, const float* topk_w, int64_t tokens,
+                           int32_t top_k, int32_t cols, void* y, int64_t ld_y, void* stream);
+
+/* Gradients of mok_unpermute: d_rows[pos[t,j]] = topk_w[t,j] * dy[t] and d_topk_w[t,j] =
+ * <dy[t], rows[pos[t,j]]> (0 for a pair without a row).  rows and d_rows have max_rows
+ * rows each. */
+mok_status_t mok_unpermute_bwd(int32_t type, const void* dy, int64_t ld_y, const void* rows,
+                               int64_t ld_rows, int64_t max_rows, const int32_t* pos,
+                               const float* topk_w, int64_t tokens, int32_t top_k,
+                               int32_t cols, void* d_rows, int64_t ld_d_rows,
+                               float* d_topk_w, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * MXFP4 (OCP MX: e2m1 elements, one e8m0 scale per 32): beside mok_quantize_mx, the
+ * 4-bit form of the weights and activations.
+ *
+ * Codes: two a byte, the element of even index in the low half; a row of cols elements
+ * (a multiple of 32, 32..65536) takes cols / 2 bytes, its scales cols / 32 bytes.
+ * ld_codes and ld_scales are bytes from row to row: ld_codes >= cols / 2, a multiple of
+ * 16; ld_scales >= cols / 32.  Bases of codes and of src / dst 16-byte aligned; ld_src,
+ * ld_dst in elements, multiples of 8, at least cols.  rows 0..2^31-1 (0: nothing is
+ * done).  Bytes between rows are left as they are. */
+
+/* The rule of mok_quantize_mx with e2m1's largest value: the shared exponent is the
+ * smallest n with amax * 2^-n <= 6 (clamped to [-127, 127]; an all-zero block gets -127),
+ * code = e2m1 round-to-nearest-even of v * 2^-n.  A block that holds a NaN or an infinity
+ * gets the NaN scale (255) and zero codes. */
+mok_status_t mok_quantize_mx4(int32_t type, const void* src, int64_t ld_src, int64_t rows,
+                              int32_t cols, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                              int64_t ld_scales, void* stream);
+
+/* The values back: dst = code * 2^(scale - 127) in `type` (rounded to nearest even where
+ * fp16's range needs it; NaN for the blocks of scale 255). */
+mok_status_t mok_dequantize_mx4(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
+                                int64_t ld_scales, int64_t rows, int32_t cols, int32_t type,
+                                void* dst, int64_t ld_dst, void* stream);
+
+/* Grouped product on MX operands: for every expert e of `groups` (1..1024) and every row
+ * r in [offsets[e], offsets[e+1]) of the `max_rows` (0..2^24) rows of A
+ *   out[r, c] = sum over i of A[r, i] * B[e][c, i],   c < n, i < k,
+ * accumulated in fp32 by scaled MFMA, rounded once to out_type (MOK_TYPE_BF16 or
+ * MOK_TYPE_FP32).  offsets [groups + 1] int32 stays on the device (mok_schedule's table,
+ * or {0, max_rows} for one plain product); the ranges are cut to [0, max_rows) and must
+ * not overlap; rows of no range are neither read nor written.  k a multiple of 32,
+ * 32..65536; n a multiple of 8, 8..2^20; n * k below 2^31.
+ * a_format MOK_MX_E2M1: A codes of mok_quantize_mx4; MOK_MX_E4M3: of mok_quantize_mx
+ * (k bytes a row).  ld_a (bytes, a multiple of 16) and ld_a_scales (bytes) as above, each at
+ * most MOK_MX_MAX_LD.
+ * B e2m1: codes [groups, n, k/2], scales [groups, n, k/32], contiguous.  out: ld_out
+ * elements from row to row, a multiple of 8, at least n.  A codes, B codes and out 16-byte
+ * aligned.  A NaN scale makes the results it enters NaN.  Errors as for the row
+ * operators; asynchronous on stream, one launch, no workspace, bitwise repeatable. */
+#define MOK_MX_E4M3 0
+#define MOK_MX_E2M1 1
+#define MOK_MX_MAX_LD ((int64_t)1 << 22)
+mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t ld_a,
+                             const uint8_t* a_scales, int64_t ld_a_scales, int64_t max_rows,
+                             const int32_t* offsets, int32_t groups, const uint8_t* b_codes,
+                             const uint8_t* b_scales, int32_t n, int32_t k, int32_t out_type,
+                             void* out, int64_t ld_out, void* stream);
+
 /* Synchronise `stream`, then read the sticky device status word (MOK_DEV_* bits). */
 mok_status_t mok_read_device_status(const void* ws, void* stream, uint32_t* out);
 

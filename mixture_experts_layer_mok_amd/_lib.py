@@ -30,6 +30,12 @@ MOK_FLAG_PERTURB = 0x8
 MOK_FLAG_TRACE = 0x10
 MOK_FLAG_OVERLAP_NEXT = 0x20
 MOK_TRACE_MAX_WORKGROUPS = 1024
+MOK_TYPE_BF16 = 0
+MOK_TYPE_FP16 = 1
+MOK_TYPE_FP32 = 2
+MOK_MX_E4M3 = 0
+MOK_MX_E2M1 = 1
+MOK_MX_MAX_LD = 1 << 22
 MOK_DEV_BAD_ID = 0x1
 MOK_DEV_TIMEOUT = 0x2
 
@@ -38,7 +44,8 @@ EXPORTS = (
     "mok_workspace_size", "mok_schedule", "mok_schedule_tables", "mok_quantize_mx",
     "mok_moe_fwd", "mok_moe_bwd", "mok_read_device_status", "mok_status_string",
     "mok_device_cus", "mok_trace_layout", "mok_moe_fwd_noalloc", "mok_quantize_mx_t",
-    "mok_moe_bwd_mx",
+    "mok_moe_bwd_mx", "mok_schedule_layout", "mok_permute", "mok_permute_bwd", "mok_unpermute",
+    "mok_unpermute_bwd", "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4",
 )
 
 
@@ -79,7 +86,7 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     vp, sz, i32p, u8p, f32p = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                ctypes.c_void_p, ctypes.c_void_p)
-    D = ctypes.POINTER(mok_desc_t)
+    D, i32, i64 = ctypes.POINTER(mok_desc_t), ctypes.c_int32, ctypes.c_int64
     sig = {
         "mok_workspace_size": (ctypes.c_int, [D, ctypes.POINTER(ctypes.c_size_t)]),
         "mok_schedule": (ctypes.c_int, [D, i32p, vp, sz, vp]),
@@ -100,6 +107,18 @@ def load() -> ctypes.CDLL:
                                              u8p, ctypes.c_int64, u8p, ctypes.c_int64, vp]),
         "mok_moe_bwd_mx": (ctypes.c_int, [D, vp, vp, i32p, f32p, u8p, u8p, u8p, u8p, vp, f32p,
                                           f32p, f32p, f32p, vp, sz, vp]),
+        "mok_schedule_layout": (ctypes.c_int, [D, ctypes.POINTER(ctypes.c_size_t),
+                                               ctypes.POINTER(ctypes.c_size_t)]),
+        "mok_permute": (ctypes.c_int, [i32, vp, i64, i32p, i64, i32, i32, vp, i64, i64, vp]),
+        "mok_permute_bwd": (ctypes.c_int, [i32, vp, i64, i64, i32p, i64, i32, i32, vp, i64, vp]),
+        "mok_unpermute": (ctypes.c_int, [i32, vp, i64, i64, i32p, f32p, i64, i32, i32, vp, i64,
+                                         vp]),
+        "mok_unpermute_bwd": (ctypes.c_int, [i32, vp, i64, vp, i64, i64, i32p, f32p, i64, i32, i32,
+                                             vp, i64, f32p, vp]),
+        "mok_quantize_mx4": (ctypes.c_int, [i32, vp, i64, i64, i32, u8p, i64, u8p, i64, vp]),
+        "mok_dequantize_mx4": (ctypes.c_int, [u8p, i64, u8p, i64, i64, i32, i32, vp, i64, vp]),
+        "mok_grouped_mx4": (ctypes.c_int, [i32, u8p, i64, u8p, i64, i64, i32p, i32, u8p, u8p, i32,
+                                           i32, i32, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -224,6 +243,63 @@ def mok_moe_bwd_mx(desc, dy, x, topk_ids, topk_w, wd_t, wd_t_scales, wgu_t, wgu_
         ctypes.byref(desc), _ptr(dy), _ptr(x), _ptr(topk_ids), _ptr(topk_w), _ptr(wd_t),
         _ptr(wd_t_scales), _ptr(wgu_t), _ptr(wgu_t_scales), _ptr(dx), _ptr(d_topk_w),
         _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def mok_schedule_layout(desc: mok_desc_t) -> tuple[int, int]:
+    """Byte offsets of the tables offsets [E_loc + 1] and pos [T*k] (int32) in the workspace."""
+    off, pos = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check("mok_schedule_layout", load().mok_schedule_layout(
+        ctypes.byref(desc), ctypes.byref(off), ctypes.byref(pos)))
+    return off.value, pos.value
+
+
+def mok_permute(type, x, ld_x, pos, tokens, top_k, cols, rows, ld_rows, max_rows,
+                stream=None) -> None:
+    _check("mok_permute", load().mok_permute(type, _ptr(x), ld_x, _ptr(pos), tokens, top_k, cols,
+                                             _ptr(rows), ld_rows, max_rows, _stream(stream)))
+
+
+def mok_permute_bwd(type, d_rows, ld_rows, max_rows, pos, tokens, top_k, cols, dx, ld_x,
+                    stream=None) -> None:
+    _check("mok_permute_bwd", load().mok_permute_bwd(type, _ptr(d_rows), ld_rows, max_rows,
+                                                     _ptr(pos), tokens, top_k, cols, _ptr(dx),
+                                                     ld_x, _stream(stream)))
+
+
+def mok_unpermute(type, rows, ld_rows, max_rows, pos, topk_w, tokens, top_k, cols, y, ld_y,
+                  stream=None) -> None:
+    _check("mok_unpermute", load().mok_unpermute(type, _ptr(rows), ld_rows, max_rows, _ptr(pos),
+                                                 _ptr(topk_w), tokens, top_k, cols, _ptr(y), ld_y,
+                                                 _stream(stream)))
+
+
+def mok_unpermute_bwd(type, dy, ld_y, rows, ld_rows, max_rows, pos, topk_w, tokens, top_k, cols,
+                      d_rows, ld_d_rows, d_topk_w, stream=None) -> None:
+    _check("mok_unpermute_bwd", load().mok_unpermute_bwd(
+        type, _ptr(dy), ld_y, _ptr(rows), ld_rows, max_rows, _ptr(pos), _ptr(topk_w), tokens,
+        top_k, cols, _ptr(d_rows), ld_d_rows, _ptr(d_topk_w), _stream(stream)))
+
+
+def mok_quantize_mx4(type, src, ld_src, rows, cols, codes, ld_codes, scales, ld_scales,
+                     stream=None) -> None:
+    _check("mok_quantize_mx4", load().mok_quantize_mx4(
+        type, _ptr(src), ld_src, rows, cols, _ptr(codes), ld_codes, _ptr(scales), ld_scales,
+        _stream(stream)))
+
+
+def mok_dequantize_mx4(codes, ld_codes, scales, ld_scales, rows, cols, type, dst, ld_dst,
+                       stream=None) -> None:
+    _check("mok_dequantize_mx4", load().mok_dequantize_mx4(
+        _ptr(codes), ld_codes, _ptr(scales), ld_scales, rows, cols, type, _ptr(dst), ld_dst,
+        _stream(stream)))
+
+
+def mok_grouped_mx4(a_format, a_codes, ld_a, a_scales, ld_a_scales, max_rows, offsets, groups,
+                    b_codes, b_scales, n, k, out_type, out, ld_out, stream=None) -> None:
+    _check("mok_grouped_mx4", load().mok_grouped_mx4(
+        a_format, _ptr(a_codes), ld_a, _ptr(a_scales), ld_a_scales, max_rows, _ptr(offsets),
+        groups, _ptr(b_codes), _ptr(b_scales), n, k, out_type, _ptr(out), ld_out,
+        _stream(stream)))
 
 
 def mok_read_device_status(ws, stream=None) -> int:

@@ -7,6 +7,7 @@ import numpy as np
 import torch
 
 from . import _lib as L
+from . import ops
 
 
 def bf16_tensor(bits: np.ndarray, device="cuda") -> torch.Tensor:
@@ -100,6 +101,37 @@ class MoKLayer:
         res["perm"] = res["perm"][:R]
         res["R"], res["n_mb"], res["n_mtiles"], res["status"] = (int(v) for v in res["hdr"])
         return res
+
+    def schedule_tables(self) -> tuple[torch.Tensor, torch.Tensor]:
+        """(pos [T, k], offsets [E_loc + 1]): int32 views of the schedule's tables in the
+        workspace, as the row operators and the grouped product (`ops`) read them, valid
+        until the next schedule on this workspace."""
+        d = self.desc
+        off, pos = L.mok_schedule_layout(d)
+        tables = self.ws.view(torch.int32)
+        T, k, nl = d.num_tokens, d.top_k, d.num_local_experts
+        return (tables[pos // 4:pos // 4 + T * k].view(T, k),
+                tables[off // 4:off // 4 + nl + 1])
+
+    def permute(self, x, out, stream=None):
+        """Rows of x in expert order (ops.permute with this schedule)."""
+        return ops.permute(x, self.schedule_tables()[0], out, stream=stream)
+
+    def permute_backward(self, d_rows, out=None, stream=None):
+        return ops.permute_backward(d_rows, self.schedule_tables()[0], out=out, stream=stream)
+
+    def unpermute(self, rows, gates, out=None, stream=None):
+        """Gate-weighted sums of expert-ordered rows per token (ops.unpermute)."""
+        return ops.unpermute(rows, self.schedule_tables()[0], gates, out=out, stream=stream)
+
+    def unpermute_backward(self, dy, rows, gates, d_rows, d_gates=None, stream=None):
+        return ops.unpermute_backward(dy, rows, self.schedule_tables()[0], gates, d_rows,
+                                      d_weights=d_gates, stream=stream)
+
+    def grouped_mx4(self, a, a_scales, b, b_scales, out=None, dtype=torch.bfloat16, stream=None):
+        """Expert-ordered MX rows times each expert's MXFP4 weights (ops.grouped_mx4)."""
+        return ops.grouped_mx4(a, a_scales, self.schedule_tables()[1], b, b_scales, out=out,
+                               dtype=dtype, stream=stream)
 
     def status(self, stream=None) -> int:
         return L.mok_read_device_status(self.ws, stream)

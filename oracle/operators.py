@@ -1,0 +1,114 @@
+"""Plain float64 forms of the row operators and the MXFP4 operators, for the tests: explicit
+loops over tokens, slots and blocks, sharing nothing with the HIP library."""
+from __future__ import annotations
+
+import numpy as np
+
+# magnitudes of the eight e2m1 codes without sign (1 sign, 2 exponent, 1 mantissa bit, bias 1)
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _pairs(pos, max_rows):
+    """(token, slot, row) of every pair that has a row, in (token, slot) order."""
+    for t in range(pos.shape[0]):
+        for j in range(pos.shape[1]):
+            if 0 <= pos[t, j] < max_rows:
+                yield t, j, int(pos[t, j])
+
+
+def permute(x, pos, rows):
+    """rows (float64, changed in place): row pos[t, j] becomes x[t]."""
+    for t, _, r in _pairs(pos, rows.shape[0]):
+        rows[r] = x[t]
+    return rows
+
+
+def unpermute(rows, pos, w=None):
+    """(sum over slots of w * row, sum of its magnitudes), float64 [T, D]."""
+    y = np.zeros((pos.shape[0], rows.shape[1]))
+    s = np.zeros_like(y)
+    for t, j, r in _pairs(pos, rows.shape[0]):
+        v = rows[r].astype(np.float64) * (1.0 if w is None else float(w[t, j]))
+        y[t] += v
+        s[t] += np.abs(v)
+    return y, s
+
+
+def unpermute_backward(dy, rows, pos, w, d_rows):
+    """d_rows changed in place; (d_rows, d_w, sum of the magnitudes in each d_w)."""
+    dw = np.zeros(pos.shape)
+    s = np.zeros(pos.shape)
+    for t, j, r in _pairs(pos, rows.shape[0]):
+        g = dy[t].astype(np.float64)
+        d_rows[r] = float(w[t, j]) * g
+        p = g * rows[r].astype(np.float64)
+        dw[t, j], s[t, j] = p.sum(), np.abs(p).sum()
+    return d_rows, dw, s
+
+
+def quantize_mx4(x):
+    """(codes [R, K] 0..15 one a byte, scales [R, K / 32] as e8m0 bytes) of float64 x.
+    The exponent is found by trial: the smallest n in [-127, 127] with amax <= 6 * 2^n; the
+    code by nearest distance, a tie to the even code."""
+    R, K = x.shape
+    codes = np.zeros((R, K), np.uint8)
+    scales = np.zeros((R, K // 32), np.uint8)
+    for r in range(R):
+        for b in range(K // 32):
+            v = x[r, 32 * b:32 * b + 32].astype(np.float64)
+            if not np.isfinite(v).all():
+                scales[r, b] = 255
+                continue
+            amax = np.abs(v).max()
+            n = -127
+            if amax > 0:
+                n = max(-127, int(np.floor(np.log2(amax))) - 4)
+                while amax > 6 * 2.0**n:
+                    n += 1
+            d = np.abs(np.abs(v)[:, None] * 2.0**-n - E2M1[None, :])
+            near = d.min(axis=1, keepdims=True)
+            pick = [min(np.nonzero(row == m)[0], key=lambda c: c % 2) for row, m in zip(d, near)]
+            codes[r, 32 * b:32 * b + 32] = np.array(pick, np.uint8) | (np.signbit(v) * 8).astype(np.uint8)
+            scales[r, b] = n + 127
+    return codes, scales
+
+
+def pack4(codes):
+    return (codes[..., 0::2] | (codes[..., 1::2] << 4)).astype(np.uint8)
+
+
+def unpack4(packed):
+    out = np.empty(packed.shape[:-1] + (packed.shape[-1] * 2,), np.uint8)
+    out[..., 0::2], out[..., 1::2] = packed & 15, packed >> 4
+    return out
+
+
+def _scaled(v, scales):
+    s = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return v * np.repeat(s, 32, axis=-1)
+
+
+def values_mx4(packed, scales):
+    c = unpack4(packed)
+    return _scaled(np.where(c & 8, -1.0, 1.0) * E2M1[c & 7], scales)
+
+
+def values_mx8(codes, scales):
+    """e4m3: 1 sign, 4 exponent bits of bias 7, 3 mantissa bits; code 0x7F is NaN."""
+    c = codes.astype(np.int64)
+    e, m = (c >> 3) & 15, (c & 7) / 8.0
+    v = np.where(e == 0, m * 2.0**-6, (1 + m) * 2.0 ** (e - 7.0))
+    v = np.where((c & 127) == 127, np.nan, v)
+    return _scaled(np.where(c & 128, -v, v), scales)
+
+
+def grouped(a, offsets, b, out):
+    """out (float64, changed in place) and the sums of the products' magnitudes: out[r] =
+    b[e] @ a[r] for the rows of every expert, the ranges cut to a's rows."""
+    s = np.zeros_like(out)
+    for e in range(len(offsets) - 1):
+        lo, hi = max(int(offsets[e]), 0), min(int(offsets[e + 1]), a.shape[0])
+        if hi > lo:
+            out[lo:hi] = a[lo:hi] @ b[e].T
+            s[lo:hi] = np.abs(a[lo:hi]) @ np.abs(b[e]).T
+    return out, s

@@ -1,0 +1,333 @@
+"""Row operators on the GPU against their float64 forms.
+
+Tolerances, from the arithmetic: a sum of m products in fp32 (each product and each addition
+rounded, relative 2^-24) is within (m + 1) 2^-24 S of the exact one, S the sum of the
+magnitudes; storing it in a type rounds by at most half a step, u = eps / 2 of the value (and
+2^-25 absolutely for fp16's subnormals).  A dot product over D columns sums at most D / 64 + 96
+terms in one chain (a lane's own, then the lanes', then the waves')."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_mok_amd import _lib as L
+from mixture_experts_layer_mok_amd import gen, ops
+from mixture_experts_layer_mok_amd.layer import MoKLayer
+from oracle import operators as O
+from tests.gpu_util import say
+from tests.test_operators import _routing
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E24 = 2.0**-24
+TINY = {torch.bfloat16: 2.0**-133, torch.float16: 2.0**-25, torch.float32: 2.0**-149}
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+IDS = ["bf16", "fp16", "fp32"]
+
+
+def unit(t):
+    return torch.finfo(t).eps / 2
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def randn(rng, *shape, dtype):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(DEV, dtype)
+
+
+def close(got, want, s, terms, dtype, what):
+    e = (terms + 1) * E24 * s
+    bound = e + unit(dtype) * (np.abs(want) + e) + TINY[dtype]
+    bad = ~(np.abs(f64(got) - want) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size}, worst {np.abs(f64(got) - want).max()}"
+
+
+def run_all(T, k, E, D, dtype, seed, masked=0.2, slack=5, pad=0, pos=None, R=None):
+    """All four operators on one routing, against float64; returns the device outputs."""
+    if pos is None:
+        pos, R = _routing(T, k, E, seed, masked)
+    rng = np.random.default_rng(seed + 1)
+    n = R + slack
+
+    def matrix(rows):
+        return randn(rng, rows, D + pad, dtype=dtype)[:, :D]
+
+    p = torch.from_numpy(pos).to(DEV)
+    x, rows, dy = matrix(T), matrix(n), matrix(T)
+    w = torch.softmax(randn(rng, T, k, dtype=torch.float32), 1)
+    w[p < 0] = float("nan")  # the weight of a pair without a row is not read
+    used = np.zeros(n, bool)
+    for _, _, r in O._pairs(pos, n):
+        used[r] = True
+    rows[torch.from_numpy(~used).to(DEV)] = float("nan")  # nor is a row without a pair
+    full = torch.full((n, D + pad), -7.0, dtype=dtype, device=DEV)
+    out = full[:, :D]
+    ops.permute(x, p, out)
+    want = O.permute(f64(x), pos, np.full((n, D), -7.0))
+    np.testing.assert_array_equal(f64(out), want)
+    assert (full[:, D:] == -7).all()
+    dx = ops.permute_backward(rows, p)
+    rows0 = np.nan_to_num(f64(rows))
+    want, s = O.unpermute(rows0, pos)
+    close(dx, want, s, k, dtype, "permute_backward")
+    y = ops.unpermute(rows, p, w)
+    wn = np.nan_to_num(f64(w))
+    want, s = O.unpermute(rows0, pos, wn)
+    close(y, want, s, k, dtype, "unpermute")
+    d_rows = torch.full((n, D + pad), -7.0, dtype=dtype, device=DEV)
+    d_rows, dw = ops.unpermute_backward(dy, rows, p, w, d_rows[:, :D])
+    want, want_w, s = O.unpermute_backward(f64(dy), rows0, pos, wn, np.full((n, D), -7.0))
+    close(d_rows, want, np.abs(want), 1, dtype, "d_rows")
+    assert (d_rows[torch.from_numpy(~used).to(DEV)] == -7).all()
+    e = (D / 64 + 96) * E24 * s
+    assert (np.abs(f64(dw) - want_w) <= e + E24 * np.abs(want_w)).all(), "d_weights"
+    return out, dx, y, d_rows, dw
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,k,E,D", [(1, 1, 1, 8), (1, 8, 8, 7168), (3, 2, 5, 72), (64, 8, 64, 1000),
+                                     (5, 64, 64, 520), (2, 3, 4, 65536), (130, 4, 6, 2056)])
+def test_small(T, k, E, D, dtype):
+    say(f"[rows] T={T} k={k} E={E} D={D} {dtype}")
+    run_all(T, k, E, D, dtype, seed=T + k)
+
+
+# both sides of the tokens at which fewer waves share a token
+@pytest.mark.parametrize("T", [511, 512, 2047, 2048, 2053])
+@pytest.mark.parametrize("D", [64, 8200])
+def test_many_tokens(T, D):
+    say(f"[rows] T={T} D={D}")
+    run_all(T, 2, 7, D if T < 600 or D == 64 else 1032, torch.bfloat16, seed=T)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_row_strides(dtype):
+    say(f"[rows] strides {dtype}")
+    run_all(37, 3, 6, 136, dtype, seed=9, pad=24)
+
+
+def test_repeated_input_row():
+    """A gradient that is one row for every token (an expanded tensor)."""
+    pos, R = _routing(9, 2, 4, 3)
+    p = torch.from_numpy(pos).to(DEV)
+    rng = np.random.default_rng(4)
+    rows, w = randn(rng, R, 64, dtype=torch.float32), torch.rand(9, 2, device=DEV)
+    one = randn(rng, 1, 64, dtype=torch.float32)
+    a = ops.unpermute_backward(one.expand(9, 64), rows, p, w, torch.zeros(R, 64, device=DEV))
+    b = ops.unpermute_backward(one.repeat(9, 1), rows, p, w, torch.zeros(R, 64, device=DEV))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    out = ops.permute(one.expand(9, 64), p, torch.zeros(R, 64, device=DEV))
+    assert torch.equal(out, one.expand(R, 64))
+
+
+def test_nothing_routed_and_rows_out_of_range():
+    say("[rows] no pair has a row")
+    T, k, D = 7, 3, 64
+    none = np.full((T, k), -1, np.int32)
+    out, dx, y, d_rows, dw = run_all(T, k, 4, D, torch.bfloat16, 1, pos=none, R=0)
+    assert not dx.any() and not y.any() and not dw.any()
+    # rows outside [0, max_rows): skipped, whatever they are
+    say("[rows] rows out of range")
+    pos, R = _routing(T, k, 4, 2, masked=0)
+    bad = pos.copy()
+    bad[0, 0], bad[1, 1], bad[2, 2] = -2**31, 2**31 - 1, R
+    bad[bad == R - 1] = -5
+    run_all(T, k, 4, D, torch.float32, 1, pos=bad, R=R - 1, slack=0)
+    # no rows at all
+    p = torch.from_numpy(pos).to(DEV)
+    x = torch.ones(T, D, device=DEV)
+    empty = torch.empty(0, D, device=DEV)
+    ops.permute(x, p, empty)
+    assert not ops.permute_backward(empty, p).any()
+    w = torch.ones(T, k, device=DEV)
+    assert not ops.unpermute(empty, p, w).any()
+    assert not ops.unpermute_backward(x, empty, p, w, torch.empty(0, D, device=DEV))[1].any()
+    # no tokens
+    e = torch.empty(0, D, device=DEV)
+    p0, w0 = torch.empty(0, k, dtype=torch.int32, device=DEV), torch.empty(0, k, device=DEV)
+    rows = torch.full((3, D), 2.0, device=DEV)
+    ops.permute(e, p0, rows)
+    assert ops.permute_backward(rows, p0).shape == (0, D)
+    assert ops.unpermute(rows, p0, w0).shape == (0, D)
+    ops.unpermute_backward(e, rows, p0, w0, rows.clone())
+    assert (rows == 2).all()
+
+
+def test_infinities_and_nan_go_where_they_belong():
+    pos = torch.tensor([[0, 1], [2, -1], [-1, -1]], dtype=torch.int32, device=DEV)
+    rows = torch.ones(3, 64, device=DEV)
+    rows[1, 5], rows[2, 7] = float("inf"), float("nan")
+    y = ops.unpermute(rows, pos, torch.full((3, 2), 0.5, device=DEV))
+    want = torch.tensor([[1.0], [0.5], [0.0]], device=DEV).repeat(1, 64)
+    want[0, 5], want[1, 7] = float("inf"), float("nan")
+    assert torch.equal(torch.nan_to_num(y, nan=9.0, posinf=8.0),
+                       torch.nan_to_num(want, nan=9.0, posinf=8.0))
+
+
+def test_offsets_past_32_bits():
+    """Rows whose bytes lie past 2^32: 16,500 rows of 65536 fp32 values (4.3 GB)."""
+    say("[rows] offsets past 32 bits")
+    n, D = 16500, 65536
+    rows = torch.empty(n, D, device=DEV)
+    pos = torch.tensor([[n - 1, 3], [n - 2, -1]], dtype=torch.int32, device=DEV)
+    x = torch.randn(2, D, device=DEV)
+    ops.permute(x, pos, rows)
+    assert torch.equal(rows[n - 1], x[0]) and torch.equal(rows[3], x[0])
+    assert torch.equal(rows[n - 2], x[1])
+    dx = ops.permute_backward(rows, pos)
+    assert torch.equal(dx, torch.stack([x[0] + x[0], x[1]]))
+    w = torch.tensor([[0.5, 0.25], [2.0, 0.0]], device=DEV)
+    y = ops.unpermute(rows, pos, w)
+    assert torch.equal(y, torch.stack([x[0] * 0.75, x[1] * 2.0]))
+    ones = torch.ones(2, D, device=DEV)
+    d = torch.empty(n, D, device=DEV)
+    d, dw = ops.unpermute_backward(ones, rows, pos, w, d)
+    assert (d[n - 1] == 0.5).all() and (d[3] == 0.25).all() and (d[n - 2] == 2).all()
+    s = x.double().abs().sum(1)
+    want = x.double().sum(1)
+    assert (abs(dw[0].double() - want[0]) <= (D / 64 + 96) * E24 * s[0]).all()
+    assert dw[1, 1] == 0
+
+
+def _layer(cfg, **kw):
+    return MoKLayer(L.desc_from_config(cfg, **kw))
+
+
+def test_with_the_schedule():
+    """The layer's tables drive the operators: permute gives the rows in expert order, and
+    permute -> experts -> unpermute with its backward equals the float64 chain."""
+    cfg = gen.small_config("rows", T=300, D=192, I=64, E=6, k=2, M=96, e0=1, E_loc=4)
+    d = gen.make_inputs(cfg, with_dy=True)
+    d["ids"] = gen.mask_ids(d["ids"], 0.2, seed=5)
+    layer = _layer(cfg)
+    layer.schedule(torch.from_numpy(d["ids"]).to(DEV))
+    t = layer.tables()
+    pos, offsets = layer.schedule_tables()
+    np.testing.assert_array_equal(pos.cpu().numpy().reshape(-1), t["pos"])
+    np.testing.assert_array_equal(offsets.cpu().numpy(), t["offsets"])
+    R = t["R"]
+    x = torch.from_numpy(d["x"]).to(DEV)
+    g = torch.from_numpy(d["gates"]).to(DEV)
+    dy = torch.from_numpy(d["dy"]).to(DEV)
+    rows = layer.permute(x, torch.zeros(cfg.T * cfg.k, cfg.D, device=DEV))
+    np.testing.assert_array_equal(rows[:R].cpu().numpy(), d["x"][t["perm"] // cfg.k])
+    assert not rows[R:].any()
+    # one matrix an expert, in float32 by torch
+    rng = np.random.default_rng(8)
+    W = rng.standard_normal((cfg.n_local, cfg.D, cfg.D)) / 16
+    off = t["offsets"]
+    h64 = np.zeros((R, cfg.D))
+    for e in range(cfg.n_local):
+        h64[off[e]:off[e + 1]] = f64(rows)[off[e]:off[e + 1]] @ W[e]
+    h = torch.zeros_like(rows)
+    h[:R] = torch.from_numpy(h64).to(DEV, torch.float32)
+    y = layer.unpermute(h, g)
+    P = t["pos"].reshape(cfg.T, cfg.k)
+    want, s = O.unpermute(f64(h), P, d["gates"])
+    close(y, want, s, cfg.k, torch.float32, "unpermute")
+    d_h, dg = layer.unpermute_backward(dy, h, g, torch.zeros_like(h))
+    want_h, want_g, sg = O.unpermute_backward(d["dy"], f64(h), P, d["gates"], np.zeros(h.shape))
+    close(d_h, want_h, np.abs(want_h), 1, torch.float32, "d_rows")
+    assert (np.abs(f64(dg) - want_g) <= (cfg.D / 64 + 96) * E24 * sg).all()
+    d_rows = torch.zeros_like(h)
+    for e in range(cfg.n_local):
+        lo, hi = off[e], off[e + 1]
+        d_rows[lo:hi] = torch.from_numpy(f64(d_h)[lo:hi] @ W[e].T).to(DEV, torch.float32)
+    dx = layer.permute_backward(d_rows)
+    want, s = O.unpermute(f64(d_rows), P)
+    close(dx, want, s, cfg.k, torch.float32, "permute_backward")
+    assert layer.status() == 0
+
+
+def test_gradients_against_differences():
+    """<g, unpermute(f * permute(x), w)> changes as the gradients say: central differences
+    of the GPU's own forward in fp32.  It is bilinear, so the difference over a step h has
+    only rounding: each of the two sums of T D values is within 2 (k + 2) 2^-24 S of exact
+    (products of three factors summed over k; the outer sum is taken in float64)."""
+    T, k, D, h = 6, 2, 64, 0.5
+    pos, R = _routing(T, k, 4, 11)
+    p = torch.from_numpy(pos).to(DEV)
+    rng = np.random.default_rng(12)
+    x, dy, f = (randn(rng, n, D, dtype=torch.float32) for n in (T, T, R))
+    w = torch.rand(T, k, device=DEV)
+
+    def forward(x, w):
+        rows = f * ops.permute(x, p, torch.zeros(R, D, device=DEV))
+        return rows, ops.unpermute(rows, p, w)
+
+    def loss(x, w):
+        return float((forward(x, w)[1].double() * dy.double()).sum())
+
+    rows, y = forward(x, w)
+    d_rows, dw = ops.unpermute_backward(dy, rows, p, w, torch.zeros(R, D, device=DEV))
+    dx = ops.permute_backward(f * d_rows, p)
+    big = f64(torch.maximum(x.abs(), torch.tensor(1.0)) + h).max()
+    s = float((np.abs(f64(dy)).sum() * f64(f.abs()).max() * big * (f64(w).max() + h) * k))
+    tol = 2 * 2 * (k + 2) * E24 * s / (2 * h) + 1e-6
+    for v, g, places in ((x, dx, [(0, 0), (3, 17), (5, 63)]), (w, dw, list(np.ndindex(T, k)))):
+        for i in places:
+            keep = v[i].item()
+            v[i] = keep + h
+            up = loss(x, w)
+            v[i] = keep - h
+            down = loss(x, w)
+            v[i] = keep
+            assert abs((up - down) / (2 * h) - g[i].item()) <= tol
+
+
+def test_repeatable_streams_and_graph():
+    """The same bits again, on another stream, and from a replayed graph with new inputs."""
+    T, k, D = 600, 3, 264
+    pos, R = _routing(T, k, 8, 21)
+    pos2, R2 = _routing(T, k, 8, 22, masked=0.5)
+    n = max(R, R2)
+    rng = np.random.default_rng(23)
+
+    def inputs(pos):
+        return [torch.from_numpy(pos).to(DEV), randn(rng, T, D, dtype=torch.bfloat16),
+                randn(rng, n, D, dtype=torch.bfloat16), randn(rng, T, D, dtype=torch.bfloat16),
+                torch.rand(T, k, device=DEV)]
+
+    def step(v, outs, stream=None):
+        p, x, rows, dy, w = v
+        ops.permute(x, p, outs[0], stream=stream)
+        ops.permute_backward(rows, p, out=outs[1], stream=stream)
+        ops.unpermute(rows, p, w, out=outs[2], stream=stream)
+        ops.unpermute_backward(dy, rows, p, w, outs[3], d_weights=outs[4], stream=stream)
+
+    def outputs():
+        z = dict(dtype=torch.bfloat16, device=DEV)
+        return [torch.zeros(n, D, **z), torch.zeros(T, D, **z), torch.zeros(T, D, **z),
+                torch.zeros(n, D, **z), torch.zeros(T, k, device=DEV)]
+
+    a, b = inputs(pos), inputs(pos2)
+    ref_a, ref_b = outputs(), outputs()
+    step(a, ref_a)
+    step(b, ref_b)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = outputs()
+    torch.cuda.synchronize()
+    step(a, got, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, r) for g, r in zip(got, ref_a))
+    held = [t.clone() for t in a]
+    got = outputs()
+    step(held, got)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(held, got)
+    for src, ref in ((b, ref_b), (a, ref_a), (b, ref_b)):
+        for t, s in zip(held, src):
+            t.copy_(s)
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        again = outputs()
+        step(src, again)  # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, r) for g, r in zip(got, ref))
+        assert all(torch.equal(g, r) for g, r in zip(again, ref))
