@@ -10,9 +10,11 @@
 // has, in lane l, column l % 16 and rows 4 (l / 16) .. +4.  Weights are the first operand, so
 // a lane ends with four consecutive columns of one row of out.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "launch.h"
+#include "gemm_mx4.h"
 
 namespace mok {
 
@@ -110,9 +112,84 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
   }
 }
 
+// Tile m of the m-tiles of all experts (each expert's rows cut from its first row on into
+// tiles of TM): its expert, first row and rows.  False when there are no more than m.  Every
+// wave scans the experts, 64 at a time.
+template <int TM>
+__device__ __forceinline__ bool find_tile(const GroupedArgs& p, int m, int* e, int64_t* r0, int* rows,
+                                          int* total) {
+  const int lane = threadIdx.x & 63;
+  int before = 0, found = -1;
+  int64_t flo = 0, fhi = 0;
+  int fbefore = 0;
+  for (int e0 = 0; e0 < p.groups; e0 += 64) {
+    int64_t lo = 0, hi = 0;
+    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &lo, &hi);
+    const int tiles = hi > lo ? int((hi - lo + TM - 1) / TM) : 0;
+    int incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(incl, d);
+      if (lane >= d) incl += u;
+    }
+    const uint64_t at = __ballot(before + incl > m);
+    if (found < 0 && at) {
+      const int s = __ffsll((unsigned long long)at) - 1;
+      found = e0 + s;
+      flo = int64_t(uint32_t(__builtin_amdgcn_readlane(int(lo), s)));
+      fhi = int64_t(uint32_t(__builtin_amdgcn_readlane(int(hi), s)));
+      fbefore = before + __builtin_amdgcn_readlane(incl - tiles, s);
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  *total = before;
+  if (found < 0) return false;
+  *e = found;
+  *r0 = flo + int64_t(m - fbefore) * TM;
+  *rows = int(min(fhi - *r0, int64_t(TM)));
+  return true;
+}
+
+template <bool A8, bool OUT32, int SG>
+__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int nt) {
+  constexpr int TM = mx4::tile_rows<A8>();
+  const int m = blockIdx.x / nt, n = blockIdx.x - m * nt;
+  int e, rows, total;
+  int64_t r0;
+  if (!find_tile<TM>(p, m, &e, &r0, &rows, &total)) return;
+  mx4::Tile<A8, SG> t;
+  t.init(p, e, r0, rows, n * mx4::kTN);
+  t.run();
+  t.template store<OUT32>(p, r0, rows, n * mx4::kTN);
+}
+
 }  // namespace
 
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
+  if (a.max_rows / a.groups >= 64) {
+    const int tm = a.a8 ? mx4::tile_rows<true>() : mx4::tile_rows<false>();
+    const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
+    // at most this many m-tiles: every expert may end inside one
+    const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
+    const dim3 grid(unsigned(mt * nt)), block(mx4::kThr);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, nt); };
+    auto sg = [&](auto g) {
+      constexpr int SG = decltype(g)::value;
+      if (a.a8) {
+        if (a.out32) go(k_grouped_tile<true, true, SG>);
+        else go(k_grouped_tile<true, false, SG>);
+      } else {
+        if (a.out32) go(k_grouped_tile<false, true, SG>);
+        else go(k_grouped_tile<false, false, SG>);
+      }
+    };
+    const int64_t align = int64_t(reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) |
+                                  uintptr_t(a.ld_as) | uintptr_t(a.k / 32));
+    if (align % 16 == 0) sg(std::integral_constant<int, 16>());
+    else if (align % 4 == 0) sg(std::integral_constant<int, 4>());
+    else sg(std::integral_constant<int, 1>());
+    return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
+  }
   const dim3 grid(unsigned((a.n + 15) / 16), unsigned(a.groups)), block(256);
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a); };
   if (a.a8) {
