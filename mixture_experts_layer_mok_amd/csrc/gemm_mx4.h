@@ -16,9 +16,9 @@
 // the four blocks 4 h .. 4 h + 3 over the step's four slices, whose scales are one dword of
 // the row, its byte s selected by the instruction.
 //
-// Scales: eight steps' worth (64 bytes a row, so no cache line is fetched for a few
-// bytes) go through registers into LDS at a time, as [dword of the window][row], which
-// the lanes of a fragment read without bank conflicts.
+// Scales: a ring of eight steps (64 bytes a row) in LDS, refilled four steps at a time once
+// every wave has read the four (32 bytes a row, so that a cache line is not fetched for a
+// few bytes each step), by direct-to-LDS loads too where their alignment allows it.
 //
 // LDS data rows: 128 bytes hold 8 chunks of 16, chunk c of row r at c ^ (r & 7) ^ ((r >> 3)
 // & 1); 256 bytes hold 16, at c ^ (r & 15): the 16 rows that one pass of a 16-byte read
@@ -36,8 +36,13 @@ namespace mx4 {
 constexpr int kThr = 256;
 constexpr int kTN = 256;
 constexpr int kStep = 256;                // K elements a step
-constexpr int kWin = 8;                   // steps a scale window
+constexpr int kRing = 8;                  // steps of scales in LDS
 constexpr uint32_t kStageB = 32768;       // bytes of one operand's stage
+#ifndef KD1
+#define KD1 8
+#define KD2 8
+#endif
+constexpr int kD1 = KD1, kD2 = KD2;       // data loads issued under slices 1 and 2 (the rest: 3)
 constexpr uint32_t kPastRange = 0x80000000u;
 
 template <bool A8>
@@ -45,8 +50,11 @@ constexpr int tile_rows() { return A8 ? 128 : 256; }
 
 static __shared__ __align__(1024) v4u g_a[2 * kStageB / 16];
 static __shared__ __align__(1024) v4u g_b[2 * kStageB / 16];
-static __shared__ uint32_t g_sa[2 * kWin * 256];  // [dword of the window][row]
-static __shared__ uint32_t g_sb[2 * kWin * 256];
+// Scales: two dwords a row and step.  With 16-byte loads piece q (of the ring's four, two
+// steps each) of row r lies at 16-byte place q * rows + r; otherwise dword d (of sixteen) of
+// row r at dword place d * rows + r.
+static __shared__ __align__(1024) uint32_t g_sa[2 * kRing * 256];
+static __shared__ __align__(1024) uint32_t g_sb[2 * kRing * 256];
 
 typedef __attribute__((address_space(3))) const v4u lds_v4u;
 typedef __attribute__((address_space(3))) v4u lds_wv4u;
@@ -58,29 +66,25 @@ __device__ __forceinline__ i32x4_t rsrc_2g(const void* base) {
   return r;
 }
 
-// Sixteen scale bytes at byte `off` of r, of which `have` exist (a multiple of SG, or all);
-// the others are zeros.  SG: bytes a load, 16 where every row's scales are whole 16-byte
-// pieces, 4 where they are whole dwords, 1 otherwise.
-template <int SG>
-__device__ __forceinline__ v4u load_scales16(rsrc_t r, uint32_t off, int have) {
-  if (SG == 16) return buf_ld16<kCpolPlain>(r, have >= 16 ? off : kPastRange);
-  uint32_t w[4];
+// Four scale bytes at byte `off` of r, of which `have` exist; the others are zeros.
+__device__ __forceinline__ uint32_t scale_bytes4(rsrc_t r, uint32_t off, int have) {
+  uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (SG == 4) {
-      w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, have > 4 * i ? off + 4 * i : kPastRange, 0, 0);
-    } else {
-      w[i] = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        w[i] |= uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(
-                    r, have > 4 * i + c ? off + 4 * i + c : kPastRange, 0, 0)))
-                << (8 * c);
-    }
-  }
-  return v4u{w[0], w[1], w[2], w[3]};
+  for (int c = 0; c < 4; ++c)
+    w |= uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(r, have > c ? off + c : kPastRange, 0, 0)))
+         << (8 * c);
+  return w;
 }
 
+// Direct-to-LDS load of one dword a lane (see dma16_at).
+__device__ __forceinline__ void dma4_at(const i32x4_t& rsrc, uint32_t voff, uint32_t lds_wave_addr) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
+  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "s"(m0)
+               : "memory", "m0");
+}
+
+// SG: bytes a scale load moves: 16 where every row's scales are whole 16-byte pieces at
+// 16-byte addresses, 4 where they are whole dwords, 1 otherwise (through registers).
 template <bool A8, int SG>
 struct Tile {
   static constexpr int kTM = tile_rows<A8>();
@@ -91,10 +95,9 @@ struct Tile {
   uint32_t oa[8], ob[8];     // byte offsets of this lane's chunks in step 0
   uint32_t la[4];            // LDS byte address of the A fragment of slice s, block 0, stage 0
   uint32_t lb[4];            // the same of B
-  rsrc_t rsa, rsb;           // scales of A from the tile's first row, of the expert's B
+  const uint8_t *psa, *psb;  // scales of A from the tile's first row, of the expert's B
   uint32_t osa, osb;         // this thread's scale rows (past the range: none)
   int nblk, steps, ca, cb;   // K blocks, steps; this lane's chunk of an A and of a B row
-  v4u wa[4], wb[4];          // the next window's scales of this thread's rows
   f32x16_t acc[kIB][kJB];
 
   __device__ __forceinline__ void init(const GroupedArgs& p, int e, int64_t r0, int rows, int n0) {
@@ -121,8 +124,8 @@ struct Tile {
                                   : uint32_t(wm * 128 + r) * 128 + (((4 * h + s) ^ sw) * 16));
       lb[s] = lds_addr(g_b) + uint32_t(wn * 128 + r) * 128 + (((4 * h + s) ^ sw) * 16);
     }
-    rsa = row_rsrc(p.as + r0 * p.ld_as, kPastRange);
-    rsb = row_rsrc(p.bs + int64_t(e) * p.n * nblk, kPastRange);
+    psa = p.as + r0 * p.ld_as;
+    psb = p.bs + int64_t(e) * p.n * nblk;
     osa = t < kTM ? uint32_t(min(t, rows - 1) * p.ld_as) : kPastRange;
     osb = uint32_t(min(n0 + t, p.n - 1)) * uint32_t(nblk);
 #pragma unroll
@@ -148,23 +151,40 @@ struct Tile {
     }
   }
 
-  __device__ __forceinline__ void load_window(int win) {
+  // Scales of steps 4 quad .. 4 quad + 3 (32 bytes a row) into their half of the ring; each
+  // wave moves those of 64 rows of A and of B.
+  __device__ __forceinline__ void issue_scales(int quad) {
+    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int at = quad * 32, half = quad & 1;
+    const i32x4_t rsa = rsrc_2g(psa), rsb = rsrc_2g(psb);
+    if (SG == 16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = win * 64 + 16 * i, have = nblk - at;
-      wa[i] = load_scales16<SG>(rsa, osa + at, have);
-      wb[i] = load_scales16<SG>(rsb, osb + at, have);
-    }
-  }
-  __device__ __forceinline__ void store_window() {
-    const int t = threadIdx.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (!A8 || t < kTM) g_sa[(4 * i + c) * kTM + t] = wa[i][c];
-        g_sb[(4 * i + c) * 256 + t] = wb[i][c];
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t past = at + 16 * i < nblk ? 0u : kPastRange;
+        if (w * 64 < kTM)
+          dma16_at<false>(rsa, (osa + at + 16 * i) | past, 0,
+                          lds_addr(g_sa) + uint32_t((half * 2 + i) * kTM + w * 64) * 16);
+        dma16_at<false>(rsb, (osb + at + 16 * i) | past, 0,
+                        lds_addr(g_sb) + uint32_t((half * 2 + i) * 256 + w * 64) * 16);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int have = nblk - at - 4 * i;
+        if (SG == 4) {
+          const uint32_t past = have > 0 ? 0u : kPastRange;
+          if (w * 64 < kTM)
+            dma4_at(rsa, (osa + at + 4 * i) | past,
+                    lds_addr(g_sa) + uint32_t((half * 8 + i) * kTM + w * 64) * 4);
+          dma4_at(rsb, (osb + at + 4 * i) | past,
+                  lds_addr(g_sb) + uint32_t((half * 8 + i) * 256 + w * 64) * 4);
+        } else {
+          if (w * 64 < kTM)
+            g_sa[(half * 8 + i) * kTM + t] = scale_bytes4(row_rsrc(psa, kPastRange), osa + at + 4 * i, have);
+          g_sb[(half * 8 + i) * 256 + t] = scale_bytes4(row_rsrc(psb, kPastRange), osb + at + 4 * i, have);
+        }
+      }
+    }
   }
 
   struct Scales {
@@ -173,15 +193,18 @@ struct Tile {
   __device__ __forceinline__ void read_scales(Scales& s, int ks) const {
     const int t = threadIdx.x, l = t & 63, w = t >> 6;
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
-    const int d = 2 * (ks & (kWin - 1)) + h;
+    const int d = 2 * (ks & (kRing - 1)) + h;  // dword of the ring
+    const int ra_ = wm * (kTM / 2) + r, rb_ = wn * 128 + r;
 #pragma unroll
-    for (int i = 0; i < kIB; ++i) s.a[i] = g_sa[d * kTM + wm * (kTM / 2) + 32 * i + r];
+    for (int i = 0; i < kIB; ++i)
+      s.a[i] = SG == 16 ? g_sa[((d >> 2) * kTM + ra_ + 32 * i) * 4 + (d & 3)] : g_sa[d * kTM + ra_ + 32 * i];
 #pragma unroll
-    for (int j = 0; j < kJB; ++j) s.b[j] = g_sb[d * 256 + wn * 128 + 32 * j + r];
+    for (int j = 0; j < kJB; ++j)
+      s.b[j] = SG == 16 ? g_sb[((d >> 2) * 256 + rb_ + 32 * j) * 4 + (d & 3)] : g_sb[d * 256 + rb_ + 32 * j];
   }
 
-  __device__ __forceinline__ i32x8_t read_a(int s, int i) const {
-    const uint32_t o = uint32_t(i) * 32 * (A8 ? 256 : 128);
+  __device__ __forceinline__ i32x8_t read_a(int s, int i, uint32_t stage) const {
+    const uint32_t o = uint32_t(i) * 32 * (A8 ? 256 : 128) + stage;
     const v4u x = *reinterpret_cast<lds_v4u*>(uintptr_t(la[s] + o));
     if (A8) {
       const v4u y = *reinterpret_cast<lds_v4u*>(uintptr_t((la[s] ^ 128u) + o));
@@ -189,98 +212,82 @@ struct Tile {
     }
     return i32x8_t{int(x.x), int(x.y), int(x.z), int(x.w), 0, 0, 0, 0};
   }
-  __device__ __forceinline__ i32x8_t read_b(int s, int j) const {
-    const v4u x = *reinterpret_cast<lds_v4u*>(uintptr_t(lb[s] + uint32_t(j) * 32 * 128));
+  __device__ __forceinline__ i32x8_t read_b(int s, int j, uint32_t stage) const {
+    const v4u x = *reinterpret_cast<lds_v4u*>(uintptr_t(lb[s] + stage + uint32_t(j) * 32 * 128));
     return i32x8_t{int(x.x), int(x.y), int(x.z), int(x.w), 0, 0, 0, 0};
   }
 
-  template <int SL>
-  __device__ __forceinline__ void mma_row(const i32x8_t& a, const i32x8_t (&b)[kJB], uint32_t sa_,
-                                          const uint32_t (&sb_)[kJB], f32x16_t (&c)[kJB]) {
-#pragma unroll
-    for (int j = 0; j < kJB; ++j)
-      c[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b[j], a, c[j], 4, A8 ? 0 : 4, SL,
-                                                             int(sb_[j]), SL, int(sa_));
-  }
+  struct Frag {
+    i32x8_t a[kIB], b[kJB];
+  };
 
-  // One slice: its MFMAs, with the next slice's fragments (slice NSL, at la, lb) read under
-  // them: B into bn, each A block in place once its row of MFMAs has issued.  With DMA, the
-  // loads of step ks + 2 into the current stage are issued between the rows too.
-  template <int SL, int NSL, bool DMA>
-  __device__ __forceinline__ void slice(i32x8_t (&a)[kIB], i32x8_t (&b)[kJB], const Scales& sc, int ks,
-                                        uint32_t stage) {
-    i32x8_t bn[kJB];
+  // One slice's MFMAs on f, and between them: the fragments of slice RS (of the stage that la,
+  // lb plus rd point at) read into fr, and data loads D0 .. D0 + DN - 1 of step ks + 2 issued
+  // into stage `wr`.
+  template <int SL, int RS, int D0, int DN>
+  __device__ __forceinline__ void slice(const Frag& f, Frag& fr, const Scales& sc, uint32_t rd, int ks,
+                                        uint32_t wr) {
+    constexpr int kM = kIB * kJB;  // MFMAs
+    constexpr int kR = kIB + kJB;  // fragment reads, one or two after each of the first MFMAs
+    constexpr int kPer = (kR + kM / 2 - 1) / (kM / 2);
 #pragma unroll
-    for (int i = 0; i < kIB; ++i) {
+    for (int m = 0; m < kM; ++m) {
+      const int i = m / kJB, j = m % kJB;
       __builtin_amdgcn_sched_barrier(0);
-      constexpr int kRB = 2;  // rows over which the B reads are spread
-      if (i < kRB) {
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          f.b[j], f.a[i], acc[i][j], 4, A8 ? 0 : 4, SL, int(sc.b[j]), SL, int(sc.a[i]));
 #pragma unroll
-        for (int j = 0; j < kJB / kRB; ++j) bn[i * (kJB / kRB) + j] = read_b(NSL, i * (kJB / kRB) + j);
+      for (int x = 0; x < kPer; ++x) {
+        const int r = m * kPer + x;
+        if (r < kIB) fr.a[r] = read_a(RS, r, rd);
+        else if (r < kR) fr.b[r - kIB] = read_b(RS, r - kIB, rd);
       }
-      mma_row<SL>(a[i], b, sc.a[i], sc.b, acc[i]);
-      if (DMA) {
 #pragma unroll
-        for (int q = 0; q < 16 / kIB; ++q) issue(ks + 2, i * (16 / kIB) + q, stage);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      a[i] = read_a(NSL, i);
+      for (int q = 0; q < DN; ++q)
+        if (q * kM / (DN > 0 ? DN : 1) == m) issue(ks + 2, D0 + q, wr);
     }
-#pragma unroll
-    for (int j = 0; j < kJB; ++j) b[j] = bn[j];
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   __device__ __forceinline__ void run() {
     asm volatile("" ::: "memory");
-    load_window(0);
+    issue_scales(0);
+    issue_scales(1);
 #pragma unroll
     for (int q = 0; q < 16; ++q) issue(0, q, 0);
 #pragma unroll
     for (int q = 0; q < 16; ++q) issue(1, q, kStageB);
-    store_window();
     wait_loads_and_lds();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    i32x8_t a[kIB], b[kJB];
-    Scales sc;
+    // f[s]: the fragments of slice s.  Those of slices 0..2 are read one step ahead, those of
+    // slice 3 under slice 0 of their own step.
+    Frag f[4];
+    Scales sc, sn;
     read_scales(sc, 0);
 #pragma unroll
-    for (int i = 0; i < kIB; ++i) a[i] = read_a(0, i);
+    for (int s = 0; s < 3; ++s) {
 #pragma unroll
-    for (int j = 0; j < kJB; ++j) b[j] = read_b(0, j);
-    // Step ks: on entry a, b hold its slice 0 and sc its scales.
-    uint32_t stage = 0;
+      for (int i = 0; i < kIB; ++i) f[s].a[i] = read_a(s, i, 0);
+#pragma unroll
+      for (int j = 0; j < kJB; ++j) f[s].b[j] = read_b(s, j, 0);
+    }
+    uint32_t cur = 0;  // stage of step ks
     for (int ks = 0; ks < steps; ++ks) {
-      slice<0, 1, false>(a, b, sc, ks, stage);
-      slice<1, 2, false>(a, b, sc, ks, stage);
-      slice<2, 3, false>(a, b, sc, ks, stage);
-      __builtin_amdgcn_sched_barrier(0);
+      slice<0, 3, 0, 0>(f[0], f[3], sc, cur, ks, cur);
       // step ks + 1 has landed (mine by the wait, everyone's by the barrier), and every wave
-      // has read the last of this stage and the scales of step ks
+      // has read the last of this step's stage and its scales
       wait_loads_and_lds();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      const int nx = ks + 1;
-      if ((nx & (kWin - 1)) == 0) {  // the next step opens a scale window
-        store_window();
-        wait_loads_and_lds();
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-      }
-      if ((nx & (kWin - 1)) == kWin / 2) load_window(nx / kWin + 1);
-      const uint32_t turn = stage ? 0u - kStageB : kStageB;
-      la[0] += turn;
-      lb[0] += turn;
-      Scales sn;
-      read_scales(sn, nx);
-      slice<3, 0, true>(a, b, sc, ks, stage);
+      const uint32_t nxt = cur ^ kStageB;
+      if ((ks & 3) == 3) issue_scales(ks / 4 + 2);  // into the half of the ring just read
+      read_scales(sn, ks + 1);
+      slice<1, 0, 0, kD1>(f[1], f[0], sc, nxt, ks, cur);
+      slice<2, 1, kD1, kD2>(f[2], f[1], sc, nxt, ks, cur);
+      slice<3, 2, kD1 + kD2, 16 - kD1 - kD2>(f[3], f[2], sc, nxt, ks, cur);
       sc = sn;
-#pragma unroll
-      for (int s = 1; s < 4; ++s) {
-        la[s] += turn;
-        lb[s] += turn;
-      }
-      stage ^= kStageB;
+      cur = nxt;
     }
     // every load has landed and every wave has read its last fragments: the stages are free
     wait_loads_and_lds();
