@@ -27,6 +27,11 @@
 // Rows past the expert's last are read as its last one (never stored); weight rows past N
 // as the last one; chunks past K as zeros (an out-of-range offset reads no memory), with
 // zero scales.
+// Tiles of few rows (the end of an expert's rows, or all of them) run with fewer row blocks
+// a wave: IB = 1 covers 64 rows, 2 covers 128, 4 covers 256.
+//
+// A workgroup walks several tiles: the next one's first loads are in flight while the current
+// one's results are stored, straight from the registers.
 #pragma once
 #include "gemm_bf16.h"
 
@@ -38,11 +43,6 @@ constexpr int kTN = 256;
 constexpr int kStep = 256;                // K elements a step
 constexpr int kRing = 8;                  // steps of scales in LDS
 constexpr uint32_t kStageB = 32768;       // bytes of one operand's stage
-#ifndef KD1
-#define KD1 8
-#define KD2 8
-#endif
-constexpr int kD1 = KD1, kD2 = KD2;       // data loads issued under slices 1 and 2 (the rest: 3)
 constexpr uint32_t kPastRange = 0x80000000u;
 
 template <bool A8>
@@ -60,10 +60,21 @@ typedef __attribute__((address_space(3))) const v4u lds_v4u;
 typedef __attribute__((address_space(3))) v4u lds_wv4u;
 typedef __attribute__((address_space(3))) uint64_t lds_wu64;
 
+// A wave-uniform value into a scalar register, whatever the compiler holds it in: the loads
+// below are inline asm, which cannot take a resource from vector registers.  (The builtin is
+// dropped where its operand is known to be uniform, also when that lies in a vector register.)
+// The compiler does not see into the asm, so it has the wait states that gfx950 asks for:
+// one between a vector write and the lane read of its result, five between a scalar result
+// of a vector instruction and a vector memory operation that reads it.
+__device__ __forceinline__ int scalar(int v) {
+  int s;
+  asm volatile("s_nop 0\n\tv_readfirstlane_b32 %0, %1\n\ts_nop 4" : "=s"(s) : "v"(v));
+  return s;
+}
 __device__ __forceinline__ i32x4_t rsrc_2g(const void* base) {
-  i32x4_t r = make_rsrc(base);
-  r.z = int(kPastRange);
-  return r;
+  const uint64_t x = reinterpret_cast<uint64_t>(base);
+  return i32x4_t{scalar(int(uint32_t(x))), scalar(int(uint32_t(x >> 32) & 0xFFFFu)), int(kPastRange),
+                 0x00020000};
 }
 
 // Four scale bytes at byte `off` of r, of which `have` exist; the others are zeros.
@@ -76,39 +87,48 @@ __device__ __forceinline__ uint32_t scale_bytes4(rsrc_t r, uint32_t off, int hav
   return w;
 }
 
-// Direct-to-LDS load of one dword a lane (see dma16_at).
-__device__ __forceinline__ void dma4_at(const i32x4_t& rsrc, uint32_t voff, uint32_t lds_wave_addr) {
+// Direct-to-LDS loads of 16 or 4 bytes a lane: lane l's land at lds_wave_addr + 16 (4) l.  One
+// wait state lies between the write of M0 and the load that reads it.
+__device__ __forceinline__ void lds_load16(const i32x4_t& rsrc, uint32_t voff, uint32_t soff,
+                                           uint32_t lds_wave_addr) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
-  asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff), "s"(rsrc), "s"(m0)
+  soff = __builtin_amdgcn_readfirstlane(soff);
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
+               "s"(rsrc), "s"(soff), "s"(m0)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void lds_load4(const i32x4_t& rsrc, uint32_t voff, uint32_t lds_wave_addr) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff),
+               "s"(rsrc), "s"(m0)
                : "memory", "m0");
 }
 
 // SG: bytes a scale load moves: 16 where every row's scales are whole 16-byte pieces at
 // 16-byte addresses, 4 where they are whole dwords, 1 otherwise (through registers).
+//
+// Where a tile's operands come from, and its direct-to-LDS loads.
 template <bool A8, int SG>
-struct Tile {
+struct Source {
   static constexpr int kTM = tile_rows<A8>();
-  static constexpr int kIB = A8 ? 2 : 4;  // 32-row blocks of A a wave
-  static constexpr int kJB = 4;           // 32-row blocks of B a wave
-
-  i32x4_t ra, rb;
+  i32x4_t ra, rb;            // codes of A from the tile's first row, of the expert's B
+  i32x4_t rsa, rsb;          // their scales
   uint32_t oa[8], ob[8];     // byte offsets of this lane's chunks in step 0
-  uint32_t la[4];            // LDS byte address of the A fragment of slice s, block 0, stage 0
-  uint32_t lb[4];            // the same of B
-  const uint8_t *psa, *psb;  // scales of A from the tile's first row, of the expert's B
-  uint32_t osa, osb;         // this thread's scale rows (past the range: none)
-  int nblk, steps, ca, cb;   // K blocks, steps; this lane's chunk of an A and of a B row
-  f32x16_t acc[kIB][kJB];
+  const uint8_t *psa, *psb;  // the scales' addresses (SG 1)
+  uint32_t osa, osb;         // this thread's scale rows
+  int nblk;                  // K blocks
+  int ca, cb;                // this lane's chunk of an A and of a B row
+  int qa;                    // A loads a step (those of rows that a block covers)
 
   __device__ __forceinline__ void init(const GroupedArgs& p, int e, int64_t r0, int rows, int n0) {
     const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int kb = p.k / 2;
     nblk = p.k / 32;
-    steps = (p.k + kStep - 1) / kStep;
     ra = rsrc_2g(p.a + r0 * p.ld_a);
     rb = rsrc_2g(p.b + int64_t(e) * p.n * kb);
     ca = A8 ? ((l & 15) ^ (((w & 3) * 4 + (l >> 4)) & 15)) : ((l & 7) ^ (l >> 3) ^ (w & 1));
     cb = (l & 7) ^ (l >> 3) ^ (w & 1);
+    qa = rows <= 64 ? (A8 ? 4 : 2) : rows <= 128 ? (A8 ? 8 : 4) : 8;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int ar = A8 ? (q * 4 + w) * 4 + (l >> 4) : (q * 4 + w) * 8 + (l >> 3);
@@ -116,55 +136,42 @@ struct Tile {
       oa[q] = uint32_t(int64_t(min(ar, rows - 1)) * p.ld_a) + ca * 16;
       ob[q] = uint32_t(min(n0 + br, p.n - 1)) * uint32_t(kb) + cb * 16;
     }
-    const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
-    const int sw = (r & 7) ^ ((r >> 3) & 1);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      la[s] = lds_addr(g_a) + (A8 ? uint32_t(wm * 64 + r) * 256 + (((2 * s + h) ^ (r & 15)) * 16)
-                                  : uint32_t(wm * 128 + r) * 128 + (((4 * h + s) ^ sw) * 16));
-      lb[s] = lds_addr(g_b) + uint32_t(wn * 128 + r) * 128 + (((4 * h + s) ^ sw) * 16);
-    }
     psa = p.as + r0 * p.ld_as;
     psb = p.bs + int64_t(e) * p.n * nblk;
+    rsa = rsrc_2g(psa);
+    rsb = rsrc_2g(psb);
     osa = t < kTM ? uint32_t(min(t, rows - 1) * p.ld_as) : kPastRange;
     osb = uint32_t(min(n0 + t, p.n - 1)) * uint32_t(nblk);
-#pragma unroll
-    for (int i = 0; i < kIB; ++i)
-#pragma unroll
-      for (int j = 0; j < kJB; ++j)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
   }
 
-  // Direct-to-LDS load q (0..7 A, 8..15 B) of step ks into the stage at byte `stage` of the
-  // rings.  A step past the last reads nothing.
-  __device__ __forceinline__ void issue(int ks, int q, uint32_t stage) {
+  // Load q (0..7 A, 8..15 B) of step ks into the stage at byte `stage` of the rings.  A step
+  // past the last reads nothing.
+  __device__ __forceinline__ void issue(int ks, int q, uint32_t stage) const {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (q < 8) {
       const uint32_t past = (A8 ? 16 * ks + ca < 2 * nblk : 8 * ks + ca < nblk) ? 0u : kPastRange;
-      dma16_at<false>(ra, oa[q] | past, uint32_t(ks) * (A8 ? 256 : 128),
+      lds_load16(ra, oa[q] | past, uint32_t(ks) * (A8 ? 256 : 128),
                       lds_addr(g_a) + stage + (q * 4 + w) * 1024);
     } else {
       const uint32_t past = 8 * ks + cb < nblk ? 0u : kPastRange;
-      dma16_at<false>(rb, ob[q - 8] | past, uint32_t(ks) * 128,
+      lds_load16(rb, ob[q - 8] | past, uint32_t(ks) * 128,
                       lds_addr(g_b) + stage + ((q - 8) * 4 + w) * 1024);
     }
   }
 
   // Scales of steps 4 quad .. 4 quad + 3 (32 bytes a row) into their half of the ring; each
   // wave moves those of 64 rows of A and of B.
-  __device__ __forceinline__ void issue_scales(int quad) {
+  __device__ __forceinline__ void issue_scales(int quad) const {
     const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int at = quad * 32, half = quad & 1;
-    const i32x4_t rsa = rsrc_2g(psa), rsb = rsrc_2g(psb);
     if (SG == 16) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t past = at + 16 * i < nblk ? 0u : kPastRange;
         if (w * 64 < kTM)
-          dma16_at<false>(rsa, (osa + at + 16 * i) | past, 0,
+          lds_load16(rsa, (osa + at + 16 * i) | past, 0,
                           lds_addr(g_sa) + uint32_t((half * 2 + i) * kTM + w * 64) * 16);
-        dma16_at<false>(rsb, (osb + at + 16 * i) | past, 0,
+        lds_load16(rsb, (osb + at + 16 * i) | past, 0,
                         lds_addr(g_sb) + uint32_t((half * 2 + i) * 256 + w * 64) * 16);
       }
     } else {
@@ -174,9 +181,9 @@ struct Tile {
         if (SG == 4) {
           const uint32_t past = have > 0 ? 0u : kPastRange;
           if (w * 64 < kTM)
-            dma4_at(rsa, (osa + at + 4 * i) | past,
+            lds_load4(rsa, (osa + at + 4 * i) | past,
                     lds_addr(g_sa) + uint32_t((half * 8 + i) * kTM + w * 64) * 4);
-          dma4_at(rsb, (osb + at + 4 * i) | past,
+          lds_load4(rsb, (osb + at + 4 * i) | past,
                   lds_addr(g_sb) + uint32_t((half * 8 + i) * 256 + w * 64) * 4);
         } else {
           if (w * 64 < kTM)
@@ -187,16 +194,83 @@ struct Tile {
     }
   }
 
+  // The same with what is wave-uniform in scalar registers again (values that were chosen on
+  // several paths may have lost them).
+  __device__ __forceinline__ Source uniform() const {
+    Source s = *this;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s.ra[i] = scalar(ra[i]);
+      s.rb[i] = scalar(rb[i]);
+      s.rsa[i] = scalar(rsa[i]);
+      s.rsb[i] = scalar(rsb[i]);
+    }
+    s.ra.z = s.rb.z = s.rsa.z = s.rsb.z = int(kPastRange);
+    s.ra.w = s.rb.w = s.rsa.w = s.rsb.w = 0x00020000;
+    s.nblk = scalar(nblk);
+    return s;
+  }
+
+  // The first two steps and the scales of the first eight.
+  __device__ __forceinline__ void begin() const {
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) issue(ks, q, ks * kStageB);
+    issue_scales(0);
+    issue_scales(1);
+  }
+};
+
+// Columns 8 c .. 8 c + 7 of one row, this lane's: of two neighbouring groups of eight, lanes 0..31
+// hold the first and lanes 32..63 the second.  lo, hi: two bf16 pairs of each group as the
+// accumulators have them (lane r: columns 0..3 of row r, lane 32 + r: columns 4..7).
+__device__ __forceinline__ v4u join_halves(uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {
+  const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+  const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+  return v4u{uint32_t(s0[0]), uint32_t(s1[0]), uint32_t(s0[1]), uint32_t(s1[1])};
+}
+
+template <bool A8, int SG, int IB>
+struct Tile {
+  typedef Source<A8, SG> Src;
+  static constexpr int kTM = tile_rows<A8>();
+  static constexpr int kJB = 4;  // 32-row blocks of B a wave; IB: of A
+  static constexpr int kQA = A8 ? 4 * IB : 2 * IB;  // A loads a step
+
+  uint32_t la[4];  // LDS byte address of the A fragment of slice s, block 0, stage 0
+  uint32_t lb[4];  // the same of B
+  f32x16_t acc[IB][kJB];
+
+  __device__ __forceinline__ void init() {
+    const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
+    const int sw = (r & 7) ^ ((r >> 3) & 1);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      la[s] = lds_addr(g_a) + (A8 ? uint32_t(wm * 32 * IB + r) * 256 + (((2 * s + h) ^ (r & 15)) * 16)
+                                  : uint32_t(wm * 32 * IB + r) * 128 + (((4 * h + s) ^ sw) * 16));
+      lb[s] = lds_addr(g_b) + uint32_t(wn * 128 + r) * 128 + (((4 * h + s) ^ sw) * 16);
+    }
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+      for (int j = 0; j < kJB; ++j)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
+  }
+
   struct Scales {
-    uint32_t a[kIB], b[kJB];
+    uint32_t a[IB], b[kJB];
   };
   __device__ __forceinline__ void read_scales(Scales& s, int ks) const {
     const int t = threadIdx.x, l = t & 63, w = t >> 6;
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
     const int d = 2 * (ks & (kRing - 1)) + h;  // dword of the ring
-    const int ra_ = wm * (kTM / 2) + r, rb_ = wn * 128 + r;
+    const int ra_ = wm * 32 * IB + r, rb_ = wn * 128 + r;
 #pragma unroll
-    for (int i = 0; i < kIB; ++i)
+    for (int i = 0; i < IB; ++i)
       s.a[i] = SG == 16 ? g_sa[((d >> 2) * kTM + ra_ + 32 * i) * 4 + (d & 3)] : g_sa[d * kTM + ra_ + 32 * i];
 #pragma unroll
     for (int j = 0; j < kJB; ++j)
@@ -218,18 +292,17 @@ struct Tile {
   }
 
   struct Frag {
-    i32x8_t a[kIB], b[kJB];
+    i32x8_t a[IB], b[kJB];
   };
 
-  // One slice's MFMAs on f, and between them: the fragments of slice RS (of the stage that la,
-  // lb plus rd point at) read into fr, and data loads D0 .. D0 + DN - 1 of step ks + 2 issued
-  // into stage `wr`.
+  // One slice's MFMAs on f, and between them: the fragments of slice RS (of the stage at rd)
+  // read into fr, and the data loads D0 .. D0 + DN - 1 of step ks + 2 issued into stage `wr`.
   template <int SL, int RS, int D0, int DN>
-  __device__ __forceinline__ void slice(const Frag& f, Frag& fr, const Scales& sc, uint32_t rd, int ks,
-                                        uint32_t wr) {
-    constexpr int kM = kIB * kJB;  // MFMAs
-    constexpr int kR = kIB + kJB;  // fragment reads, one or two after each of the first MFMAs
-    constexpr int kPer = (kR + kM / 2 - 1) / (kM / 2);
+  __device__ __forceinline__ void slice(const Src& src, const Frag& f, Frag& fr, const Scales& sc,
+                                        uint32_t rd, int ks, uint32_t wr) {
+    constexpr int kM = IB * kJB;  // MFMAs
+    constexpr int kR = IB + kJB;  // fragment reads, after each of the first MFMAs
+    constexpr int kPer = IB == 1 ? 2 : 1;
 #pragma unroll
     for (int m = 0; m < kM; ++m) {
       const int i = m / kJB, j = m % kJB;
@@ -237,55 +310,59 @@ struct Tile {
       acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
           f.b[j], f.a[i], acc[i][j], 4, A8 ? 0 : 4, SL, int(sc.b[j]), SL, int(sc.a[i]));
 #pragma unroll
-      for (int x = 0; x < kPer; ++x) {
-        const int r = m * kPer + x;
-        if (r < kIB) fr.a[r] = read_a(RS, r, rd);
-        else if (r < kR) fr.b[r - kIB] = read_b(RS, r - kIB, rd);
+      for (int x = 0; x < kPer; ++x) read_one(fr, RS, m * kPer + x, rd);
+      if (m == kM - 1) {
+#pragma unroll
+        for (int r = kM * kPer; r < kR; ++r) read_one(fr, RS, r, rd);
       }
 #pragma unroll
       for (int q = 0; q < DN; ++q)
-        if (q * kM / (DN > 0 ? DN : 1) == m) issue(ks + 2, D0 + q, wr);
+        if (q * kM / (DN > 0 ? DN : 1) == m) {
+          const int d = D0 + q;
+          src.issue(ks + 2, d < kQA ? d : d - kQA + 8, wr);
+        }
     }
     __builtin_amdgcn_sched_barrier(0);
   }
+  __device__ __forceinline__ void read_one(Frag& fr, int s, int r, uint32_t rd) const {
+    if (r < IB) fr.a[r] = read_a(s, r, rd);
+    else if (r < IB + kJB) fr.b[r - IB] = read_b(s, r - IB, rd);
+  }
 
-  __device__ __forceinline__ void run() {
-    asm volatile("" ::: "memory");
-    issue_scales(0);
-    issue_scales(1);
-#pragma unroll
-    for (int q = 0; q < 16; ++q) issue(0, q, 0);
-#pragma unroll
-    for (int q = 0; q < 16; ++q) issue(1, q, kStageB);
+  // The K loop; src.begin() has been issued.
+  __device__ __forceinline__ void run(const Src& opened) {
+    const Src src = opened.uniform();
+    init();
     wait_loads_and_lds();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     // f[s]: the fragments of slice s.  Those of slices 0..2 are read one step ahead, those of
-    // slice 3 under slice 0 of their own step.
+    // slice 3 under slice 0 of their own step: a stage is free from then on, and the loads of
+    // two steps ahead have the rest of the step to be issued in.
     Frag f[4];
     Scales sc, sn;
     read_scales(sc, 0);
 #pragma unroll
-    for (int s = 0; s < 3; ++s) {
+    for (int s = 0; s < 3; ++s)
 #pragma unroll
-      for (int i = 0; i < kIB; ++i) f[s].a[i] = read_a(s, i, 0);
-#pragma unroll
-      for (int j = 0; j < kJB; ++j) f[s].b[j] = read_b(s, j, 0);
-    }
+      for (int r = 0; r < IB + kJB; ++r) read_one(f[s], s, r, 0);
+    const int steps = (src.nblk + 7) / 8;
     uint32_t cur = 0;  // stage of step ks
+    constexpr int kD = kQA + 8;  // data loads a step
+    constexpr int kD1 = kD / 2, kD2 = kD - kD1;
     for (int ks = 0; ks < steps; ++ks) {
-      slice<0, 3, 0, 0>(f[0], f[3], sc, cur, ks, cur);
+      slice<0, 3, 0, 0>(src, f[0], f[3], sc, cur, ks, cur);
       // step ks + 1 has landed (mine by the wait, everyone's by the barrier), and every wave
       // has read the last of this step's stage and its scales
       wait_loads_and_lds();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       const uint32_t nxt = cur ^ kStageB;
-      if ((ks & 3) == 3) issue_scales(ks / 4 + 2);  // into the half of the ring just read
+      if ((ks & 3) == 3) src.issue_scales(ks / 4 + 2);  // into the half of the ring just read
       read_scales(sn, ks + 1);
-      slice<1, 0, 0, kD1>(f[1], f[0], sc, nxt, ks, cur);
-      slice<2, 1, kD1, kD2>(f[2], f[1], sc, nxt, ks, cur);
-      slice<3, 2, kD1 + kD2, 16 - kD1 - kD2>(f[3], f[2], sc, nxt, ks, cur);
+      slice<1, 0, 0, kD1>(src, f[1], f[0], sc, nxt, ks, cur);
+      slice<2, 1, kD1, kD2>(src, f[2], f[1], sc, nxt, ks, cur);
+      slice<3, 2, 0, 0>(src, f[3], f[2], sc, nxt, ks, cur);
       sc = sn;
       cur = nxt;
     }
@@ -296,51 +373,45 @@ struct Tile {
   }
 
   // Block (i, j): lane l holds row l % 32 of A and, of B's 32 rows, 8 q + 4 h + u (q, u =
-  // 0..3): four consecutive columns of out each.
+  // 0..3): four consecutive columns of out each.  fp32: 16 bytes a lane, two lanes to 32 bytes
+  // of a row; bf16: the two lanes of a row trade halves (v_permlane32_swap) so that each
+  // stores 16 bytes, again 32 of a row.
   template <bool OUT32>
-  __device__ __forceinline__ void store(const GroupedArgs& p, int64_t r0, int rows, int n0) {
+  __device__ __forceinline__ void store(const GroupedArgs& p, int64_t r0, int rows, int n0) const {
     const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
-    const int row0 = wm * (kTM / 2), col0 = n0 + wn * 128;
-    if (OUT32) {
-      float* o = static_cast<float*>(p.out);
+    const int col0 = n0 + wn * 128;
 #pragma unroll
-      for (int i = 0; i < kIB; ++i) {
-        const int row = row0 + 32 * i + r;
-        float* orow = o + (r0 + row) * p.ld_out;
+    for (int i = 0; i < IB; ++i) {
+      const int row = (wm * IB + i) * 32 + r;
+      const int64_t at = (r0 + row) * p.ld_out;
 #pragma unroll
-        for (int j = 0; j < kJB; ++j)
+      for (int j = 0; j < kJB; ++j) {
+        if (OUT32) {
+          float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int col = col0 + 32 * j + 8 * q + 4 * h;
             if (row < rows && col < p.n)
-              *reinterpret_cast<f32x4_t*>(orow + col) =
+              *reinterpret_cast<f32x4_t*>(o + col) =
                   f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           }
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + at;
+          uint32_t d[4][2];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            d[q][0] = pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
+            d[q][1] = pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            const v4u v = join_halves(d[q][0], d[q][1], d[q + 1][0], d[q + 1][1]);
+            const int col = col0 + 32 * j + 8 * (q + h);
+            if (row < rows && col < p.n) *reinterpret_cast<v4u*>(o + col) = v;
+          }
+        }
       }
-      return;
-    }
-    // bf16: the wave's rows of 128 columns (256 bytes, 16-byte chunk c of row r at c ^ (r &
-    // 15)) through its own 32 KB of the stages, then whole row segments, 16 bytes a lane
-    const uint32_t base = (w & 2 ? lds_addr(g_b) : lds_addr(g_a)) + uint32_t(w & 1) * kStageB;
-#pragma unroll
-    for (int i = 0; i < kIB; ++i) {
-      const uint32_t at = base + uint32_t(32 * i + r) * 256 + 8 * h;
-#pragma unroll
-      for (int j = 0; j < kJB; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<lds_wu64*>(uintptr_t(at + (((4 * j + q) ^ (r & 15)) * 16))) =
-              uint64_t(pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1])) |
-              (uint64_t(pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])) << 32);
-    }
-    uint16_t* o = static_cast<uint16_t*>(p.out);
-#pragma unroll 4
-    for (int it = 0; it < kTM / 8; ++it) {
-      const int lr = it * 4 + (l >> 4), row = row0 + lr;
-      const int col = col0 + (((l & 15) ^ (lr & 15)) * 8);
-      const v4u v = *reinterpret_cast<lds_v4u*>(uintptr_t(base + uint32_t(lr) * 256 + (l & 15) * 16));
-      if (row < rows && col < p.n) *reinterpret_cast<v4u*>(o + (r0 + row) * p.ld_out + col) = v;
     }
   }
 };

@@ -112,55 +112,100 @@ __global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
   }
 }
 
-// Tile m of the m-tiles of all experts (each expert's rows cut from its first row on into
-// tiles of TM): its expert, first row and rows.  False when there are no more than m.  Every
-// wave scans the experts, 64 at a time.
+// The m-tiles of all experts (each expert's rows cut from its first row on into tiles of
+// TM), numbered in expert order.  Every wave scans the experts, 64 at a time; with at most 64
+// of them they are read once.
 template <int TM>
-__device__ __forceinline__ bool find_tile(const GroupedArgs& p, int m, int* e, int64_t* r0, int* rows,
-                                          int* total) {
-  const int lane = threadIdx.x & 63;
-  int before = 0, found = -1;
-  int64_t flo = 0, fhi = 0;
-  int fbefore = 0;
-  for (int e0 = 0; e0 < p.groups; e0 += 64) {
-    int64_t lo = 0, hi = 0;
-    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &lo, &hi);
-    const int tiles = hi > lo ? int((hi - lo + TM - 1) / TM) : 0;
-    int incl = tiles;
+struct Tiling {
+  int lo, hi, incl;  // this lane's expert of the current 64: rows, m-tiles up to it
+  int total;         // m-tiles of all experts
+  int tiles;         // this lane's expert's
+
+  __device__ __forceinline__ void scan(const GroupedArgs& p, int e0) {
+    const int lane = threadIdx.x & 63;
+    int64_t l = 0, h = 0;
+    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &l, &h);
+    lo = int(l);
+    hi = int(h);
+    tiles = hi > lo ? (hi - lo + TM - 1) / TM : 0;
+    incl = tiles;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int u = __shfl_up(incl, d);
       if (lane >= d) incl += u;
     }
-    const uint64_t at = __ballot(before + incl > m);
-    if (found < 0 && at) {
-      const int s = __ffsll((unsigned long long)at) - 1;
-      found = e0 + s;
-      flo = int64_t(uint32_t(__builtin_amdgcn_readlane(int(lo), s)));
-      fhi = int64_t(uint32_t(__builtin_amdgcn_readlane(int(hi), s)));
-      fbefore = before + __builtin_amdgcn_readlane(incl - tiles, s);
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
   }
-  *total = before;
-  if (found < 0) return false;
-  *e = found;
-  *r0 = flo + int64_t(m - fbefore) * TM;
-  *rows = int(min(fhi - *r0, int64_t(TM)));
-  return true;
+  __device__ __forceinline__ void init(const GroupedArgs& p) {
+    total = 0;
+    for (int e0 = 0; e0 < p.groups; e0 += 64) {
+      scan(p, e0);
+      total += __builtin_amdgcn_readlane(incl, 63);
+    }
+  }
+  // m-tile m < total: its expert, first row and rows
+  __device__ __forceinline__ void find(const GroupedArgs& p, int m, int* e, int64_t* r0, int* rows) {
+    int e0 = 0;
+    if (p.groups > 64) {
+      for (;; e0 += 64) {
+        scan(p, e0);
+        const int n = __builtin_amdgcn_readlane(incl, 63);
+        if (m < n) break;
+        m -= n;
+      }
+    }
+    const int s = __ffsll((unsigned long long)__ballot(incl > m)) - 1;
+    *e = e0 + s;
+    const int first = __builtin_amdgcn_readlane(lo, s) +
+                      (m - __builtin_amdgcn_readlane(incl - tiles, s)) * TM;
+    *r0 = first;
+    *rows = min(__builtin_amdgcn_readlane(hi, s) - first, TM);
+  }
+};
+
+// Tile t of mt x nt: groups of kGroupM m-tiles, inside them all m-tiles of an n-tile before the next,
+// so that the tiles that run at the same time share both operands' rows.
+constexpr int kGroupM = 4;
+__device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
+  const int g = t / (kGroupM * nt), r = t - g * kGroupM * nt;
+  const int gm = min(kGroupM, mt - g * kGroupM);
+  *n = r / gm;
+  *m = g * kGroupM + r - *n * gm;
 }
 
+// A workgroup's next tile: workgroups go to the eight XCDs in turn, and XCD x takes the x-th
+// eighth of the tiles, whose operands its L2 then holds; its workgroups take them in turn.
 template <bool A8, bool OUT32, int SG>
 __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int nt) {
   constexpr int TM = mx4::tile_rows<A8>();
-  const int m = blockIdx.x / nt, n = blockIdx.x - m * nt;
-  int e, rows, total;
+  Tiling<TM> til;
+  til.init(p);
+  const int total = til.total * nt, per = (total + 7) / 8;
+  const int first = int(blockIdx.x & 7) * per, end = min(first + per, total);
+  int t = first + int(blockIdx.x >> 3);
+  if (t >= end) return;
+  mx4::Source<A8, SG> src;
+  int m, n, e, rows;
   int64_t r0;
-  if (!find_tile<TM>(p, m, &e, &r0, &rows, &total)) return;
-  mx4::Tile<A8, SG> t;
-  t.init(p, e, r0, rows, n * mx4::kTN);
-  t.run();
-  t.template store<OUT32>(p, r0, rows, n * mx4::kTN);
+  auto open = [&]() __attribute__((always_inline)) {
+    tile_of(t, til.total, nt, &m, &n);
+    til.find(p, m, &e, &r0, &rows);
+    src.init(p, e, r0, rows, n * mx4::kTN);
+    src.begin();
+  };
+  open();
+  auto run = [&](auto tile) __attribute__((always_inline)) {
+    tile.run(src);
+    const int64_t r = r0;
+    const int have = rows, n0 = n * mx4::kTN;
+    t += int(gridDim.x >> 3);
+    if (t < end) open();
+    tile.template store<OUT32>(p, r, have, n0);
+  };
+  while (t < end) {
+    if (rows <= 64) run(mx4::Tile<A8, SG, 1>());
+    else if (A8 || rows <= 128) run(mx4::Tile<A8, SG, 2>());
+    else run(mx4::Tile<A8, SG, A8 ? 2 : 4>());
+  }
 }
 
 }  // namespace
@@ -171,7 +216,7 @@ mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
     const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
     // at most this many m-tiles: every expert may end inside one
     const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
-    const dim3 grid(unsigned(mt * nt)), block(mx4::kThr);
+    const dim3 grid(unsigned(std::min<int64_t>((mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
     auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, nt); };
     auto sg = [&](auto g) {
       constexpr int SG = decltype(g)::value;
