@@ -211,17 +211,37 @@ struct Source {
     return s;
   }
 
-  // The first two steps and the scales of the first eight.
+  // The scales of the first eight steps, then the data of step 0, then of step 1: kAhead loads
+  // a wave may be in flight when step 0 has landed.
+  static constexpr int kAhead = 16;
   __device__ __forceinline__ void begin() const {
     asm volatile("" ::: "memory");
+    issue_scales(0);
+    issue_scales(1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
       for (int q = 0; q < 16; ++q) issue(ks, q, ks * kStageB);
-    issue_scales(0);
-    issue_scales(1);
+    asm volatile("" ::: "memory");
   }
 };
+
+// The wave's LDS operations have completed (lgkmcnt 0; gfx9 encoding).
+__device__ __forceinline__ void wait_lds() {
+  __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));
+}
+
+// At most n (wave-uniform, one of the counts of stores a tile makes) of the wave's memory
+// operations still in flight: those it issued before its last n have completed.
+__device__ __forceinline__ void wait_all_but(int n) {
+  if (n >= 63) wait_vmcnt<63>();
+  else if (n >= 48) wait_vmcnt<48>();
+  else if (n >= 32) wait_vmcnt<32>();
+  else if (n >= 24) wait_vmcnt<24>();
+  else if (n >= 16) wait_vmcnt<16>();
+  else if (n >= 8) wait_vmcnt<8>();
+  else wait_vmcnt<0>();
+}
 
 // Columns 8 c .. 8 c + 7 of one row, this lane's: of two neighbouring groups of eight, lanes 0..31
 // hold the first and lanes 32..63 the second.  lo, hi: two bf16 pairs of each group as the
@@ -329,11 +349,12 @@ struct Tile {
     else if (r < IB + kJB) fr.b[r - IB] = read_b(s, r - IB, rd);
   }
 
-  // The K loop; src.begin() has been issued.
-  __device__ __forceinline__ void run(const Src& opened) {
+  // The K loop; src.begin() has been issued, and after it `stores` stores of the wave.
+  __device__ __forceinline__ void run(const Src& opened, int stores) {
     const Src src = opened.uniform();
     init();
-    wait_loads_and_lds();
+    wait_all_but(Src::kAhead + stores);  // step 0 and its scales
+    wait_lds();                           // scales written through registers (SG 1)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     // f[s]: the fragments of slice s.  Those of slices 0..2 are read one step ahead, those of
@@ -354,7 +375,9 @@ struct Tile {
       slice<0, 3, 0, 0>(src, f[0], f[3], sc, cur, ks, cur);
       // step ks + 1 has landed (mine by the wait, everyone's by the barrier), and every wave
       // has read the last of this step's stage and its scales
-      wait_loads_and_lds();
+      if (ks == 0) wait_all_but(stores);
+      else wait_vmcnt<0>();
+      wait_lds();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       const uint32_t nxt = cur ^ kStageB;
@@ -376,28 +399,34 @@ struct Tile {
   // 0..3): four consecutive columns of out each.  fp32: 16 bytes a lane, two lanes to 32 bytes
   // of a row; bf16: the two lanes of a row trade halves (v_permlane32_swap) so that each
   // stores 16 bytes, again 32 of a row.
+  // The stores go through a buffer resource whose range drops what lies outside the expert's
+  // rows and N, so that every wave makes the same number of them: kStores.
+  template <bool OUT32>
+  static constexpr int kStores = IB * kJB * (OUT32 ? 4 : 2);
+
   template <bool OUT32>
   __device__ __forceinline__ void store(const GroupedArgs& p, int64_t r0, int rows, int n0) const {
     const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
+    constexpr int kSize = OUT32 ? 4 : 2;
     const int col0 = n0 + wn * 128;
+    const rsrc_t ro = row_rsrc(static_cast<uint8_t*>(p.out) + r0 * p.ld_out * kSize, kPastRange);
 #pragma unroll
     for (int i = 0; i < IB; ++i) {
       const int row = (wm * IB + i) * 32 + r;
-      const int64_t at = (r0 + row) * p.ld_out;
+      const uint32_t at = row < rows ? uint32_t(row) * uint32_t(p.ld_out) * kSize : kPastRange;
 #pragma unroll
       for (int j = 0; j < kJB; ++j) {
         if (OUT32) {
-          float* o = static_cast<float*>(p.out) + at;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int col = col0 + 32 * j + 8 * q + 4 * h;
-            if (row < rows && col < p.n)
-              *reinterpret_cast<f32x4_t*>(o + col) =
-                  f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            buf_st16<kCpolPlain>(ro, col < p.n ? at + col * 4 : kPastRange,
+                                 __builtin_bit_cast(v4u, f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                                 acc[i][j][4 * q + 2],
+                                                                 acc[i][j][4 * q + 3]}));
           }
         } else {
-          uint16_t* o = static_cast<uint16_t*>(p.out) + at;
           uint32_t d[4][2];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -406,13 +435,14 @@ struct Tile {
           }
 #pragma unroll
           for (int q = 0; q < 4; q += 2) {
-            const v4u v = join_halves(d[q][0], d[q][1], d[q + 1][0], d[q + 1][1]);
             const int col = col0 + 32 * j + 8 * (q + h);
-            if (row < rows && col < p.n) *reinterpret_cast<v4u*>(o + col) = v;
+            buf_st16<kCpolPlain>(ro, col < p.n ? at + col * 2 : kPastRange,
+                                 join_halves(d[q][0], d[q][1], d[q + 1][0], d[q + 1][1]));
           }
         }
       }
     }
+    asm volatile("" ::: "memory");
   }
 };
 

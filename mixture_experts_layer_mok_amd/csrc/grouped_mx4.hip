@@ -193,13 +193,15 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int n
     src.begin();
   };
   open();
+  int stores = 0;  // made since the tile's first loads were issued
   auto run = [&](auto tile) __attribute__((always_inline)) {
-    tile.run(src);
+    tile.run(src, stores);
     const int64_t r = r0;
     const int have = rows, n0 = n * mx4::kTN;
     t += int(gridDim.x >> 3);
     if (t < end) open();
     tile.template store<OUT32>(p, r, have, n0);
+    stores = tile.template kStores<OUT32>;
   };
   while (t < end) {
     if (rows <= 64) run(mx4::Tile<A8, SG, 1>());

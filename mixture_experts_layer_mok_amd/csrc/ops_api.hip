@@ -12,6 +12,8 @@ bool type_ok(int32_t t) { return t == MOK_TYPE_BF16 || t == MOK_TYPE_FP16 || t =
 
 constexpr int64_t kMaxLd = int64_t(1) << 32;  // row strides whose products stay in 64 bits
 
+constexpr int64_t kMaxLdOut = int64_t(1) << 21;  // the product's: 256 rows stay in 31-bit offsets
+
 // A value matrix's row stride in elements; a read operand may repeat one row (ld 0).
 bool ld_ok(int64_t ld, int32_t cols, bool read) {
   return ld % 8 == 0 && ld <= kMaxLd && (ld >= cols || (read && ld == 0));
@@ -181,7 +183,7 @@ mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t l
       int64_t(n) * k >= (int64_t(1) << 31))
     return MOK_E_SHAPE;
   if (ld_a < (a8 ? k : k / 2) || ld_a % 16 != 0 || ld_a > MOK_MX_MAX_LD || ld_a_scales < k / 32 ||
-      ld_a_scales > MOK_MX_MAX_LD || ld_out < n || ld_out % 8 != 0 || ld_out > kMaxLd)
+      ld_a_scales > MOK_MX_MAX_LD || ld_out < n || ld_out % 8 != 0 || ld_out > kMaxLdOut)
     return MOK_E_SHAPE;
   if (max_rows == 0) return MOK_OK;
   if (!a_codes || !a_scales || !offsets || !b_codes || !b_scales || !out) return MOK_E_NULL;

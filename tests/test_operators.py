@@ -171,7 +171,7 @@ def test_mx4_quantisers_refuse(kw, code):
     (dict(ld_a=16), L.MOK_E_SHAPE), (dict(ld_a=40), L.MOK_E_SHAPE), (dict(ld_as=1), L.MOK_E_SHAPE),
     (dict(fmt=0), L.MOK_E_SHAPE),  # e4m3 rows take k bytes
     (dict(ld_a=L.MOK_MX_MAX_LD + 16), L.MOK_E_SHAPE), (dict(ld_as=L.MOK_MX_MAX_LD + 1), L.MOK_E_SHAPE),
-    (dict(ld_out=24), L.MOK_E_SHAPE), (dict(ld_out=68), L.MOK_E_SHAPE), (dict(a=None), L.MOK_E_NULL),
+    (dict(ld_out=24), L.MOK_E_SHAPE), (dict(ld_out=(1 << 21) + 8), L.MOK_E_SHAPE), (dict(ld_out=68), L.MOK_E_SHAPE), (dict(a=None), L.MOK_E_NULL),
     (dict(as_=None), L.MOK_E_NULL), (dict(off=None), L.MOK_E_NULL), (dict(b=None), L.MOK_E_NULL),
     (dict(bs=None), L.MOK_E_NULL), (dict(out=None), L.MOK_E_NULL), (dict(a=FAKE + 8), L.MOK_E_SHAPE),
     (dict(b=FAKE + 4), L.MOK_E_SHAPE), (dict(out=FAKE + 8), L.MOK_E_SHAPE),
