@@ -29,86 +29,187 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64
   *hi = min(int64_t(offsets[e + 1]), max_rows);
 }
 
-__device__ __forceinline__ uint32_t ld_u8(rsrc_t r, uint32_t off) {
-  return uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(r, off, 0, 0)));
-}
-
 __device__ __forceinline__ f32x4_t mfma16(i32x8_t w, i32x8_t a, f32x4_t c, int sw, int sa, bool a8) {
   return a8 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 0, 0, sw, 0, sa)
             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 4, 0, sw, 0, sa);
 }
 
-// One workgroup: 16 columns of one expert, all its rows in passes of 16 MB, the K steps of
-// 128 dealt to the four waves and their sums joined through LDS in wave order.  Loads
-// past K, past the rows and past N read zeros (zero codes and zero scales: no product).
-template <bool A8, bool OUT32, int MB>
-__global__ __launch_bounds__(256) void k_grouped_rows(GroupedArgs p) {
-  __shared__ f32x4_t s_part[4][MB][64];
-  const int e = blockIdx.y, n0 = blockIdx.x * 16;
-  int64_t lo, hi;
-  expert_rows(p.offsets, e, p.max_rows, &lo, &hi);
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int kb = p.k / 2, nblk = p.k / 32, steps = (p.k + 127) / 128;
-  const int ncols = min(16, p.n - n0);
-  const int64_t brow = int64_t(e) * p.n + n0;
-  const rsrc_t rb = row_rsrc(p.b + brow * kb, uint32_t(ncols * kb));
-  const rsrc_t rbs = row_rsrc(p.bs + brow * nblk, uint32_t(ncols * nblk));
-  const int abytes = A8 ? p.k : kb;
-  for (int64_t r0 = lo; r0 < hi; r0 += 16 * MB) {
-    const int valid = int(min(hi - r0, int64_t(16 * MB)));
-    const rsrc_t ra = row_rsrc(p.a + r0 * p.ld_a, uint32_t((valid - 1) * p.ld_a + abytes));
-    const rsrc_t ras = row_rsrc(p.as + r0 * p.ld_as, uint32_t((valid - 1) * p.ld_as + nblk));
-    f32x4_t acc[MB];
+// ------------------------------------------------------------------------------------
+// Few rows an expert (decoding): bound by reading the weights once.
+// ------------------------------------------------------------------------------------
+// One workgroup of W waves: 16 NB columns of one expert, all its rows in passes of 16 or 32.
+// The K chunks of 256 (two MFMA steps) are dealt to the waves; each loads its next chunk
+// before it multiplies the current one, straight into registers (a weight is used by one
+// wave only, so LDS would add a copy), and the waves' sums are joined through LDS in wave
+// order.  Loads past K, past the rows and past N read zeros (zero codes, zero scales: no
+// product).
+constexpr int kChunk = 256;
+
+// The eight scale bytes of a row's chunk, zeros past the row's end.  SG: bytes a load, 8 where
+// every row's scales are whole 8-byte pieces at 8-byte addresses, 4 or 1 otherwise.
+template <int SG>
+__device__ __forceinline__ void load_scales8(uint32_t (&s)[2], rsrc_t r, uint32_t off, int have) {
+  if (SG == 8) {
+    typedef uint32_t v2u_t __attribute__((ext_vector_type(2)));
+    const v2u_t v = __builtin_amdgcn_raw_buffer_load_b64(r, off | (have > 0 ? 0u : kOut), 0, 0);
+    s[0] = v.x;
+    s[1] = v.y;
+    return;
+  }
 #pragma unroll
-    for (int m = 0; m < MB; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int ks = w; ks < steps; ks += 4) {
-      const int blk = 4 * ks + g;  // this lane's scale block
-      const uint32_t out_s = blk < nblk ? 0u : kOut;
-      const v4u wv = buf_ld16<kCpolPlain>(rb, uint32_t(r16 * kb + blk * 16) + out_s);
-      const uint32_t ws = ld_u8(rbs, uint32_t(r16 * nblk + blk) + out_s);
-      const i32x8_t wf = {int(wv.x), int(wv.y), int(wv.z), int(wv.w), 0, 0, 0, 0};
+  for (int i = 0; i < 2; ++i) {
+    if (SG == 4) {
+      s[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (off + 4 * i) | (have > 4 * i ? 0u : kOut), 0, 0);
+    } else {
+      s[i] = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        s[i] |= uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(
+                    r, (off + 4 * i + c) | (have > 4 * i + c ? 0u : kOut), 0, 0)))
+                << (8 * c);
+    }
+  }
+}
+
+template <bool A8, int SG, int NB, int MB>
+struct Chunk {
+  v4u b[NB][2];         // a column block's codes, one 16-byte K block a step
+  uint32_t bs[NB][2];   // its scale dword of each step
+  v4u a[MB][2][A8 ? 2 : 1];
+  uint32_t as[MB][2];
+
+  __device__ __forceinline__ void load(const GroupedArgs& p, rsrc_t rb, rsrc_t rbs, rsrc_t ra, rsrc_t ras,
+                                       int valid, int ck) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+    const int kb = p.k / 2, nblk = p.k / 32, have = nblk - 8 * ck;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      const uint32_t row = 16 * j + r16;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        b[j][s] = buf_ld16<kCpolPlain>(
+            rb, (row * kb + (8 * ck + 4 * s + g) * 16) | (4 * s + g < have ? 0u : kOut));
+      load_scales8<SG>(bs[j], rbs, row * nblk + 8 * ck, have);
+    }
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const int row = 16 * m + r16;
+      const uint32_t out_r = row < valid ? 0u : kOut;
+      const uint32_t at = uint32_t(row * p.ld_a);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (A8) {
+          const int b0 = 4 * s + (g >> 1);
+          const uint32_t k0 = kChunk * ck + 128 * s + 16 * g;
+          a[m][s][0] = buf_ld16<kCpolPlain>(ra, (at + k0) | out_r | (b0 < have ? 0u : kOut));
+          a[m][s][A8 ? 1 : 0] = buf_ld16<kCpolPlain>(ra, (at + k0 + 64) | out_r | (b0 + 2 < have ? 0u : kOut));
+        } else {
+          a[m][s][0] = buf_ld16<kCpolPlain>(
+              ra, (at + (8 * ck + 4 * s + g) * 16) | out_r | (4 * s + g < have ? 0u : kOut));
+        }
+      }
+      load_scales8<SG>(as[m], ras, (uint32_t(row * p.ld_as) + 8 * ck) | out_r, have);
+    }
+  }
+
+  // The lane's K block of step s is 4 s + g: byte g of the step's scale dword.
+  __device__ __forceinline__ void multiply(f32x4_t (&acc)[MB][NB]) const {
+    const int sh = 8 * ((threadIdx.x & 63) >> 4);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        const int row = 16 * m + r16;
-        const uint32_t out_r = row < valid ? 0u : kOut;
-        const uint32_t as = ld_u8(ras, (uint32_t(row * p.ld_as) + blk) | out_s | out_r);
-        i32x8_t af;
-        if (A8) {
-          const int b0 = 4 * ks + (g >> 1), k0 = 128 * ks + 16 * g;
-          const v4u x = buf_ld16<kCpolPlain>(
-              ra, (uint32_t(row * p.ld_a) + k0) | out_r | (b0 < nblk ? 0u : kOut));
-          const v4u y = buf_ld16<kCpolPlain>(
-              ra, (uint32_t(row * p.ld_a) + k0 + 64) | out_r | (b0 + 2 < nblk ? 0u : kOut));
-          af = i32x8_t{int(x.x), int(x.y), int(x.z), int(x.w),
-                       int(y.x), int(y.y), int(y.z), int(y.w)};
-        } else {
-          const v4u x =
-              buf_ld16<kCpolPlain>(ra, (uint32_t(row * p.ld_a) + blk * 16) | out_s | out_r);
-          af = i32x8_t{int(x.x), int(x.y), int(x.z), int(x.w), 0, 0, 0, 0};
+        const v4u x = a[m][s][0], y = a[m][s][A8 ? 1 : 0];
+        const i32x8_t af = {int(x.x), int(x.y), int(x.z), int(x.w), int(y.x), int(y.y), int(y.z), int(y.w)};
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+          const v4u w = b[j][s];
+          const i32x8_t wf = {int(w.x), int(w.y), int(w.z), int(w.w), 0, 0, 0, 0};
+          acc[m][j] = mfma16(wf, af, acc[m][j], int(bs[j][s] >> sh), int(as[m][s] >> sh), A8);
         }
-        acc[m] = mfma16(wf, af, acc[m], int(ws), int(as), A8);
       }
-    }
+  }
+};
+
+template <bool A8, int SG, int NB, int W, int MB>
+__device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part, int64_t r0, int valid,
+                                          rsrc_t rb, rsrc_t rbs, int n0) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kb = p.k / 2, nblk = p.k / 32, chunks = (p.k + kChunk - 1) / kChunk;
+  const rsrc_t ra = row_rsrc(p.a + r0 * p.ld_a, uint32_t((valid - 1) * p.ld_a + (A8 ? p.k : kb)));
+  const rsrc_t ras = row_rsrc(p.as + r0 * p.ld_as, uint32_t((valid - 1) * p.ld_as + nblk));
+  f32x4_t acc[MB][NB];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) s_part[w][m][lane] = acc[m];
-    __syncthreads();
-    for (int i = threadIdx.x; i < MB * 64; i += 256) {
-      const int m = i >> 6, l = i & 63;
-      f32x4_t c = s_part[0][m][l];
+  for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int u = 1; u < 4; ++u) c += s_part[u][m][l];
-      const int row = 16 * m + (l & 15), col = n0 + 4 * (l >> 4);
-      if (row < valid && col < p.n) {
-        const int64_t at = (r0 + row) * p.ld_out + col;
-        if (OUT32)
-          *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at) = c;
-        else
-          *reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(p.out) + at) =
-              uint64_t(pack_bf16x2(c.x, c.y)) | (uint64_t(pack_bf16x2(c.z, c.w)) << 32);
-      }
+    for (int j = 0; j < NB; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  if (w < chunks) {
+    Chunk<A8, SG, NB, MB> cur, nxt;
+    cur.load(p, rb, rbs, ra, ras, valid, w);
+    for (int ck = w; ck < chunks; ck += W) {
+      nxt.load(p, rb, rbs, ra, ras, valid, ck + W);  // past the last: reads nothing
+      cur.multiply(acc);
+      cur = nxt;
     }
-    __syncthreads();  // s_part is rewritten by the next pass
+  }
+  // s_part[wave][block][lane]
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int j = 0; j < NB; ++j) s_part[(w * MB * NB + m * NB + j) * 64 + lane] = acc[m][j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < MB * NB * 64; i += W * 64) {
+    const int blk = i >> 6, l = i & 63, m = blk / NB, j = blk % NB;
+    f32x4_t c = s_part[i];
+#pragma unroll
+    for (int u = 1; u < W; ++u) c += s_part[u * MB * NB * 64 + i];
+    const int row = 16 * m + (l & 15), col = n0 + 16 * j + 4 * (l >> 4);
+    if (row < valid && col < p.n) {
+      const int64_t at = (r0 + row) * p.ld_out + col;
+      if (p.out32)
+        *reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at) = c;
+      else
+        *reinterpret_cast<uint64_t*>(static_cast<uint16_t*>(p.out) + at) =
+            uint64_t(pack_bf16x2(c.x, c.y)) | (uint64_t(pack_bf16x2(c.z, c.w)) << 32);
+    }
+  }
+  __syncthreads();  // s_part is rewritten by the next pass
+}
+
+template <bool A8, int SG, int NB, int W>
+__global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p) {
+  __shared__ f32x4_t s_part[W * 2 * NB * 64];
+  // the blockIdx.y-th expert that has rows
+  const int lane = threadIdx.x & 63;
+  int want = blockIdx.y, e = -1;
+  int64_t lo = 0, hi = 0;
+  for (int e0 = 0; e0 < p.groups; e0 += 64) {
+    int64_t l = 0, h = 0;
+    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &l, &h);
+    const uint64_t has = __ballot(h > l);
+    const int n = __popcll(has);
+    if (want < n) {
+      const int rank = __builtin_amdgcn_mbcnt_hi(uint32_t(has >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(has), 0u));
+      const int s = __ffsll((unsigned long long)__ballot(h > l && rank == want)) - 1;
+      e = e0 + s;
+      lo = __builtin_amdgcn_readlane(int(l), s);
+      hi = __builtin_amdgcn_readlane(int(h), s);
+      break;
+    }
+    want -= n;
+  }
+  if (e < 0) return;
+  const int n0 = blockIdx.x * 16 * NB, ncols = min(16 * NB, p.n - n0);
+  const int64_t brow = int64_t(e) * p.n + n0;
+  const rsrc_t rb = row_rsrc(p.b + brow * (p.k / 2), uint32_t(ncols * (p.k / 2)));
+  const rsrc_t rbs = row_rsrc(p.bs + brow * (p.k / 32), uint32_t(ncols * (p.k / 32)));
+  while (lo < hi) {
+    if (hi - lo <= 16) {
+      rows_pass<A8, SG, NB, W, 1>(p, s_part, lo, int(hi - lo), rb, rbs, n0);
+      break;
+    }
+    rows_pass<A8, SG, NB, W, 2>(p, s_part, lo, int(min(hi - lo, int64_t(32))), rb, rbs, n0);
+    lo += 32;
   }
 }
 
@@ -212,8 +313,21 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int n
 
 }  // namespace
 
+// Which kernel: the tiles, where they fill the GPU whatever the rows (a tile an expert and 256
+// columns at least) or where the experts have rows enough.  Measured on MI355X, weights from
+// HBM, rows kernel against tile kernel, us:
+//   128 tiles (8 experts, N 4096, K 7168, MXFP8 rows): 8 rows each 30 / 47, 32 rows 39 / 47,
+//     48 rows 63 / 48;
+//   16 tiles (1 expert, the same): 32 rows 12 / 31, 64 rows 23 / 32;
+//   224 tiles (8 experts, N 7168, K 2048, MXFP4 rows): 1 row 17 / 16, 32 rows 22 / 17;
+//   512 tiles (64 experts, N 2048, K 4096, MXFP8 rows): 4 rows 64 / 55, 32 rows 91 / 61.
+static bool use_tiles(const GroupedArgs& a) {
+  const int64_t tiles = (a.n + mx4::kTN - 1) / mx4::kTN * std::min<int64_t>(a.groups, a.max_rows);
+  return tiles >= 192 || a.max_rows > (tiles >= 64 ? 32 : 64) * int64_t(a.groups);
+}
+
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
-  if (a.max_rows / a.groups >= 64) {
+  if (use_tiles(a)) {
     const int tm = a.a8 ? mx4::tile_rows<true>() : mx4::tile_rows<false>();
     const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
     // at most this many m-tiles: every expert may end inside one
@@ -237,15 +351,30 @@ mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
     else sg(std::integral_constant<int, 1>());
     return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
   }
-  const dim3 grid(unsigned((a.n + 15) / 16), unsigned(a.groups)), block(256);
+  const int64_t align = int64_t(reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) |
+                                uintptr_t(a.ld_as) | uintptr_t(a.k / 32));
+  const int64_t experts = std::min<int64_t>(a.groups, a.max_rows);  // at most these have rows
+  auto enough = [&](int cols) { return (a.n + cols - 1) / cols * experts >= 512; };
+  const int nb = enough(64) ? 4 : enough(32) ? 2 : 1;
+  const bool deep = nb == 1 && a.k >= 16 * kChunk;
+  const dim3 grid(unsigned((a.n + 16 * nb - 1) / (16 * nb)), unsigned(experts));
+  const dim3 block(deep ? 512 : 256);
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a); };
-  if (a.a8) {
-    if (a.out32) go(k_grouped_rows<true, true, 2>);
-    else go(k_grouped_rows<true, false, 2>);
-  } else {
-    if (a.out32) go(k_grouped_rows<false, true, 2>);
-    else go(k_grouped_rows<false, false, 2>);
-  }
+  auto shape = [&](auto a8, auto g) {
+    constexpr bool A8 = decltype(a8)::value;
+    constexpr int SG = decltype(g)::value;
+    if (nb == 4) go(k_grouped_rows<A8, SG, 4, 4>);
+    else if (nb == 2) go(k_grouped_rows<A8, SG, 2, 4>);
+    else if (deep) go(k_grouped_rows<A8, SG, 1, 8>);
+    else go(k_grouped_rows<A8, SG, 1, 4>);
+  };
+  auto format = [&](auto g) {
+    if (a.a8) shape(std::true_type(), g);
+    else shape(std::false_type(), g);
+  };
+  if (align % 8 == 0) format(std::integral_constant<int, 8>());
+  else if (align % 4 == 0) format(std::integral_constant<int, 4>());
+  else format(std::integral_constant<int, 1>());
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
 }
 
