@@ -5,6 +5,7 @@
 // round to nearest even.  Nothing saturates: the rule for n bounds every magnitude by 6.
 // Both are bound by HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "launch.h"
@@ -37,142 +38,209 @@ __device__ __forceinline__ uint32_t quad_umax(uint32_t v) {
   return max(v, uint32_t(__builtin_amdgcn_mov_dpp(int(v), 0x4E, 0xF, 0xF, true)));
 }
 
-// Eight consecutive elements as floats.
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+// Eight consecutive elements: 16 bytes of a 16-bit type, 32 of fp32.
 template <int TYPE>
-__device__ __forceinline__ void load8(float (&f)[8], const void* src) {
-  const v4u* s = static_cast<const v4u*>(src);
-  const v4u v = s[0];
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  if (TYPE == MOK_TYPE_FP32) {
-    const v4u u = s[1];
-    const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+struct Eight {
+  v4u v[TYPE == MOK_TYPE_FP32 ? 2 : 1];
+
+  __device__ __forceinline__ void load(const uint8_t* src) {
+    const v4u* s = reinterpret_cast<const v4u*>(src);
+    v[0] = s[0];
+    if (TYPE == MOK_TYPE_FP32) v[TYPE == MOK_TYPE_FP32] = s[1];
+  }
+  __device__ __forceinline__ uint32_t word(int i) const {
+    const v4u& q = v[i >> 2];
+    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+  // The bits, as a float32, of the largest magnitude (magnitudes order as their bits do).
+  __device__ __forceinline__ uint32_t amax() const {
+    if (TYPE == MOK_TYPE_FP32) {
+      uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[i] = __uint_as_float(w[i]);
-      f[4 + i] = __uint_as_float(x[i]);
+      for (int i = 0; i < 8; ++i) m = max(m, word(i) & 0x7FFFFFFFu);
+      return m;
     }
-  } else {
+    u16x2_t m = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (TYPE == MOK_TYPE_BF16) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      } else {
-        const f16x2_t h = __builtin_bit_cast(f16x2_t, w[i]);
-        f[2 * i] = float(h.x);
-        f[2 * i + 1] = float(h.y);
+    for (int i = 0; i < 4; ++i)
+      m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2_t, word(i) & 0x7FFF7FFFu));
+    const uint16_t h = m.x > m.y ? m.x : m.y;
+    return TYPE == MOK_TYPE_BF16 ? uint32_t(h) << 16
+                                 : __float_as_uint(float(__builtin_bit_cast(_Float16, h)));
+  }
+  // Codes of the elements over s = 2^n.
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t q = 0;
+    q = pair<0>(q, s);
+    q = pair<1>(q, s);
+    q = pair<2>(q, s);
+    return pair<3>(q, s);
+  }
+  template <int I>
+  __device__ __forceinline__ uint32_t pair(uint32_t q, float s) const {
+    if (TYPE == MOK_TYPE_BF16)
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2_t, word(I)), s, I);
+    if (TYPE == MOK_TYPE_FP16)
+      return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(q, __builtin_bit_cast(f16x2_t, word(I)), s, I);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, __uint_as_float(word(TYPE == MOK_TYPE_FP32 ? 2 * I : 0)),
+                                                    __uint_as_float(word(TYPE == MOK_TYPE_FP32 ? 2 * I + 1 : 0)),
+                                                    s, I);
+  }
+};
+
+// Chunks of 8 elements; a quad of lanes holds one block: cols is a multiple of 32, so a quad's
+// chunks are of one row, and whole quads run or idle.  A thread takes kBatch chunks, 256 apart,
+// and loads them all before it converts any.  DENSE: the matrices have no gaps between rows and
+// are taken as one row.
+constexpr int kBatch = 4;
+
+struct Mat {
+  int64_t n_chunks;
+  int row_chunks;
+  int64_t ld_val, ld_codes, ld_scales;  // bytes from row to row
+};
+// Chunk i: its row and its place in it.
+template <bool DENSE>
+__device__ __forceinline__ void place(const Mat& m, int64_t i, int64_t* r, int64_t* c) {
+  if (DENSE) {
+    *r = 0;
+    *c = i;
+  } else {
+    *r = i / m.row_chunks;
+    *c = i - *r * m.row_chunks;
+  }
+}
+
+template <int TYPE, bool DENSE>
+__global__ __launch_bounds__(256) void k_quantize_mx4(const uint8_t* src, Mat m, uint8_t* codes,
+                                                      uint8_t* scales) {
+  constexpr int kBytes = TYPE == MOK_TYPE_FP32 ? 32 : 16;
+  for (int64_t b = int64_t(blockIdx.x) * 256 * kBatch; b < m.n_chunks;
+       b += int64_t(gridDim.x) * 256 * kBatch) {
+    Eight<TYPE> x[kBatch];
+    int64_t r[kBatch], c[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = b + 256 * u + threadIdx.x;
+      if (i < m.n_chunks) {
+        place<DENSE>(m, i, &r[u], &c[u]);
+        x[u].load(src + r[u] * m.ld_val + c[u] * kBytes);
       }
     }
-  }
-}
-
-// Chunk i of the matrix: 8 elements, row i / (cols / 8).  A quad of lanes holds one block:
-// cols is a multiple of 32, so a quad's chunks are of one row, and whole quads run or idle.
-template <int TYPE>
-__global__ __launch_bounds__(256) void k_quantize_mx4(const uint8_t* src, int64_t ld_src,
-                                                      int64_t n_chunks, int row_chunks,
-                                                      uint8_t* codes, int64_t ld_codes,
-                                                      uint8_t* scales, int64_t ld_scales) {
-  constexpr int kSize = TYPE == MOK_TYPE_FP32 ? 4 : 2;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n_chunks;
-       i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / row_chunks;
-    const int c = int(i - r * row_chunks);
-    float f[8];
-    load8<TYPE>(f, src + r * ld_src + int64_t(c) * 8 * kSize);
-    uint32_t amax = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7FFFFFFFu);
-    amax = quad_umax(amax);
-    const bool finite = amax < kInfBits;
-    const int n = mx4_shared_exp(amax);
-    const float s = pow2(min(n, 127));
-    uint32_t q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, f[0], f[1], s, 0);
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[2], f[3], s, 1);
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[4], f[5], s, 2);
-    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[6], f[7], s, 3);
-    *reinterpret_cast<uint32_t*>(codes + r * ld_codes + int64_t(c) * 4) = finite ? q : 0u;
-    if ((c & 3) == 0) scales[r * ld_scales + (c >> 2)] = finite ? uint8_t(n + 127) : uint8_t(255);
-  }
-}
-
-// Eight codes a thread.  The value of a code is exact in float32 (at scales below 2^-126
-// as a subnormal; 4 or 6 times 2^126 overflows to infinity, as a float of that value must).
-template <int TYPE>
-__global__ __launch_bounds__(256) void k_dequantize_mx4(const uint8_t* codes, int64_t ld_codes,
-                                                        const uint8_t* scales, int64_t ld_scales,
-                                                        int64_t n_chunks, int row_chunks,
-                                                        uint8_t* dst, int64_t ld_dst) {
-  constexpr int kSize = TYPE == MOK_TYPE_FP32 ? 4 : 2;
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < n_chunks;
-       i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / row_chunks;
-    const int c = int(i - r * row_chunks);
-    const uint32_t q = *reinterpret_cast<const uint32_t*>(codes + r * ld_codes + int64_t(c) * 4);
-    const int sc = scales[r * ld_scales + (c >> 2)];
-    float f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t h = (q >> (4 * e)) & 15u;
-      const uint32_t m = h & 7u;
-      // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6
-      const float mag = m < 2 ? 0.5f * float(m)
-                              : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-      const float v = ldexpf(h & 8u ? -mag : mag, sc - 127);
-      f[e] = sc == 255 ? __uint_as_float(0x7FC00000u) : v;
-    }
-    v4u* d = reinterpret_cast<v4u*>(dst + r * ld_dst + int64_t(c) * 8 * kSize);
-    if (TYPE == MOK_TYPE_FP32) {
-      d[0] = v4u{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                 __float_as_uint(f[3])};
-      d[1] = v4u{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]),
-                 __float_as_uint(f[7])};
-    } else {
-      uint32_t o[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        o[e] = TYPE == MOK_TYPE_BF16
-                   ? pack_bf16x2(f[2 * e], f[2 * e + 1])
-                   : __builtin_bit_cast(uint32_t, f16x2_t{_Float16(f[2 * e]), _Float16(f[2 * e + 1])});
-      d[0] = v4u{o[0], o[1], o[2], o[3]};
+    for (int u = 0; u < kBatch; ++u) {
+      if (b + 256 * u + threadIdx.x >= m.n_chunks) break;  // whole quads
+      const uint32_t amax = quad_umax(x[u].amax());
+      const bool finite = amax < kInfBits;
+      const int n = mx4_shared_exp(amax);
+      const uint32_t q = x[u].codes(pow2(min(n, 127)));
+      *reinterpret_cast<uint32_t*>(codes + r[u] * m.ld_codes + c[u] * 4) = finite ? q : 0u;
+      if ((threadIdx.x & 3) == 0)
+        scales[r[u] * m.ld_scales + (c[u] >> 2)] = finite ? uint8_t(n + 127) : uint8_t(255);
     }
   }
 }
 
-unsigned grid_of(int64_t n_chunks) { return unsigned(std::min<int64_t>((n_chunks + 255) / 256, 8192)); }
+// The values of four pairs of codes times s, as the eight elements of a chunk.  Exact in
+// float32 (4 or 6 times 2^126 and what lies above overflows to infinity, as a float of that
+// value must).
+template <int TYPE>
+__device__ __forceinline__ void store_values(uint8_t* dst, uint32_t q, float s, bool nan) {
+  v4u* d = reinterpret_cast<v4u*>(dst);
+  if (TYPE == MOK_TYPE_FP32) {
+    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
+    const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
+    const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
+    const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
+    const uint32_t x = 0x7FC00000u;
+    auto bits = [&](float f) { return nan ? x : __float_as_uint(f); };
+    d[0] = v4u{bits(a.x), bits(a.y), bits(b.x), bits(b.y)};
+    d[1] = v4u{bits(c.x), bits(c.y), bits(e.x), bits(e.y)};
+  } else if (TYPE == MOK_TYPE_BF16) {
+    auto two = [&](bf16x2_t h) { return nan ? 0x7FC07FC0u : __builtin_bit_cast(uint32_t, h); };
+    d[0] = v4u{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3))};
+  } else {
+    auto two = [&](f16x2_t h) { return nan ? 0x7E007E00u : __builtin_bit_cast(uint32_t, h); };
+    d[0] = v4u{two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 0)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 1)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 2)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 3))};
+  }
+}
+
+template <int TYPE, bool DENSE>
+__global__ __launch_bounds__(256) void k_dequantize_mx4(const uint8_t* codes, const uint8_t* scales,
+                                                        Mat m, uint8_t* dst) {
+  constexpr int kBytes = TYPE == MOK_TYPE_FP32 ? 32 : 16;
+  for (int64_t b = int64_t(blockIdx.x) * 256 * kBatch; b < m.n_chunks;
+       b += int64_t(gridDim.x) * 256 * kBatch) {
+    uint32_t q[kBatch];
+    int sc[kBatch];
+    int64_t r[kBatch], c[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = b + 256 * u + threadIdx.x;
+      if (i < m.n_chunks) {
+        place<DENSE>(m, i, &r[u], &c[u]);
+        q[u] = *reinterpret_cast<const uint32_t*>(codes + r[u] * m.ld_codes + c[u] * 4);
+        sc[u] = scales[r[u] * m.ld_scales + (c[u] >> 2)];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (b + 256 * u + threadIdx.x >= m.n_chunks) break;
+      store_values<TYPE>(dst + r[u] * m.ld_val + c[u] * kBytes, q[u], pow2(min(sc[u], 254) - 127),
+                         sc[u] == 255);
+    }
+  }
+}
+
 mok_status_t launched() { return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH; }
+
+Mat mat_of(const Mx4Args& a) {
+  const int es = a.type == MOK_TYPE_FP32 ? 4 : 2;
+  return Mat{a.rows * (a.cols / 8), a.cols / 8, a.ld_val * es, a.ld_codes, a.ld_scales};
+}
+bool dense(const Mx4Args& a) {
+  return a.rows == 1 || (a.ld_val == a.cols && a.ld_codes == a.cols / 2 && a.ld_scales == a.cols / 32);
+}
+unsigned grid_of(const Mat& m) {
+  return unsigned(std::min<int64_t>((m.n_chunks + 256 * kBatch - 1) / (256 * kBatch), 1 << 20));
+}
+// Calls f with the element type and density as compile-time values.
+template <typename F>
+void with_form(const Mx4Args& a, F f) {
+  auto form = [&](auto type) {
+    dense(a) ? f(type, std::true_type()) : f(type, std::false_type());
+  };
+  if (a.type == MOK_TYPE_BF16) form(std::integral_constant<int, MOK_TYPE_BF16>());
+  else if (a.type == MOK_TYPE_FP16) form(std::integral_constant<int, MOK_TYPE_FP16>());
+  else form(std::integral_constant<int, MOK_TYPE_FP32>());
+}
 
 }  // namespace
 
 mok_status_t launch_quantize_mx4(const Mx4Args& a, hipStream_t st) {
-  const int rc = a.cols / 8;
-  const int64_t n = a.rows * rc;
-  const int es = a.type == MOK_TYPE_FP32 ? 4 : 2;
-  const auto* s = static_cast<const uint8_t*>(a.src);
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3(grid_of(n)), dim3(256), 0, st, s, a.ld_val * es, n, rc, a.codes,
-                       a.ld_codes, a.scales, a.ld_scales);
-  };
-  if (a.type == MOK_TYPE_BF16) go(k_quantize_mx4<MOK_TYPE_BF16>);
-  else if (a.type == MOK_TYPE_FP16) go(k_quantize_mx4<MOK_TYPE_FP16>);
-  else go(k_quantize_mx4<MOK_TYPE_FP32>);
+  const Mat m = mat_of(a);
+  with_form(a, [&](auto type, auto flat) {
+    hipLaunchKernelGGL((k_quantize_mx4<decltype(type)::value, decltype(flat)::value>), dim3(grid_of(m)),
+                       dim3(256), 0, st, static_cast<const uint8_t*>(a.src), m, a.codes, a.scales);
+  });
   return launched();
 }
 
 mok_status_t launch_dequantize_mx4(const Mx4Args& a, hipStream_t st) {
-  const int rc = a.cols / 8;
-  const int64_t n = a.rows * rc;
-  const int es = a.type == MOK_TYPE_FP32 ? 4 : 2;
-  auto* d = static_cast<uint8_t*>(a.dst);
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, dim3(grid_of(n)), dim3(256), 0, st,
-                       static_cast<const uint8_t*>(a.codes), a.ld_codes,
-                       static_cast<const uint8_t*>(a.scales), a.ld_scales, n, rc, d,
-                       a.ld_val * es);
-  };
-  if (a.type == MOK_TYPE_BF16) go(k_dequantize_mx4<MOK_TYPE_BF16>);
-  else if (a.type == MOK_TYPE_FP16) go(k_dequantize_mx4<MOK_TYPE_FP16>);
-  else go(k_dequantize_mx4<MOK_TYPE_FP32>);
+  const Mat m = mat_of(a);
+  with_form(a, [&](auto type, auto flat) {
+    hipLaunchKernelGGL((k_dequantize_mx4<decltype(type)::value, decltype(flat)::value>), dim3(grid_of(m)),
+                       dim3(256), 0, st, static_cast<const uint8_t*>(a.codes),
+                       static_cast<const uint8_t*>(a.scales), m, static_cast<uint8_t*>(a.dst));
+  });
   return launched();
 }
 

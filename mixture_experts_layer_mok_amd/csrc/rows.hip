@@ -9,10 +9,11 @@
 //                  dw[t,j] = <dy[t], rows[pos[t,j]]>      written
 // Owning by token rather than by row reads x and dy once instead of once per routed row.
 // All are bound by HBM.
-#include <algorithm>
+#include <type_traits>
 
 #include "device.h"
 #include "launch.h"
+#include "mx.h"
 
 namespace mok {
 
@@ -101,7 +102,7 @@ __device__ __forceinline__ bool my_token(const RowGeom& g, int64_t* t, uint32_t*
 template <int W>
 constexpr int threads_of() { return W >= 4 ? W * 64 : 256; }
 
-template <int W>
+template <int W, int U>
 __global__ __launch_bounds__(threads_of<W>()) void k_permute(RowGeom g, const uint8_t* x,
                                                              const int32_t* pos, uint8_t* rows) {
   int64_t t;
@@ -111,7 +112,6 @@ __global__ __launch_bounds__(threads_of<W>()) void k_permute(RowGeom g, const ui
   const uint64_t has = __ballot(p >= 0);
   if (!has) return;
   const rsrc_t rx = row_rsrc(x + t * g.ld_tok, g.bytes);
-  constexpr int U = W == 1 ? 8 : 4;
   for (uint32_t b0 = 0; b0 < g.bytes; b0 += W * 64 * 16 * U) {
     v4u v[U];
 #pragma unroll
@@ -126,12 +126,16 @@ __global__ __launch_bounds__(threads_of<W>()) void k_permute(RowGeom g, const ui
   }
 }
 
-// dst[t] = sum_j g_j rows[pos[t,j]], g_j = w[t,j], or 1 without weights.
-template <int TYPE, int W>
+// dst[t] = sum_j g_j rows[pos[t,j]], g_j = w[t,j], or 1 without weights.  The rows of kSlots
+// pairs are loaded before any is added; missing ones get an empty range, whose loads read
+// nothing.
+template <int TYPE, int W, int U, bool NT>
 __global__ __launch_bounds__(threads_of<W>()) void k_sum_rows(RowGeom g, const uint8_t* rows,
                                                               const int32_t* pos, const float* w,
                                                               uint8_t* dst) {
   typedef Elem<TYPE> El;
+  constexpr int kSlots = U >= 8 ? 2 : 4;
+  constexpr int kPol = NT ? kCpolStream : kCpolPlain;
   int64_t t;
   uint32_t l;
   if (!my_token<W>(g, &t, &l)) return;
@@ -140,24 +144,35 @@ __global__ __launch_bounds__(threads_of<W>()) void k_sum_rows(RowGeom g, const u
   const float gate = p >= 0 ? (w ? w[t * g.k + lane] : 1.f) : 0.f;
   const uint64_t has = __ballot(p >= 0);
   const rsrc_t rd = row_rsrc(dst + t * g.ld_out, g.bytes);
-  constexpr int U = W == 1 ? 4 : 2;
   for (uint32_t b0 = 0; b0 < g.bytes; b0 += W * 64 * 16 * U) {
     float acc[U][El::kN];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int e = 0; e < El::kN; ++e) acc[u][e] = 0.f;
-    for (uint64_t m = has; m; m &= m - 1) {
-      const int j = __ffsll((unsigned long long)m) - 1;
-      const rsrc_t rr =
-          row_rsrc(rows + int64_t(__builtin_amdgcn_readlane(p, j)) * g.ld_rows, g.bytes);
-      const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate), j));
+    for (uint64_t m = has; m;) {
+      int js[kSlots];
+      v4u v[kSlots][U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float f[El::kN];
-        El::load(f, buf_ld16<kCpolPlain>(rr, b0 + (l + 64 * W * u) * 16));
+      for (int s = 0; s < kSlots; ++s) {
+        js[s] = m ? __ffsll((unsigned long long)m) - 1 : -1;
+        if (m) m &= m - 1;
+        const int64_t row = __builtin_amdgcn_readlane(p, js[s] >= 0 ? js[s] : 0);
+        const rsrc_t rr = row_rsrc(rows + (js[s] >= 0 ? row : 0) * g.ld_rows, js[s] >= 0 ? g.bytes : 0u);
 #pragma unroll
-        for (int e = 0; e < El::kN; ++e) acc[u][e] = __fadd_rn(acc[u][e], __fmul_rn(gj, f[e]));
+        for (int u = 0; u < U; ++u) v[s][u] = buf_ld16<kPol>(rr, b0 + (l + 64 * W * u) * 16);
+      }
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s) {
+        if (js[s] < 0) break;  // wave-uniform
+        const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate), js[s]));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[El::kN];
+          El::load(f, v[s][u]);
+#pragma unroll
+          for (int e = 0; e < El::kN; ++e) acc[u][e] = __fadd_rn(acc[u][e], __fmul_rn(gj, f[e]));
+        }
       }
     }
 #pragma unroll
@@ -166,111 +181,123 @@ __global__ __launch_bounds__(threads_of<W>()) void k_sum_rows(RowGeom g, const u
   }
 }
 
+// Sum over the wave, the same in every lane: the butterfly inside each row of 16 lanes by DPP
+// moves, then across the four rows.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v = row16_sum(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
 }
 
-template <int TYPE, int W>
+// One pair after the other: dy's row is read for each (from the caches after the first), so
+// that a pair's dot product stays in registers over the whole row and is summed over the
+// lanes once.
+template <int TYPE, int W, int U, bool NT>
 __global__ __launch_bounds__(threads_of<W>()) void k_unpermute_bwd(RowGeom g, const uint8_t* dy,
                                                                    const uint8_t* rows,
                                                                    const int32_t* pos,
                                                                    const float* w, uint8_t* d_rows,
                                                                    float* dw) {
   typedef Elem<TYPE> El;
+  constexpr int kPol = NT ? kCpolStream : kCpolPlain;
   __shared__ float s_dw[W > 1 ? kMaxWaves : 1][64];
   int64_t t;
   uint32_t l;
-  const bool valid = my_token<W>(g, &t, &l);
-  if (!valid) return;  // whole waves, and whole workgroups where waves share a token
+  if (!my_token<W>(g, &t, &l)) return;  // whole waves; whole workgroups where they share a token
   const int lane = threadIdx.x & 63;
   const int32_t p = my_row(g, pos, t);
   const float gate = p >= 0 ? w[t * g.k + lane] : 0.f;
-  const uint64_t has = __ballot(p >= 0);
   const rsrc_t ry = row_rsrc(dy + t * g.ld_tok, g.bytes);
   float my_dw = 0.f;  // lane j: this wave's part of dw[t, j]
-  constexpr int U = W == 1 ? 4 : 2;
-  if (has) {
+  for (uint64_t m = __ballot(p >= 0); m; m &= m - 1) {
+    const int j = __ffsll((unsigned long long)m) - 1;
+    const int64_t row = __builtin_amdgcn_readlane(p, j);
+    const rsrc_t rr = row_rsrc(rows + row * g.ld_rows, g.bytes);
+    const rsrc_t rd = row_rsrc(d_rows + row * g.ld_out, g.bytes);
+    const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate), j));
+    float dot = 0.f;
     for (uint32_t b0 = 0; b0 < g.bytes; b0 += W * 64 * 16 * U) {
-      float y[U][El::kN];
+      v4u yv[U], rv[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        El::load(y[u], buf_ld16<kCpolPlain>(ry, b0 + (l + 64 * W * u) * 16));
-      for (uint64_t m = has; m; m &= m - 1) {
-        const int j = __ffsll((unsigned long long)m) - 1;
-        const int64_t row = __builtin_amdgcn_readlane(p, j);
-        const rsrc_t rr = row_rsrc(rows + row * g.ld_rows, g.bytes);
-        const rsrc_t rd = row_rsrc(d_rows + row * g.ld_out, g.bytes);
-        const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(gate), j));
-        float dot = 0.f;
+      for (int u = 0; u < U; ++u) {
+        yv[u] = buf_ld16<kCpolPlain>(ry, b0 + (l + 64 * W * u) * 16);
+        rv[u] = buf_ld16<kPol>(rr, b0 + (l + 64 * W * u) * 16);
+      }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t off = b0 + (l + 64 * W * u) * 16;
-          float f[El::kN], o[El::kN];
-          El::load(f, buf_ld16<kCpolPlain>(rr, off));
+      for (int u = 0; u < U; ++u) {
+        float y[El::kN], f[El::kN], o[El::kN];
+        El::load(y, yv[u]);
+        El::load(f, rv[u]);
 #pragma unroll
-          for (int e = 0; e < El::kN; ++e) {
-            dot = fmaf(y[u][e], f[e], dot);
-            o[e] = __fmul_rn(gj, y[u][e]);
-          }
-          buf_st16<kCpolStream>(rd, off, El::store(o));
+        for (int e = 0; e < El::kN; ++e) {
+          dot = fmaf(y[e], f[e], dot);
+          o[e] = __fmul_rn(gj, y[e]);
         }
-        dot = wave_sum(dot);
-        if (lane == j) my_dw += dot;
+        buf_st16<kCpolStream>(rd, b0 + (l + 64 * W * u) * 16, El::store(o));
       }
     }
+    dot = wave_sum(dot);
+    if (lane == j) my_dw = dot;
   }
   if (W > 1) {
-    const int wv = (threadIdx.x >> 6);
+    const int wv = threadIdx.x >> 6;
     s_dw[wv][lane] = my_dw;
     __syncthreads();
-    const int w0 = wv / W * W;
-    if (wv == w0) {
-      my_dw = 0.f;
+    if (wv) return;
+    my_dw = 0.f;
 #pragma unroll
-      for (int i = 0; i < W; ++i) my_dw += s_dw[w0 + i][lane];
-    }
-    if (wv != w0) return;
+    for (int i = 0; i < W; ++i) my_dw += s_dw[i][lane];
   }
   if (lane < g.k) dw[t * g.k + lane] = my_dw;
 }
 
 mok_status_t launched() { return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH; }
 
-// Waves per token: one where the tokens alone fill the GPU, sixteen for a few tokens.
-int waves_for(int64_t T) { return T >= 2048 ? 1 : (T >= 512 ? 4 : 16); }
-unsigned grid_for(int64_t T, int W) { return unsigned(W >= 4 ? T : (T + 4 / W - 1) / (4 / W)); }
+// Launch shape.
+//   W: waves a token: one where the tokens alone fill the GPU (or the row is one chunk a lane),
+//     else four, or sixteen for long rows, so that a lane holds one chunk of its row.  Measured
+//     on MI355X, us for W = 1 / 4 / 16 (bf16, k = 8; permute, unpermute, its gradient):
+//       128 tokens of 7168:  7.0 / 5.7 / 4.7, 10.1 / 8.3 / 4.6, 18.6 / 11.5 / 7.3
+//       512 tokens of 2048:  4.6 / 4.3 / 5.2,  4.7 / 4.1 / 6.1,  8.0 / 6.5 / 10.1
+//       1024 tokens of 2048: 6.8 / 6.6 / 7.4,  6.8 / 6.5 / 11.7, 11.6 / 11.9 / 18.9
+//       4096 tokens of 512:  6.8 / 7.6 / 20.3, 7.0 / 12.5 / 36.7, 12.8 / 19.3 / 59.8
+//   U: 16-byte chunks a lane in flight, the smallest that takes the row in one pass (loads past
+//     its end cost an issue), at most umax.
+//   nt: rows too many for the last-level cache (256 MB) are read non-temporally; smaller ones
+//     may still be there from the operator that wrote them.  Measured: 86,552 rows of 7168
+//     (1.24 GB) 296 us plain, 285 nt; 512 rows of 7168 4.9 us plain, 6.9 nt.
+struct Shape {
+  int W, U;
+  bool nt;
+};
+Shape shape_of(const RowGeom& g, int umax) {
+  Shape s;
+  s.W = g.T >= 1024 || g.bytes <= 1024 ? 1 : g.bytes > 6144 ? 16 : 4;
+  const int chunks = int((g.bytes + 1023) / 1024);
+  s.U = s.W > 1 ? 1 : chunks <= 2 ? 2 : chunks <= 4 ? 4 : chunks <= 8 || umax == 8 ? 8 : 16;
+  s.nt = s.W == 1 && (g.max_rows + g.T) * int64_t(g.bytes) > (int64_t(256) << 20);
+  return s;
+}
+unsigned grid_for(int64_t T, int W) { return unsigned(W >= 4 ? T : (T + 3) / 4); }
 
-template <int W>
-void run_permute(const RowGeom& g, const RowArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(k_permute<W>, dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
-                     static_cast<const uint8_t*>(a.tok), a.pos, static_cast<uint8_t*>(a.out));
+// Calls f with the shape's W, U and nt as compile-time values.
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <int UMAX, typename F>
+void with_shape(const Shape& s, F f) {
+  if (s.W == 4) return f(Int<4>(), Int<1>(), std::false_type());
+  if (s.W == 16) return f(Int<16>(), Int<1>(), std::false_type());
+  auto nt = [&](auto u) { s.nt ? f(Int<1>(), u, std::true_type()) : f(Int<1>(), u, std::false_type()); };
+  if (s.U == 2) return nt(Int<2>());
+  if (s.U == 4) return nt(Int<4>());
+  if (UMAX == 8 || s.U == 8) return nt(Int<8>());
+  nt(Int<UMAX>());
 }
-template <int TYPE, int W>
-void run_sum(const RowGeom& g, const RowArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_sum_rows<TYPE, W>), dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st,
-                     g, static_cast<const uint8_t*>(a.rows), a.pos, a.w,
-                     static_cast<uint8_t*>(a.out));
-}
-template <int TYPE, int W>
-void run_bwd(const RowGeom& g, const RowArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_unpermute_bwd<TYPE, W>), dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0,
-                     st, g, static_cast<const uint8_t*>(a.tok),
-                     static_cast<const uint8_t*>(a.rows), a.pos, a.w,
-                     static_cast<uint8_t*>(a.out), a.dw);
-}
-template <int TYPE>
-void run_sum_w(int W, const RowGeom& g, const RowArgs& a, hipStream_t st) {
-  if (W == 1) run_sum<TYPE, 1>(g, a, st);
-  else if (W == 4) run_sum<TYPE, 4>(g, a, st);
-  else run_sum<TYPE, 16>(g, a, st);
-}
-template <int TYPE>
-void run_bwd_w(int W, const RowGeom& g, const RowArgs& a, hipStream_t st) {
-  if (W == 1) run_bwd<TYPE, 1>(g, a, st);
-  else if (W == 4) run_bwd<TYPE, 4>(g, a, st);
-  else run_bwd<TYPE, 16>(g, a, st);
+template <typename F>
+void with_type(int32_t type, F f) {
+  if (type == MOK_TYPE_BF16) f(Int<MOK_TYPE_BF16>());
+  else if (type == MOK_TYPE_FP16) f(Int<MOK_TYPE_FP16>());
+  else f(Int<MOK_TYPE_FP32>());
 }
 
 RowGeom geom_of(const RowArgs& a) {
@@ -284,28 +311,40 @@ RowGeom geom_of(const RowArgs& a) {
 mok_status_t launch_permute(const RowArgs& a, hipStream_t st) {
   RowGeom g = geom_of(a);
   g.ld_rows = g.ld_out;
-  const int W = waves_for(a.T);
-  if (W == 1) run_permute<1>(g, a, st);
-  else if (W == 4) run_permute<4>(g, a, st);
-  else run_permute<16>(g, a, st);
+  Shape s = shape_of(g, 16);
+  s.nt = false;
+  with_shape<16>(s, [&](auto w, auto u, auto) {
+    constexpr int W = decltype(w)::value, U = decltype(u)::value;
+    hipLaunchKernelGGL((k_permute<W, U>), dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
+                       static_cast<const uint8_t*>(a.tok), a.pos, static_cast<uint8_t*>(a.out));
+  });
   return launched();
 }
 
 mok_status_t launch_sum_rows(const RowArgs& a, hipStream_t st) {
   const RowGeom g = geom_of(a);
-  const int W = waves_for(a.T);
-  if (a.type == MOK_TYPE_BF16) run_sum_w<MOK_TYPE_BF16>(W, g, a, st);
-  else if (a.type == MOK_TYPE_FP16) run_sum_w<MOK_TYPE_FP16>(W, g, a, st);
-  else run_sum_w<MOK_TYPE_FP32>(W, g, a, st);
+  with_type(a.type, [&](auto type) {
+    with_shape<8>(shape_of(g, 8), [&](auto w, auto u, auto nt) {
+      constexpr int W = decltype(w)::value, U = decltype(u)::value;
+      hipLaunchKernelGGL((k_sum_rows<decltype(type)::value, W, U, decltype(nt)::value>),
+                         dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
+                         static_cast<const uint8_t*>(a.rows), a.pos, a.w, static_cast<uint8_t*>(a.out));
+    });
+  });
   return launched();
 }
 
 mok_status_t launch_unpermute_bwd(const RowArgs& a, hipStream_t st) {
   const RowGeom g = geom_of(a);
-  const int W = waves_for(a.T);
-  if (a.type == MOK_TYPE_BF16) run_bwd_w<MOK_TYPE_BF16>(W, g, a, st);
-  else if (a.type == MOK_TYPE_FP16) run_bwd_w<MOK_TYPE_FP16>(W, g, a, st);
-  else run_bwd_w<MOK_TYPE_FP32>(W, g, a, st);
+  with_type(a.type, [&](auto type) {
+    with_shape<16>(shape_of(g, 16), [&](auto w, auto u, auto nt) {
+      constexpr int W = decltype(w)::value, U = decltype(u)::value;
+      hipLaunchKernelGGL((k_unpermute_bwd<decltype(type)::value, W, U, decltype(nt)::value>),
+                         dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
+                         static_cast<const uint8_t*>(a.tok), static_cast<const uint8_t*>(a.rows), a.pos,
+                         a.w, static_cast<uint8_t*>(a.out), a.dw);
+    });
+  });
   return launched();
 }
 
