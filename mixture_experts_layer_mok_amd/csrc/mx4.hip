@@ -45,10 +45,12 @@ template <int TYPE>
 struct Eight {
   v4u v[TYPE == MOK_TYPE_FP32 ? 2 : 1];
 
+  template <bool NT>
   __device__ __forceinline__ void load(const uint8_t* src) {
     const v4u* s = reinterpret_cast<const v4u*>(src);
-    v[0] = s[0];
-    if (TYPE == MOK_TYPE_FP32) v[TYPE == MOK_TYPE_FP32] = s[1];
+#pragma unroll
+    for (int i = 0; i < (TYPE == MOK_TYPE_FP32 ? 2 : 1); ++i)
+      v[i] = NT ? __builtin_nontemporal_load(s + i) : s[i];
   }
   __device__ __forceinline__ uint32_t word(int i) const {
     const v4u& q = v[i >> 2];
@@ -90,10 +92,10 @@ struct Eight {
   }
 };
 
-// Chunks of 8 elements; a quad of lanes holds one block: cols is a multiple of 32, so a quad's
-// chunks are of one row, and whole quads run or idle.  A thread takes kBatch chunks, 256 apart,
-// and loads them all before it converts any.  DENSE: the matrices have no gaps between rows and
-// are taken as one row.
+// Chunks of a few elements (8 where quantised, so that a quad of lanes holds one block: cols
+// is a multiple of 32, so a quad's chunks are of one row, and whole quads run or idle).  A
+// wave takes 64 kBatch consecutive chunks and loads them all before it converts any.  DENSE:
+// the matrices have no gaps between rows and are taken as one row.
 constexpr int kBatch = 4;
 
 struct Mat {
@@ -113,98 +115,98 @@ __device__ __forceinline__ void place(const Mat& m, int64_t i, int64_t* r, int64
   }
 }
 
-template <int TYPE, bool DENSE>
+template <int TYPE, bool DENSE, bool NT>
 __global__ __launch_bounds__(256) void k_quantize_mx4(const uint8_t* src, Mat m, uint8_t* codes,
                                                       uint8_t* scales) {
   constexpr int kBytes = TYPE == MOK_TYPE_FP32 ? 32 : 16;
-  for (int64_t b = int64_t(blockIdx.x) * 256 * kBatch; b < m.n_chunks;
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * 64 * kBatch; b < m.n_chunks;
        b += int64_t(gridDim.x) * 256 * kBatch) {
     Eight<TYPE> x[kBatch];
     int64_t r[kBatch], c[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = b + 256 * u + threadIdx.x;
+      const int64_t i = b + 64 * u + lane;
       if (i < m.n_chunks) {
         place<DENSE>(m, i, &r[u], &c[u]);
-        x[u].load(src + r[u] * m.ld_val + c[u] * kBytes);
+        x[u].template load<NT>(src + r[u] * m.ld_val + c[u] * kBytes);
       }
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (b + 256 * u + threadIdx.x >= m.n_chunks) break;  // whole quads
+      if (b + 64 * u + lane >= m.n_chunks) break;  // whole quads
       const uint32_t amax = quad_umax(x[u].amax());
       const bool finite = amax < kInfBits;
       const int n = mx4_shared_exp(amax);
       const uint32_t q = x[u].codes(pow2(min(n, 127)));
       *reinterpret_cast<uint32_t*>(codes + r[u] * m.ld_codes + c[u] * 4) = finite ? q : 0u;
-      if ((threadIdx.x & 3) == 0)
+      if ((lane & 3) == 0)
         scales[r[u] * m.ld_scales + (c[u] >> 2)] = finite ? uint8_t(n + 127) : uint8_t(255);
     }
   }
 }
 
-// The values of four pairs of codes times s, as the eight elements of a chunk.  Exact in
-// float32 (4 or 6 times 2^126 and what lies above overflows to infinity, as a float of that
-// value must).
+// Sixteen bytes of values: code pairs 0.. of q times s.  Exact in float32 (4 or 6 times 2^126
+// and what lies above overflows to infinity, as a float of that value must).
 template <int TYPE>
-__device__ __forceinline__ void store_values(uint8_t* dst, uint32_t q, float s, bool nan) {
-  v4u* d = reinterpret_cast<v4u*>(dst);
+__device__ __forceinline__ v4u values16(uint32_t q, float s, bool nan) {
   if (TYPE == MOK_TYPE_FP32) {
     const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 0);
     const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 1);
-    const f32x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 2);
-    const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, s, 3);
-    const uint32_t x = 0x7FC00000u;
-    auto bits = [&](float f) { return nan ? x : __float_as_uint(f); };
-    d[0] = v4u{bits(a.x), bits(a.y), bits(b.x), bits(b.y)};
-    d[1] = v4u{bits(c.x), bits(c.y), bits(e.x), bits(e.y)};
-  } else if (TYPE == MOK_TYPE_BF16) {
+    auto bits = [&](float f) { return nan ? 0x7FC00000u : __float_as_uint(f); };
+    return v4u{bits(a.x), bits(a.y), bits(b.x), bits(b.y)};
+  }
+  if (TYPE == MOK_TYPE_BF16) {
     auto two = [&](bf16x2_t h) { return nan ? 0x7FC07FC0u : __builtin_bit_cast(uint32_t, h); };
-    d[0] = v4u{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0)),
+    return v4u{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 0)),
                two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 1)),
                two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 2)),
                two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, s, 3))};
-  } else {
-    auto two = [&](f16x2_t h) { return nan ? 0x7E007E00u : __builtin_bit_cast(uint32_t, h); };
-    d[0] = v4u{two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 0)),
-               two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 1)),
-               two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 2)),
-               two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 3))};
   }
+  auto two = [&](f16x2_t h) { return nan ? 0x7E007E00u : __builtin_bit_cast(uint32_t, h); };
+  return v4u{two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 0)),
+             two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 1)),
+             two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 2)),
+             two(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, s, 3))};
 }
 
+// Chunks of 16 bytes of values: a wave's stores are whole lines (fp32 in chunks of 32 bytes, two
+// stores each, was 131 us at [16384, 7168] against 100 us of traffic).
 template <int TYPE, bool DENSE>
 __global__ __launch_bounds__(256) void k_dequantize_mx4(const uint8_t* codes, const uint8_t* scales,
                                                         Mat m, uint8_t* dst) {
-  constexpr int kBytes = TYPE == MOK_TYPE_FP32 ? 32 : 16;
-  for (int64_t b = int64_t(blockIdx.x) * 256 * kBatch; b < m.n_chunks;
+  constexpr int kElems = TYPE == MOK_TYPE_FP32 ? 4 : 8;
+  const int lane = threadIdx.x & 63;
+  for (int64_t b = (int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6)) * 64 * kBatch; b < m.n_chunks;
        b += int64_t(gridDim.x) * 256 * kBatch) {
     uint32_t q[kBatch];
     int sc[kBatch];
     int64_t r[kBatch], c[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = b + 256 * u + threadIdx.x;
+      const int64_t i = b + 64 * u + lane;
       if (i < m.n_chunks) {
         place<DENSE>(m, i, &r[u], &c[u]);
-        q[u] = *reinterpret_cast<const uint32_t*>(codes + r[u] * m.ld_codes + c[u] * 4);
-        sc[u] = scales[r[u] * m.ld_scales + (c[u] >> 2)];
+        const uint8_t* at = codes + r[u] * m.ld_codes + c[u] * (kElems / 2);
+        q[u] = TYPE == MOK_TYPE_FP32 ? *reinterpret_cast<const uint16_t*>(at)
+                                     : *reinterpret_cast<const uint32_t*>(at);
+        sc[u] = scales[r[u] * m.ld_scales + c[u] / (32 / kElems)];
       }
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      if (b + 256 * u + threadIdx.x >= m.n_chunks) break;
-      store_values<TYPE>(dst + r[u] * m.ld_val + c[u] * kBytes, q[u], pow2(min(sc[u], 254) - 127),
-                         sc[u] == 255);
+      if (b + 64 * u + lane >= m.n_chunks) break;
+      *reinterpret_cast<v4u*>(dst + r[u] * m.ld_val + c[u] * 16) =
+          values16<TYPE>(q[u], pow2(min(sc[u], 254) - 127), sc[u] == 255);
     }
   }
 }
 
 mok_status_t launched() { return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH; }
 
-Mat mat_of(const Mx4Args& a) {
+Mat mat_of(const Mx4Args& a, int elems) {
   const int es = a.type == MOK_TYPE_FP32 ? 4 : 2;
-  return Mat{a.rows * (a.cols / 8), a.cols / 8, a.ld_val * es, a.ld_codes, a.ld_scales};
+  return Mat{a.rows * (a.cols / elems), a.cols / elems, a.ld_val * es, a.ld_codes, a.ld_scales};
 }
 bool dense(const Mx4Args& a) {
   return a.rows == 1 || (a.ld_val == a.cols && a.ld_codes == a.cols / 2 && a.ld_scales == a.cols / 32);
@@ -226,16 +228,26 @@ void with_form(const Mx4Args& a, F f) {
 }  // namespace
 
 mok_status_t launch_quantize_mx4(const Mx4Args& a, hipStream_t st) {
-  const Mat m = mat_of(a);
+  const Mat m = mat_of(a, 8);
+  // What the call reads and writes, against the last-level cache: a larger source is read
+  // non-temporally ([16384, 7168] bf16 53 -> 47 us; [4096, 7168] 12.9 plain, 14.0 so).
+  const int64_t moved = a.rows * a.cols * (a.type == MOK_TYPE_FP32 ? 4 : 2) + a.rows * (a.cols / 2);
+  const bool nt = moved > (int64_t(256) << 20);
   with_form(a, [&](auto type, auto flat) {
-    hipLaunchKernelGGL((k_quantize_mx4<decltype(type)::value, decltype(flat)::value>), dim3(grid_of(m)),
-                       dim3(256), 0, st, static_cast<const uint8_t*>(a.src), m, a.codes, a.scales);
+    constexpr int kType = decltype(type)::value;
+    constexpr bool kFlat = decltype(flat)::value;
+    auto go = [&](auto kern) {
+      hipLaunchKernelGGL(kern, dim3(grid_of(m)), dim3(256), 0, st, static_cast<const uint8_t*>(a.src), m,
+                         a.codes, a.scales);
+    };
+    if (nt) go(k_quantize_mx4<kType, kFlat, true>);
+    else go(k_quantize_mx4<kType, kFlat, false>);
   });
   return launched();
 }
 
 mok_status_t launch_dequantize_mx4(const Mx4Args& a, hipStream_t st) {
-  const Mat m = mat_of(a);
+  const Mat m = mat_of(a, a.type == MOK_TYPE_FP32 ? 4 : 8);
   with_form(a, [&](auto type, auto flat) {
     hipLaunchKernelGGL((k_dequantize_mx4<decltype(type)::value, decltype(flat)::value>), dim3(grid_of(m)),
                        dim3(256), 0, st, static_cast<const uint8_t*>(a.codes),

@@ -119,6 +119,24 @@ def test_dequantise_every_code_and_scale():
         assert torch.equal(torch.signbit(v).cpu()[:255, 0], torch.signbit(want)[:255])
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_quantise_more_than_the_cache(dtype):
+    """A source past 256 MB: the rows at both ends and in between, and the same rows alone."""
+    R, K = 70000, 2048
+    src = torch.zeros(R, K, dtype=dtype, device=DEV)
+    at = torch.tensor([0, 1, 35001, R - 2, R - 1], device=DEV)
+    some = torch.randn(5, K, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    src[at] = some.to(dtype)
+    codes, scales = ops.quantize_mx4(src)
+    c, s = check_quantise(src[at])
+    assert torch.equal(codes[at], c) and torch.equal(scales[at], s)
+    rest = torch.ones(R, dtype=torch.bool, device=DEV)
+    rest[at] = False
+    assert not codes[rest].any() and not scales[rest].any()
+    back = ops.dequantize_mx4(codes, scales, dtype=dtype)
+    assert torch.equal(back[at], ops.dequantize_mx4(c, s, dtype=dtype)) and not back[rest].any()
+
+
 def test_empty():
     c, s = ops.quantize_mx4(torch.empty(0, 64, device=DEV))
     assert c.shape == (0, 32) and s.shape == (0, 2)

@@ -93,12 +93,55 @@ def test_small(T, k, E, D, dtype):
     run_all(T, k, E, D, dtype, seed=T + k)
 
 
-# both sides of the tokens at which fewer waves share a token
-@pytest.mark.parametrize("T", [511, 512, 2047, 2048, 2053])
-@pytest.mark.parametrize("D", [64, 8200])
+# both sides of the tokens and row lengths at which fewer waves share a token
+@pytest.mark.parametrize("T", [511, 1023, 1024, 2053])
+@pytest.mark.parametrize("D", [64, 512, 520, 1032])
 def test_many_tokens(T, D):
     say(f"[rows] T={T} D={D}")
-    run_all(T, 2, 7, D if T < 600 or D == 64 else 1032, torch.bfloat16, seed=T)
+    run_all(T, 2, 7, D, torch.bfloat16, seed=T)
+
+
+# one wave a token: each number of chunks in flight, rows of one pass and of several
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("D", [1536, 2600, 4104, 8200])
+def test_long_rows_of_many_tokens(D, dtype):
+    say(f"[rows] T=1030 D={D} {dtype}")
+    run_all(1030, 1, 3, D, dtype, seed=D)
+
+
+@pytest.mark.parametrize("D", [3064, 3080])
+def test_rows_on_both_sides_of_sixteen_waves(D):
+    say(f"[rows] T=40 D={D}")
+    run_all(40, 3, 7, D, torch.bfloat16, seed=D)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_more_rows_than_the_cache(dtype):
+    """Row buffers past 256 MB, few of whose rows are routed."""
+    say(f"[rows] large buffers {dtype}")
+    n, D, T, k = 140000, 1032 if dtype != torch.float32 else 520, 1100, 2
+    pos, R = _routing(T, k, 5, 77)
+    place = np.random.default_rng(78).permutation(n)[:R].astype(np.int32)
+    pos = np.where(pos >= 0, place[np.maximum(pos, 0)], -1).astype(np.int32)
+    rng = np.random.default_rng(79)
+    p = torch.from_numpy(pos).to(DEV)
+    rows = torch.empty(n, D, dtype=dtype, device=DEV)
+    x, w = randn(rng, T, D, dtype=dtype), torch.rand(T, k, device=DEV)
+    ops.permute(x, p, rows)
+    used = f64(rows[torch.from_numpy(place).to(DEV).long()])
+    compact = np.full(n, -1, np.int64)
+    compact[place] = np.arange(R)
+    cpos = np.where(pos >= 0, compact[np.maximum(pos, 0)], -1)
+    np.testing.assert_array_equal(used, O.permute(f64(x), cpos, np.zeros((R, D))))
+    y = ops.unpermute(rows, p, w)
+    want, s = O.unpermute(used, cpos, f64(w))
+    close(y, want, s, k, dtype, "unpermute")
+    dy = randn(rng, T, D, dtype=dtype)
+    d_rows, dw = ops.unpermute_backward(dy, rows, p, w, torch.empty_like(rows))
+    want, want_w, s = O.unpermute_backward(f64(dy), used, cpos, f64(w), np.zeros((R, D)))
+    got = d_rows[torch.from_numpy(place).to(DEV).long()]
+    close(got, want, np.abs(want), 1, dtype, "d_rows")
+    assert (np.abs(f64(dw) - want_w) <= (D / 64 + 96) * E24 * s + E24 * np.abs(want_w)).all()
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=IDS)
