@@ -31,7 +31,7 @@
 // a wave: IB = 1 covers 64 rows, 2 covers 128, 4 covers 256.
 //
 // A workgroup walks several tiles: the next one's first loads are in flight while the current
-// one's results are stored, straight from the registers.
+// one's results are stored, through LDS that those loads leave free.
 #pragma once
 #include "gemm_bf16.h"
 
@@ -118,7 +118,6 @@ struct Source {
   uint32_t osa, osb;         // this thread's scale rows
   int nblk;                  // K blocks
   int ca, cb;                // this lane's chunk of an A and of a B row
-  int qa;                    // A loads a step (those of rows that a block covers)
 
   __device__ __forceinline__ void init(const GroupedArgs& p, int e, int64_t r0, int rows, int n0) {
     const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -128,7 +127,6 @@ struct Source {
     rb = rsrc_2g(p.b + int64_t(e) * p.n * kb);
     ca = A8 ? ((l & 15) ^ (((w & 3) * 4 + (l >> 4)) & 15)) : ((l & 7) ^ (l >> 3) ^ (w & 1));
     cb = (l & 7) ^ (l >> 3) ^ (w & 1);
-    qa = rows <= 64 ? (A8 ? 4 : 2) : rows <= 128 ? (A8 ? 8 : 4) : 8;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int ar = A8 ? (q * 4 + w) * 4 + (l >> 4) : (q * 4 + w) * 8 + (l >> 3);
@@ -211,13 +209,12 @@ struct Source {
     return s;
   }
 
-  // The scales of the first eight steps, then the data of step 0, then of step 1: kAhead loads
+  // The scales of the first four steps, then the data of step 0, then of step 1: kAhead loads
   // a wave may be in flight when step 0 has landed.
   static constexpr int kAhead = 16;
   __device__ __forceinline__ void begin() const {
     asm volatile("" ::: "memory");
     issue_scales(0);
-    issue_scales(1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -241,15 +238,6 @@ __device__ __forceinline__ void wait_all_but(int n) {
   else if (n >= 16) wait_vmcnt<16>();
   else if (n >= 8) wait_vmcnt<8>();
   else wait_vmcnt<0>();
-}
-
-// Columns 8 c .. 8 c + 7 of one row, this lane's: of two neighbouring groups of eight, lanes 0..31
-// hold the first and lanes 32..63 the second.  lo, hi: two bf16 pairs of each group as the
-// accumulators have them (lane r: columns 0..3 of row r, lane 32 + r: columns 4..7).
-__device__ __forceinline__ v4u join_halves(uint32_t x0, uint32_t x1, uint32_t y0, uint32_t y1) {
-  const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-  const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-  return v4u{uint32_t(s0[0]), uint32_t(s1[0]), uint32_t(s0[1]), uint32_t(s1[1])};
 }
 
 template <bool A8, int SG, int IB>
@@ -354,7 +342,7 @@ struct Tile {
     const Src src = opened.uniform();
     init();
     wait_all_but(Src::kAhead + stores);  // step 0 and its scales
-    wait_lds();                           // scales written through registers (SG 1)
+    wait_lds();  // scales written through registers (SG 1); the last tile's results read back
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     // f[s]: the fragments of slice s.  Those of slices 0..2 are read one step ahead, those of
@@ -381,7 +369,10 @@ struct Tile {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       const uint32_t nxt = cur ^ kStageB;
-      if ((ks & 3) == 3) src.issue_scales(ks / 4 + 2);  // into the half of the ring just read
+      // The scales of the next four steps into the half of the ring that all have read (for step
+      // 0 the half that the last tile's results went through).
+      if ((ks & 3) == 3) src.issue_scales(ks / 4 + 2);
+      if (ks == 0) src.issue_scales(1);
       read_scales(sn, ks + 1);
       slice<1, 0, 0, kD1>(src, f[1], f[0], sc, nxt, ks, cur);
       slice<2, 1, kD1, kD2>(src, f[2], f[1], sc, nxt, ks, cur);
@@ -396,9 +387,12 @@ struct Tile {
   }
 
   // Block (i, j): lane l holds row l % 32 of A and, of B's 32 rows, 8 q + 4 h + u (q, u =
-  // 0..3): four consecutive columns of out each.  fp32: 16 bytes a lane, two lanes to 32 bytes
-  // of a row; bf16: the two lanes of a row trade halves (v_permlane32_swap) so that each
-  // stores 16 bytes, again 32 of a row.
+  // 0..3): four consecutive columns of out each.  Stored as they are, an instruction would write
+  // 16 or 32 bytes of 32 rows, and the results cost as much as if nothing ran beside them.  So 32
+  // rows of 128 bytes at a time go through 4 KB a wave of the scale ring's second half, which
+  // the next tile fills later, and leave as whole 128-byte lines, non-temporally (8 chunks of 16
+  // bytes, chunk c of row r at c ^ (r & 7) ^ ((r >> 3) & 1)).  16,384 rows, N 7168, K 2048 in
+  // MXFP4 on MI355X: 171 us with 32-byte stores, 167 with whole lines, 157 non-temporally.
   // The stores go through a buffer resource whose range drops what lies outside the expert's
   // rows and N, so that every wave makes the same number of them: kStores.
   template <bool OUT32>
@@ -409,39 +403,42 @@ struct Tile {
     const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
     constexpr int kSize = OUT32 ? 4 : 2;
-    const int col0 = n0 + wn * 128;
+    constexpr int kJ = OUT32 ? 1 : 2;  // column blocks that make 128 bytes
     const rsrc_t ro = row_rsrc(static_cast<uint8_t*>(p.out) + r0 * p.ld_out * kSize, kPastRange);
+    const uint32_t area = (w & 2 ? lds_addr(g_sb) : lds_addr(g_sa)) + 8192 + uint32_t(w & 1) * 4096;
+    const uint32_t wr = area + uint32_t(r) * 128;
+    const int sw = (r & 7) ^ ((r >> 3) & 1);
+    // read back: instruction x takes rows 8 x + l / 8, place l % 8
+    const int rr = l >> 3, rsw = rr & 7;
 #pragma unroll
-    for (int i = 0; i < IB; ++i) {
-      const int row = (wm * IB + i) * 32 + r;
-      const uint32_t at = row < rows ? uint32_t(row) * uint32_t(p.ld_out) * kSize : kPastRange;
+    for (int i = 0; i < IB; ++i)
 #pragma unroll
-      for (int j = 0; j < kJB; ++j) {
-        if (OUT32) {
+      for (int j0 = 0; j0 < kJB; j0 += kJ) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int col = col0 + 32 * j + 8 * q + 4 * h;
-            buf_st16<kCpolPlain>(ro, col < p.n ? at + col * 4 : kPastRange,
-                                 __builtin_bit_cast(v4u, f32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1],
-                                                                 acc[i][j][4 * q + 2],
-                                                                 acc[i][j][4 * q + 3]}));
-          }
-        } else {
-          uint32_t d[4][2];
+        for (int j = j0; j < j0 + kJ; ++j)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            d[q][0] = pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]);
-            d[q][1] = pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+            const f32x16_t& c = acc[i][j];
+            if (OUT32)
+              *reinterpret_cast<lds_wv4u*>(uintptr_t(wr + (((2 * q + h) ^ sw) * 16))) = __builtin_bit_cast(
+                  v4u, f32x4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]});
+            else
+              *reinterpret_cast<lds_wu64*>(uintptr_t(wr + (((4 * (j - j0) + q) ^ sw) * 16) + 8 * h)) =
+                  uint64_t(pack_bf16x2(c[4 * q], c[4 * q + 1])) |
+                  (uint64_t(pack_bf16x2(c[4 * q + 2], c[4 * q + 3])) << 32);
           }
+        asm volatile("" ::: "memory");  // the wave's LDS operations run in order
 #pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            const int col = col0 + 32 * j + 8 * (q + h);
-            buf_st16<kCpolPlain>(ro, col < p.n ? at + col * 2 : kPastRange,
-                                 join_halves(d[q][0], d[q][1], d[q + 1][0], d[q + 1][1]));
-          }
+        for (int x = 0; x < 4; ++x) {
+          const int row = (wm * IB + i) * 32 + 8 * x + rr;
+          const int chunk = (l & 7) ^ rsw ^ (x & 1);
+          const int col = n0 + wn * 128 + 32 * j0 + chunk * (16 / kSize);
+          const v4u v = *reinterpret_cast<lds_v4u*>(uintptr_t(area + uint32_t(8 * x + rr) * 128 + (l & 7) * 16));
+          const bool in = row < rows && col < p.n;
+          buf_st16<kCpolStream>(ro, in ? uint32_t(row) * uint32_t(p.ld_out) * kSize + col * kSize : kPastRange, v);
         }
+        asm volatile("" ::: "memory");
       }
-    }
     asm volatile("" ::: "memory");
   }
 };

@@ -276,10 +276,11 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
 // A workgroup's next tile: workgroups go to the eight XCDs in turn, and XCD x takes the x-th
 // eighth of the tiles, whose operands its L2 then holds; its workgroups take them in turn.
 template <bool A8, bool OUT32, int SG>
-__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int nt) {
+__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt) {
   constexpr int TM = mx4::tile_rows<A8>();
   Tiling<TM> til;
   til.init(p);
+  til.total = min(til.total, max_mt);  // more only where ranges overlap
   const int total = til.total * nt, per = (total + 7) / 8;
   const int first = int(blockIdx.x & 7) * per, end = min(first + per, total);
   int t = first + int(blockIdx.x >> 3);
@@ -333,7 +334,7 @@ mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
     // at most this many m-tiles: every expert may end inside one
     const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
     const dim3 grid(unsigned(std::min<int64_t>((mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, nt); };
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, int(mt), nt); };
     auto sg = [&](auto g) {
       constexpr int SG = decltype(g)::value;
       if (a.a8) {
