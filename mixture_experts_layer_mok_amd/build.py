@@ -3,7 +3,8 @@
     python -m mixture_experts_layer_mok_amd.build [--jobs N]
 
 Every .hip file under csrc/ is compiled to an object (in parallel), then linked into
-mixture_experts_layer_mok_amd/libmok.so.  All device code is built with packed-FP32
+mixture_experts_layer_mok_amd/libmok.so; csrc/fast_calls.cpp is compiled by the host
+compiler to the extension module _fast.so.  All device code is built with packed-FP32
 instructions disabled (the compiler would otherwise form v_pk_* fp32 ops on its own).
 """
 from __future__ import annotations
@@ -19,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 OUT = os.path.join(HERE, "libmok.so")
+FAST = os.path.join(HERE, "_fast.so")
 BUILD = os.path.join(ROOT, "_build")
 
 ARCH = "gfx950"
@@ -52,12 +54,35 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_fast() -> None:
+    """The extension module of ops.py's ordinary calls, against torch's headers and libraries
+    (found at run time as the ones the importing process has loaded)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    include = [d for p in [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+               for d in ("-I", p)]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include,
+           os.path.join(CSRC, "fast_calls.cpp"), "-o", FAST + ".tmp", "-L", libs, "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fast_calls.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(FAST + ".tmp", FAST)
+
+
 def build(jobs: int | None = None, verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    jobs = jobs or min(len(srcs), os.cpu_count() or 4, 8)
+    jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4, 8)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        fast = ex.submit(_build_fast)
         objs = list(ex.map(_compile, srcs))
+        fast.result()
     tmp = OUT + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

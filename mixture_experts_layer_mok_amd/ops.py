@@ -10,6 +10,10 @@ are not the layer's own:
     d_rows, d_weights = unpermute_backward(dy, rows, pos, weights, d_rows)
     dx = permute_backward(d_rows, pos)
 
+Ordinary calls run through the extension module _fast (the same checks and the same C entry
+point in native code); what it does not take runs through the code here, which has the
+messages.
+
 Every function checks its tensors (ValueError), makes one call of the C entry point of the
 same name (MokError for what that refuses) on the tensors' device and returns without
 synchronising.  Value tensors are bf16, fp16 or fp32 matrices whose rows are contiguous;
@@ -19,12 +23,15 @@ passed in; those allocated here belong to the stream the work runs on.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib as L
 
 _TYPES = {torch.bfloat16: L.MOK_TYPE_BF16, torch.float16: L.MOK_TYPE_FP16,
           torch.float32: L.MOK_TYPE_FP32}
+_MAX = 2**31 - 1  # sizes that the entry points take as 32 bits
 
 
 # Every check here runs on every call, so the ones that pass do little: messages are made only
@@ -45,6 +52,8 @@ def _matrix(name, t, rows=-1, cols=-1, dtype=None, write=False) -> tuple:
     if (rows >= 0 and r != rows) or (cols >= 0 and c != cols):
         raise ValueError(f"{name}: {rows if rows >= 0 else 'any'} x {cols if cols >= 0 else 'any'} "
                          f"is wanted, not {r} x {c}")
+    if c > _MAX:
+        raise ValueError(f"{name}: a row has at most {_MAX} elements")
     ld, step = t.stride()
     if step != 1 and c > 1:
         raise ValueError(f"{name}: rows must be contiguous")
@@ -123,9 +132,27 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _call(fn: str, *args) -> None:
-    code = getattr(L.load(), fn)(*args)
+    lib = L.load()
+    if _fast is None:
+        _bind(lib)
+    code = getattr(lib, fn)(*args)
     if code:
         raise L.MokError(fn, code)
+
+
+_fast = None  # the extension module, from the first call on
+
+
+def _bind(lib) -> None:
+    """Gives the extension module the library's entry points."""
+    global _fast
+    from . import _fast as module
+
+    names = ("mok_permute", "mok_permute_bwd", "mok_unpermute", "mok_unpermute_bwd",
+             "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4")
+    module.bind(torch._C._cuda_getDevice, _raw_stream,
+                *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    _fast = module
 
 
 def _pos(pos) -> tuple:
@@ -133,6 +160,8 @@ def _pos(pos) -> tuple:
             not pos.is_contiguous():
         raise ValueError("pos: a contiguous int32 matrix [tokens, top_k] is wanted")
     T, k = pos.shape
+    if k > _MAX:
+        raise ValueError(f"pos: a row has at most {_MAX} elements")
     p = pos.data_ptr()
     return T, k, p, p + 4 * T * k
 
@@ -140,6 +169,10 @@ def _pos(pos) -> tuple:
 def permute(x, pos, out, stream=None):
     """out[pos[t, j]] = x[t] for every pair with 0 <= pos < len(out); the other rows of out
     stay as they are.  x [T, D], pos [T, k] int32, out [max_rows, D]; returns out."""
+    if stream is None and _fast is not None:
+        done = _fast.permute(x, pos, out)
+        if done is not None:
+            return done
     T, k, pp, pe = _pos(pos)
     ty = _type("x", x)
     px, ld_x, xe = _matrix("x", x, T)
@@ -180,12 +213,20 @@ def _sum_rows(fn, rows, pos, weights, out, stream):
 
 def permute_backward(d_rows, pos, out=None, stream=None):
     """Gradient of permute with respect to x: out[t] = sum over j of d_rows[pos[t, j]]."""
+    if stream is None and _fast is not None:
+        done = _fast.permute_backward(d_rows, pos, out)
+        if done is not None:
+            return done
     return _sum_rows("mok_permute_bwd", d_rows, pos, None, out, stream)
 
 
 def unpermute(rows, pos, weights, out=None, stream=None):
     """out[t] = sum over j, ascending, of weights[t, j] * rows[pos[t, j]]; pairs whose pos is
     outside [0, len(rows)) are skipped.  rows [max_rows, D], weights [T, k] float32."""
+    if stream is None and _fast is not None:
+        done = _fast.unpermute(rows, pos, weights, out)
+        if done is not None:
+            return done
     if weights is None:
         raise ValueError("weights: a contiguous float32 tensor [tokens, top_k] is wanted")
     return _sum_rows("mok_unpermute", rows, pos, weights, out, stream)
@@ -195,6 +236,10 @@ def unpermute_backward(dy, rows, pos, weights, d_rows, d_weights=None, stream=No
     """Gradients of unpermute: d_rows[pos[t, j]] = weights[t, j] * dy[t] (other rows of d_rows
     stay as they are) and d_weights[t, j] = <dy[t], rows[pos[t, j]]> (0 for pairs without a
     row).  Returns (d_rows, d_weights)."""
+    if stream is None and _fast is not None:
+        done = _fast.unpermute_backward(dy, rows, pos, weights, d_rows, d_weights)
+        if done is not None:
+            return done
     T, k, pp, pe = _pos(pos)
     ty = _type("rows", rows)
     pr, ld_r, re = _matrix("rows", rows)
@@ -232,6 +277,10 @@ def _rows_of(name, t, cols, rows=-1, dtype=None, write=False) -> tuple:
 def quantize_mx4(src, codes=None, scales=None, stream=None):
     """MXFP4 codes [..., K / 2] and scales [..., K / 32] (uint8) of src [..., K], in blocks of
     32 along its last axis.  Returns (codes, scales)."""
+    if stream is None and _fast is not None:
+        done = _fast.quantize_mx4(src, codes, scales)
+        if done is not None:
+            return done
     ty = _type("src", src)
     K = src.shape[-1] if src.dim() else 0
     if K == 0 or K % 32:
@@ -256,6 +305,10 @@ def quantize_mx4(src, codes=None, scales=None, stream=None):
 def dequantize_mx4(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values of MXFP4 codes [..., K / 2] and scales [..., K / 32], [..., K] in `dtype` (or
     in out's)."""
+    if stream is None and out is not None and _fast is not None:
+        done = _fast.dequantize_mx4(codes, scales, out)
+        if done is not None:
+            return done
     if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or codes.shape[-1] % 16 or \
             codes.shape[-1] == 0:
         raise ValueError("codes: a tensor with a last axis that is a multiple of 16 is wanted")
@@ -285,9 +338,15 @@ def grouped_mx4(a, a_scales, offsets, b, b_scales, out=None, dtype=torch.bfloat1
     (mok_quantize_mx), uint8, with a_scales [max_rows, K / 32]; offsets [E + 1] int32, on the
     device; b [E, N, K / 2] MXFP4 codes with b_scales [E, N, K / 32], contiguous; out
     [max_rows, N] bf16 or fp32."""
+    if stream is None and out is not None and _fast is not None:
+        done = _fast.grouped_mx4(a, a_scales, offsets, b, b_scales, out)
+        if done is not None:
+            return done
     if not isinstance(b, torch.Tensor) or b.dim() != 3 or b.shape[2] % 16 or b.shape[2] == 0:
         raise ValueError("b: a tensor [E, N, K / 2] with K a multiple of 32 is wanted")
     E, N, half = b.shape
+    if E > _MAX or N > _MAX:
+        raise ValueError(f"b: at most {_MAX} experts and columns")
     K = 2 * half
     pb, be = _flat("b", b, (E, N, half), torch.uint8)
     pq, qe = _flat("b_scales", b_scales, (E, N, K // 32), torch.uint8)

@@ -289,3 +289,22 @@ def test_mx4_functions_refuse():
         ops.dequantize_mx4(_t(4, 32, dtype=u8), _t(4, 2, dtype=u8))
     with pytest.raises(ValueError):
         ops.dequantize_mx4(_t(4, 32, dtype=u8), _t(4, 1, dtype=u8))
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Rows, slots and experts that the C ABI's 32-bit sizes would cut (tensors without memory)."""
+    big = 2**32 + 64
+    e = torch.empty(0, big)
+    pos = torch.empty(0, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="at most"):
+        ops.permute(e, pos, torch.empty(0, big))
+    with pytest.raises(ValueError, match="at most"):
+        ops.unpermute(e, pos, torch.empty(0, 2))
+    with pytest.raises(ValueError, match="at most"):
+        ops.permute(torch.empty(0, 64), torch.empty(0, big, dtype=torch.int32), torch.empty(0, 64))
+    with pytest.raises(ValueError, match="at most"):
+        ops.quantize_mx4(e)
+    u8 = dict(dtype=torch.uint8)
+    with pytest.raises(ValueError, match="at most"):
+        ops.grouped_mx4(torch.empty(0, 32, **u8), torch.empty(0, 2, **u8), torch.empty(1, dtype=torch.int32),
+                        torch.empty(0, big, 32, **u8), torch.empty(0, big, 2, **u8))
