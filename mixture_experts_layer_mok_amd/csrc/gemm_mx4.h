@@ -16,9 +16,9 @@
 // the four blocks 4 h .. 4 h + 3 over the step's four slices, whose scales are one dword of
 // the row, its byte s selected by the instruction.
 //
-// Scales: a ring of eight steps (64 bytes a row) in LDS, refilled four steps at a time once
-// every wave has read the four (32 bytes a row, so that a cache line is not fetched for a
-// few bytes each step), by direct-to-LDS loads too where their alignment allows it.
+// Scales: a ring of eight steps (64 bytes a row) in LDS, refilled four steps at a time (32
+// bytes a row, so that a cache line is not fetched for a few bytes each step) once every wave
+// has read the four, by direct-to-LDS loads too where their alignment allows it.
 //
 // LDS data rows: 128 bytes hold 8 chunks of 16, chunk c of row r at c ^ (r & 7) ^ ((r >> 3)
 // & 1); 256 bytes hold 16, at c ^ (r & 15): the 16 rows that one pass of a 16-byte read
@@ -50,9 +50,12 @@ constexpr int tile_rows() { return A8 ? 128 : 256; }
 
 static __shared__ __align__(1024) v4u g_a[2 * kStageB / 16];
 static __shared__ __align__(1024) v4u g_b[2 * kStageB / 16];
-// Scales: two dwords a row and step.  With 16-byte loads piece q (of the ring's four, two
-// steps each) of row r lies at 16-byte place q * rows + r; otherwise dword d (of sixteen) of
-// row r at dword place d * rows + r.
+// Scales: two dwords a row and step.  With 16-byte loads the two pieces (two steps each) of the
+// 32 bytes that a row has in half a ring are fetched by two lanes of one load, so that it
+// touches 32 lines and not 64; piece q of row r lies at 16-byte place
+//   half * 2 rows + 2 (r & ~7) + (r & 7) + 8 (q ^ ((r >> 3) & 1)),
+// where reading one dword of 32 rows meets each bank twice.  Otherwise dword d (of sixteen) of
+// row r lies at dword place d * rows + r.
 static __shared__ __align__(1024) uint32_t g_sa[2 * kRing * 256];
 static __shared__ __align__(1024) uint32_t g_sb[2 * kRing * 256];
 
@@ -111,11 +114,12 @@ __device__ __forceinline__ void lds_load4(const i32x4_t& rsrc, uint32_t voff, ui
 template <bool A8, int SG>
 struct Source {
   static constexpr int kTM = tile_rows<A8>();
+  static constexpr int kSA = kTM / 128;  // 16-byte loads of A's scales a wave
   i32x4_t ra, rb;            // codes of A from the tile's first row, of the expert's B
   i32x4_t rsa, rsb;          // their scales
   uint32_t oa[8], ob[8];     // byte offsets of this lane's chunks in step 0
   const uint8_t *psa, *psb;  // the scales' addresses (SG 1)
-  uint32_t osa, osb;         // this thread's scale rows
+  uint32_t osa[2], osb[2];   // the scales this thread fetches (SG 16: of kSA and 2 rows; else [0])
   int nblk;                  // K blocks
   int ca, cb;                // this lane's chunk of an A and of a B row
 
@@ -138,8 +142,18 @@ struct Source {
     psb = p.bs + int64_t(e) * p.n * nblk;
     rsa = rsrc_2g(psa);
     rsb = rsrc_2g(psb);
-    osa = t < kTM ? uint32_t(min(t, rows - 1) * p.ld_as) : kPastRange;
-    osb = uint32_t(min(n0 + t, p.n - 1)) * uint32_t(nblk);
+    if (SG == 16) {
+      const int row = 8 * (l >> 4) + (l & 7);
+      const uint32_t piece = 16u * (((l >> 3) ^ (l >> 4)) & 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        osa[i] = i < kSA ? uint32_t(min((w * kSA + i) * 32 + row, rows - 1) * p.ld_as) + piece : kPastRange;
+        osb[i] = uint32_t(min(n0 + w * 64 + i * 32 + row, p.n - 1)) * uint32_t(nblk) + piece;
+      }
+    } else {
+      osa[0] = t < kTM ? uint32_t(min(t, rows - 1) * p.ld_as) : kPastRange;
+      osb[0] = uint32_t(min(n0 + t, p.n - 1)) * uint32_t(nblk);
+    }
   }
 
   // Load q (0..7 A, 8..15 B) of step ks into the stage at byte `stage` of the rings.  A step
@@ -157,36 +171,35 @@ struct Source {
     }
   }
 
-  // Scales of steps 4 quad .. 4 quad + 3 (32 bytes a row) into their half of the ring; each
-  // wave moves those of 64 rows of A and of B.
-  __device__ __forceinline__ void issue_scales(int quad) const {
-    const int t = threadIdx.x, w = __builtin_amdgcn_readfirstlane(t >> 6);
+  // Part 0..3 of the scales of steps 4 quad .. 4 quad + 3 (32 bytes a row) into their half of the
+  // ring; each wave moves those of a quarter of the rows.
+  __device__ __forceinline__ void issue_scales(int quad, int part) const {
+    const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int at = quad * 32, half = quad & 1;
     if (SG == 16) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t past = at + 16 * i < nblk ? 0u : kPastRange;
-        if (w * 64 < kTM)
-          lds_load16(rsa, (osa + at + 16 * i) | past, 0,
-                          lds_addr(g_sa) + uint32_t((half * 2 + i) * kTM + w * 64) * 16);
-        lds_load16(rsb, (osb + at + 16 * i) | past, 0,
-                        lds_addr(g_sb) + uint32_t((half * 2 + i) * 256 + w * 64) * 16);
-      }
+      const uint32_t past = at + 16 * (((l >> 3) ^ (l >> 4)) & 1) < nblk ? 0u : kPastRange;
+      const int i = part & 1;
+      if (part >= 2)
+        lds_load16(rsb, (i ? osb[1] : osb[0]) | past, uint32_t(at),
+                   lds_addr(g_sb) + uint32_t(half * 512 + (2 * w + i) * 64) * 16);
+      else if (i < kSA)
+        lds_load16(rsa, (i ? osa[1] : osa[0]) | past, uint32_t(at),
+                   lds_addr(g_sa) + uint32_t(half * 2 * kTM + (kSA * w + i) * 64) * 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int have = nblk - at - 4 * i;
+      for (int x = 0; x < 2; ++x) {
+        const int i = 2 * part + x, have = nblk - at - 4 * i;
         if (SG == 4) {
           const uint32_t past = have > 0 ? 0u : kPastRange;
           if (w * 64 < kTM)
-            lds_load4(rsa, (osa + at + 4 * i) | past,
-                    lds_addr(g_sa) + uint32_t((half * 8 + i) * kTM + w * 64) * 4);
-          lds_load4(rsb, (osb + at + 4 * i) | past,
-                  lds_addr(g_sb) + uint32_t((half * 8 + i) * 256 + w * 64) * 4);
+            lds_load4(rsa, (osa[0] + at + 4 * i) | past,
+                      lds_addr(g_sa) + uint32_t((half * 8 + i) * kTM + w * 64) * 4);
+          lds_load4(rsb, (osb[0] + at + 4 * i) | past,
+                    lds_addr(g_sb) + uint32_t((half * 8 + i) * 256 + w * 64) * 4);
         } else {
           if (w * 64 < kTM)
-            g_sa[(half * 8 + i) * kTM + t] = scale_bytes4(row_rsrc(psa, kPastRange), osa + at + 4 * i, have);
-          g_sb[(half * 8 + i) * 256 + t] = scale_bytes4(row_rsrc(psb, kPastRange), osb + at + 4 * i, have);
+            g_sa[(half * 8 + i) * kTM + t] = scale_bytes4(row_rsrc(psa, kPastRange), osa[0] + at + 4 * i, have);
+          g_sb[(half * 8 + i) * 256 + t] = scale_bytes4(row_rsrc(psb, kPastRange), osb[0] + at + 4 * i, have);
         }
       }
     }
@@ -214,7 +227,8 @@ struct Source {
   static constexpr int kAhead = 16;
   __device__ __forceinline__ void begin() const {
     asm volatile("" ::: "memory");
-    issue_scales(0);
+#pragma unroll
+    for (int part = 0; part < 4; ++part) issue_scales(0, part);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -277,12 +291,14 @@ struct Tile {
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
     const int d = 2 * (ks & (kRing - 1)) + h;  // dword of the ring
     const int ra_ = wm * 32 * IB + r, rb_ = wn * 128 + r;
+    // (a block of 32 rows is 64 places on)
+    const int place = 2 * (r & ~7) + (r & 7) + 8 * (((d >> 2) ^ (r >> 3)) & 1);
+    const int wa = 4 * ((d >> 3) * 2 * kTM + wm * 64 * IB + place) + (d & 3);
+    const int wb = 4 * ((d >> 3) * 512 + wn * 256 + place) + (d & 3);
 #pragma unroll
-    for (int i = 0; i < IB; ++i)
-      s.a[i] = SG == 16 ? g_sa[((d >> 2) * kTM + ra_ + 32 * i) * 4 + (d & 3)] : g_sa[d * kTM + ra_ + 32 * i];
+    for (int i = 0; i < IB; ++i) s.a[i] = SG == 16 ? g_sa[wa + 256 * i] : g_sa[d * kTM + ra_ + 32 * i];
 #pragma unroll
-    for (int j = 0; j < kJB; ++j)
-      s.b[j] = SG == 16 ? g_sb[((d >> 2) * 256 + rb_ + 32 * j) * 4 + (d & 3)] : g_sb[d * 256 + rb_ + 32 * j];
+    for (int j = 0; j < kJB; ++j) s.b[j] = SG == 16 ? g_sb[wb + 256 * j] : g_sb[d * 256 + rb_ + 32 * j];
   }
 
   __device__ __forceinline__ i32x8_t read_a(int s, int i, uint32_t stage) const {
@@ -369,10 +385,15 @@ struct Tile {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       const uint32_t nxt = cur ^ kStageB;
-      // The scales of the next four steps into the half of the ring that all have read (for step
-      // 0 the half that the last tile's results went through).
-      if ((ks & 3) == 3) src.issue_scales(ks / 4 + 2);
-      if (ks == 0) src.issue_scales(1);
+      // A quarter of the scales of four steps each step, from the one on that finds their half of
+      // the ring read by all (of step 0 the half that the last tile's results went through).
+      if (!A8) {
+        if (ks == 0) src.issue_scales(1, 0);
+        src.issue_scales((ks + 1) / 4 + 1, (ks + 1) & 3);
+      } else if ((ks & 3) == 3 || ks == 0) {
+#pragma unroll
+        for (int part = 0; part < 4; ++part) src.issue_scales(ks == 0 ? 1 : ks / 4 + 2, part);
+      }
       read_scales(sn, ks + 1);
       slice<1, 0, 0, kD1>(src, f[1], f[0], sc, nxt, ks, cur);
       slice<2, 1, kD1, kD2>(src, f[2], f[1], sc, nxt, ks, cur);
