@@ -161,9 +161,12 @@ def values(codes, scales, fmt):
     return f(codes.cpu().numpy(), scales.cpu().numpy())
 
 
-def check_product(got, want, s, K, what):
+def scales8(fmt, sa, sb):
+    return None if fmt == "e2m1" else (sa.cpu().numpy(), sb.cpu().numpy())
+
+
+def check_product(got, want, e, what):
     got = f64(got)
-    e = K * 2.0**-23 * s
     u = 2.0**-8 if what == torch.bfloat16 else 2.0**-24
     np.testing.assert_array_equal(np.isnan(got), np.isnan(want))
     ok = np.isnan(want) | (np.abs(got - want) <= e + u * (np.abs(want) + e) + 2.0**-133)
@@ -189,8 +192,9 @@ def run_product(counts, N, K, fmt, dtype, seed, slack=3, first=0, pad=0):
     out = full[:, :N]
     got = ops.grouped_mx4(a, sa, torch.from_numpy(off).to(DEV), b, sb, out=out)
     assert got is out
-    want, s = O.grouped(values(a, sa, fmt), off, values(b, sb, "e2m1"), np.full((n, N), -7.0))
-    check_product(out, want, s, K, dtype)
+    want, e = O.grouped(values(a, sa, fmt), off, values(b, sb, "e2m1"), np.full((n, N), -7.0),
+                        scales8(fmt, sa, sb))
+    check_product(out, want, e, dtype)
     assert (full[:, N:] == -7).all()
     return out
 
@@ -222,10 +226,77 @@ def test_product_many_rows(counts, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("K", [64, 512, 544, 640])  # scales by single bytes, 16 and 4 bytes
+@pytest.mark.parametrize("E,N", [(16, 2048), (16, 2040), (8, 2048), (8, 2056), (3, 40)])
+def test_product_few_rows_of_many_columns(E, N, K, fmt):
+    """64, 32 and 16 columns a workgroup, whole and cut; an expert with several passes of rows
+    among experts with a few or none."""
+    say(f"[mx4] product few rows E={E} N={N} K={K} {fmt}")
+    counts = np.random.default_rng(E + N + K).integers(0, 5, E)
+    counts[1], counts[E - 1] = 0, 75
+    run_product(list(counts), N, K, fmt, torch.bfloat16, seed=N + K + 3)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("K", [4096, 4128, 8448])  # one chunk a wave and more
+def test_product_long_rows(K, fmt):
+    say(f"[mx4] product long rows K={K} {fmt}")
+    run_product([3, 0, 21, 40], 72, K, fmt, torch.float32, seed=K)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("N,K", [(5128, 288), (4096, 1024), (4360, 2432)])
+def test_product_several_tiles_a_workgroup(N, K, dtype, fmt):
+    """More tiles than the GPU has workgroups for, of 1 to 256 rows, one after the other."""
+    say(f"[mx4] product tiles N={N} K={K} {dtype} {fmt}")
+    run_product([700, 3, 0, 129, 65, 1000, 257, 12], N, K, fmt, dtype, seed=N + K + 4, pad=K == 288)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_product_tiles_of_many_groups(fmt):
+    counts = np.random.default_rng(23).integers(0, 40, 130)
+    counts[[0, 63, 64, 127]] = 0
+    counts[65], counts[129] = 300, 260
+    run_product(list(counts), 520, 96, fmt, torch.bfloat16, 24)
+    run_product([0] * 1000 + [3] + [0] * 22 + [30], 264, 64, fmt, torch.float32, 25)
+
+
+@pytest.mark.parametrize("fmt", FMT)
 def test_product_strides_and_first_row(fmt):
     say(f"[mx4] product strides {fmt}")
     run_product([20, 0, 13], 48, 352, fmt, torch.bfloat16, 5, first=4, pad=3)
     run_product([300, 290], 272, 352, fmt, torch.float32, 6, first=2, pad=5)
+
+
+@pytest.mark.parametrize("rows", [1, 200])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_product_of_eight_bits_cuts_small_products(rows, sign):
+    """Eight neighbours' products are cut, toward zero, to 2^-13 of the largest exponent: beside
+    256 * 4 = 2^10 a product keeps its multiples of 2^-3.  Beside products of other eights, and
+    with 4-bit rows, nothing is cut."""
+    K = 128
+    small = [0.0625, 0.125, 0.1875, 0.234375]
+    b = torch.zeros(8, K)
+    b[:, 0] = 4.0
+    for j in range(4):  # column j: the neighbour small[j]; column 4 + j: one of the next eight
+        b[j, 1 + j] = b[4 + j, 8 + j] = sign
+    a = torch.zeros(rows, K)
+    a[:, 0] = 256.0
+    a[:, 1:5] = a[:, 8:12] = torch.tensor(small)
+    off = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    ones = torch.full((max(rows, 8), K // 32), 127, dtype=torch.uint8, device=DEV)
+    bc, bs = ops.quantize_mx4(b.to(DEV))
+    ac = a.to(DEV).to(torch.float8_e4m3fn).view(torch.uint8)
+    out = ops.grouped_mx4(ac, ones[:rows], off, bc.view(1, 8, -1), bs.view(1, 8, -1), dtype=torch.float32)
+    want = [1024 + sign * v for v in (0.0, 0.125, 0.125, 0.125, *small)]
+    assert out[rows - 1].tolist() == want and out[0].tolist() == want
+    a4 = torch.zeros(rows, K)
+    a4[:, 0] = 6.0
+    a4[:, 1:5] = a4[:, 8:12] = 0.5
+    a4, s4 = ops.quantize_mx4(a4.to(DEV))
+    out = ops.grouped_mx4(a4, s4, off, bc.view(1, 8, -1), bs.view(1, 8, -1), dtype=torch.float32)
+    assert (out == 24 + sign * 0.5).all()
 
 
 @pytest.mark.parametrize("fmt", FMT)
@@ -252,9 +323,9 @@ def test_product_offsets_cut_to_the_rows(fmt, big):
                         sb.view(4, N, -1), out=out)
         if off == [-2**31, -1, 7, 5, 2**31 - 1]:
             continue  # rows 5 and 6 are in two ranges: either result, but no fault
-        want, s = O.grouped(values(a, sa, fmt), off, values(b.view(4, N, -1), sb.view(4, N, -1), "e2m1"),
-                            np.full((n, N), -7.0))
-        check_product(out, want, s, K, torch.float32)
+        want, e = O.grouped(values(a, sa, fmt), off, values(b.view(4, N, -1), sb.view(4, N, -1), "e2m1"),
+                            np.full((n, N), -7.0), scales8(fmt, sa, sb.view(4, N, -1)))
+        check_product(out, want, e, torch.float32)
 
 
 @pytest.mark.parametrize("fmt", FMT)
@@ -273,9 +344,9 @@ def test_product_nan_scales(fmt, counts, N, K):
     off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     out = torch.full((n, N), -7.0, device=DEV)
     ops.grouped_mx4(a, sa, torch.from_numpy(off).to(DEV), b.view(E, N, -1), sb.view(E, N, -1), out=out)
-    want, s = O.grouped(values(a, sa, fmt), off, values(b.view(E, N, -1), sb.view(E, N, -1), "e2m1"),
-                        np.full((n, N), -7.0))
-    check_product(out, want, np.nan_to_num(s), K, torch.float32)
+    want, e = O.grouped(values(a, sa, fmt), off, values(b.view(E, N, -1), sb.view(E, N, -1), "e2m1"),
+                        np.full((n, N), -7.0), scales8(fmt, sa, sb.view(E, N, -1)))
+    check_product(out, want, np.nan_to_num(e), torch.float32)
     assert 0 < np.isnan(want).sum() < want.size
 
 
@@ -367,18 +438,19 @@ def test_experts_of_four_bits(T, fmt):
             return ops.quantize_mx4(r)
         return layer.quantize_weights(r.to(torch.bfloat16))
 
-    def check(codes, scales, q, out, K):
-        want, s = O.grouped(values(codes, scales, fmt), off, values(*q, "e2m1"), np.zeros(out.shape))
-        check_product(out[:R], want[:R], s[:R], K, out.dtype)
+    def check(codes, scales, q, out):
+        want, e = O.grouped(values(codes, scales, fmt), off, values(*q, "e2m1"), np.zeros(out.shape),
+                            scales8(fmt, scales, q[1]))
+        check_product(out[:R], want[:R], e[:R], out.dtype)
 
     rows = layer.permute(x, torch.zeros(n, D, dtype=torch.bfloat16, device=DEV))
     a, sa = rows_mx(rows)
     h = layer.grouped_mx4(a, sa, *q1, out=torch.zeros(n, 2 * I, device=DEV))
-    check(a, sa, q1, h, D)
+    check(a, sa, q1, h)
     h = torch.nn.functional.silu(h[:, :I]) * h[:, I:]
     a, sa = rows_mx(h)
     o = layer.grouped_mx4(a, sa, *q2)
-    check(a, sa, q2, o, I)
+    check(a, sa, q2, o)
     y = layer.unpermute(o, g)
     o0 = f64(o)
     o0[R:] = 0
