@@ -296,8 +296,8 @@ mok_status_t mok_moe_fwd_noalloc(const mok_desc_t* desc, const void* x, const in
  *
  * Common rules.  `type` is the element type of every row operand (MOK_TYPE_*); sums run
  * in fp32 and are rounded once.  A row operand is `ld` elements from row to row; cols a
- * multiple of 8, 8..65536; ld a multiple of 8, at least cols (a read operand may also have
- * ld 0: every row the same); bases 16-byte aligned.  tokens 0..2^24, top_k 1..64,
+ * multiple of 8, 8..65536; ld a multiple of 8, at least cols and at most 2^30 (a read
+ * operand may also have ld 0: every row the same); bases 16-byte aligned.  tokens 0..2^24, top_k 1..64,
  * tokens*top_k at most 2^24.  topk_w, d_topk_w: [T, k] fp32.  A pair whose pos lies
  * outside [0, max_rows) has no row and is skipped, its weight unread; rows without a pair
  * are neither read nor written, so max_rows may exceed the routed rows (their number
@@ -352,7 +352,7 @@ mok_status_t mok_unpermute_bwd(int32_t type, const void* dy, int64_t ld_y, const
  * (a multiple of 32, 32..65536) takes cols / 2 bytes, its scales cols / 32 bytes.
  * ld_codes and ld_scales are bytes from row to row: ld_codes >= cols / 2, a multiple of
  * 16; ld_scales >= cols / 32.  Bases of codes and of src / dst 16-byte aligned; ld_src,
- * ld_dst in elements, multiples of 8, at least cols.  rows 0..2^31-1 (0: nothing is
+ * ld_dst in elements, multiples of 8, at least cols; every ld at most 2^30.  rows 0..2^31-1 (0: nothing is
  * done).  Bytes between rows are left as they are. */
 
 /* The rule of mok_quantize_mx with e2m1's largest value: the shared exponent is the

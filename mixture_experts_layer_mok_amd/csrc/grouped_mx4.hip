@@ -318,16 +318,21 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int m
 }  // namespace
 
 // Which kernel: the tiles, where they fill the GPU whatever the rows (a tile an expert and 256
-// columns at least) or where the experts have rows enough.  Measured on MI355X, weights from
-// HBM, rows kernel against tile kernel, us:
-//   128 tiles (8 experts, N 4096, K 7168, MXFP8 rows): 8 rows each 30 / 47, 32 rows 39 / 47,
-//     48 rows 63 / 48;
-//   16 tiles (1 expert, the same): 32 rows 12 / 31, 64 rows 23 / 32;
-//   224 tiles (8 experts, N 7168, K 2048, MXFP4 rows): 1 row 17 / 16, 32 rows 22 / 17;
-//   512 tiles (64 experts, N 2048, K 4096, MXFP8 rows): 4 rows 64 / 55, 32 rows 91 / 61.
+// columns at least) or where there are more rows than the other kernel takes in a few passes
+// should one expert have them all: how they are spread is known on the device only.  Measured
+// on MI355X, weights from HBM, rows kernel / tile kernel, us:
+//   128 tiles (8 experts, N 4096, K 7168, MXFP8 rows), even, a share p ~ 1 / rank^1.2, all in one:
+//     64 rows  30 / 45, 33 / 45, 34 / 31
+//     128 rows 32 / 45, 48 / 46, 65 / 38
+//     256 rows 40 / 46, 78 / 53, 128 / 39
+//   64 tiles (16 experts, N 1024, K 2048), the same: 64 rows 7 / 12, 8 / 12, 11 / 10;
+//     256 rows 8 / 12, 20 / 15, 37 / 14
+//   16 tiles (1 expert, N 4096, K 7168): 32 rows 12 / 31, 64 rows 22 / 31
+//   224 tiles (8 experts, N 7168, K 2048, MXFP4 rows): 1 row each 17 / 16, 32 rows 22 / 17
+//   512 tiles (64 experts, N 2048, K 4096, MXFP8 rows): 4 rows each 64 / 55, 32 rows 91 / 61
 static bool use_tiles(const GroupedArgs& a) {
   const int64_t tiles = (a.n + mx4::kTN - 1) / mx4::kTN * std::min<int64_t>(a.groups, a.max_rows);
-  return tiles >= 192 || a.max_rows > (tiles >= 64 ? 32 : 64) * int64_t(a.groups);
+  return tiles >= 192 || a.max_rows > std::min<int64_t>(128, 64 * int64_t(a.groups));
 }
 
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {

@@ -10,8 +10,8 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool type_ok(int32_t t) { return t == MOK_TYPE_BF16 || t == MOK_TYPE_FP16 || t == MOK_TYPE_FP32; }
 
-constexpr int64_t kMaxLd = int64_t(1) << 32;  // row strides whose products stay in 64 bits
-
+// Row strides, in elements of up to 4 bytes, whose products with 2^31 - 2 rows stay in 64 bits.
+constexpr int64_t kMaxLd = int64_t(1) << 30;
 constexpr int64_t kMaxLdOut = int64_t(1) << 21;  // the product's: 256 rows stay in 31-bit offsets
 
 // A value matrix's row stride in elements; a read operand may repeat one row (ld 0).

@@ -238,6 +238,16 @@ def test_product_few_rows_of_many_columns(E, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("rows", [64, 65, 128, 129])
+def test_product_around_the_choice_of_kernel(rows, fmt):
+    """One expert, and two of which one has every row, on both sides of the rows that the
+    few-rows kernel takes."""
+    say(f"[mx4] product choice {rows} {fmt}")
+    run_product([rows], 72, 608, fmt, torch.bfloat16, seed=rows, slack=0)
+    run_product([0, rows], 72, 608, fmt, torch.float32, seed=rows + 1, slack=0)
+
+
+@pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("K", [4096, 4128, 8448])  # one chunk a wave and more
 def test_product_long_rows(K, fmt):
     say(f"[mx4] product long rows K={K} {fmt}")

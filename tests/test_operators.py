@@ -113,7 +113,8 @@ def _rows_calls(type=0, ld_x=64, pos=FAKE, T=4, k=2, cols=64, ld_r=64, n=8, x=FA
     (dict(cols=0), L.MOK_E_SHAPE), (dict(cols=60), L.MOK_E_SHAPE),
     (dict(cols=65544, ld_x=65544, ld_r=65544), L.MOK_E_SHAPE), (dict(n=-1), L.MOK_E_SHAPE),
     (dict(n=1 << 31), L.MOK_E_SHAPE), (dict(ld_x=56), L.MOK_E_SHAPE), (dict(ld_r=68), L.MOK_E_SHAPE),
-    (dict(ld_r=-64), L.MOK_E_SHAPE), (dict(pos=None), L.MOK_E_NULL), (dict(x=None), L.MOK_E_NULL),
+    (dict(ld_r=-64), L.MOK_E_SHAPE), (dict(ld_x=2**30 + 8), L.MOK_E_SHAPE),
+    (dict(ld_r=2**30 + 8), L.MOK_E_SHAPE), (dict(pos=None), L.MOK_E_NULL), (dict(x=None), L.MOK_E_NULL),
     (dict(rows=None), L.MOK_E_NULL), (dict(x=FAKE + 8), L.MOK_E_SHAPE),
     (dict(rows=FAKE + 2), L.MOK_E_SHAPE), (dict(pos=FAKE + 1), L.MOK_E_SHAPE),
 ])
@@ -148,7 +149,8 @@ def test_empty_calls_do_nothing():
     (dict(type=7), L.MOK_E_UNSUPPORTED), (dict(cols=48), L.MOK_E_SHAPE), (dict(cols=0), L.MOK_E_SHAPE),
     (dict(cols=65568), L.MOK_E_SHAPE), (dict(rows=-1), L.MOK_E_SHAPE), (dict(ld=56), L.MOK_E_SHAPE),
     (dict(ld=0), L.MOK_E_SHAPE), (dict(ld=68), L.MOK_E_SHAPE), (dict(ldc=24), L.MOK_E_SHAPE),
-    (dict(ldc=40), L.MOK_E_SHAPE), (dict(lds=1), L.MOK_E_SHAPE), (dict(v=None), L.MOK_E_NULL),
+    (dict(ldc=40), L.MOK_E_SHAPE), (dict(ld=2**30 + 8), L.MOK_E_SHAPE),
+    (dict(ldc=2**30 + 16), L.MOK_E_SHAPE), (dict(lds=2**30 + 1), L.MOK_E_SHAPE), (dict(lds=1), L.MOK_E_SHAPE), (dict(v=None), L.MOK_E_NULL),
     (dict(c=None), L.MOK_E_NULL), (dict(s=None), L.MOK_E_NULL), (dict(v=FAKE + 4), L.MOK_E_SHAPE),
     (dict(c=FAKE + 8), L.MOK_E_SHAPE),
 ])
