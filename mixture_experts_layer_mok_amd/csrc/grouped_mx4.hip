@@ -16,7 +16,7 @@
 #include <type_traits>
 
 #include "device.h"
-#include "launch.h"
+#include "ops_launch.h"
 #include "gemm_mx4.h"
 
 namespace mok {

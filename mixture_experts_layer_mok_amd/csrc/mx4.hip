@@ -8,7 +8,7 @@
 #include <type_traits>
 
 #include "device.h"
-#include "launch.h"
+#include "ops_launch.h"
 #include "mx.h"
 
 namespace mok {

@@ -1,7 +1,7 @@
 // C ABI of the row operators and the MXFP4 operators: argument checks (all before any HIP
 // runtime call) and the launches.  Declarations and contracts: include/mok.h.
 #include "../../include/mok.h"
-#include "launch.h"
+#include "ops_launch.h"
 
 using namespace mok;
 

@@ -310,3 +310,19 @@ def test_sizes_past_32_bits_are_refused():
     with pytest.raises(ValueError, match="at most"):
         ops.grouped_mx4(torch.empty(0, 32, **u8), torch.empty(0, 2, **u8), torch.empty(1, dtype=torch.int32),
                         torch.empty(0, big, 32, **u8), torch.empty(0, big, 2, **u8))
+
+
+def test_the_layers_kernels_do_not_include_the_operators():
+    """Counter summaries of the layer's kernels hold while only the operators' files change."""
+    import os
+    import re
+
+    import bench
+
+    names = os.listdir(bench.CSRC)
+    assert set(bench.OPERATOR_SOURCES) <= set(names)
+    for name in names:
+        if name.endswith((".hip", ".h")) and name not in bench.OPERATOR_SOURCES:
+            with open(os.path.join(bench.CSRC, name)) as f:
+                included = re.findall(r'#include "([^"]+)"', f.read())
+            assert not set(included) & set(bench.OPERATOR_SOURCES), name
