@@ -386,7 +386,8 @@ mok_status_t mok_dequantize_mx4(const uint8_t* codes, int64_t ld_codes, const ui
  * B e2m1: codes [groups, n, k/2], scales [groups, n, k/32], contiguous.  out: ld_out
  * elements from row to row, a multiple of 8, at least n and at most 2^21.  A codes, B codes
  * and out 16-byte aligned.  A NaN scale makes the results it enters NaN.  Errors as for the row
- * operators; asynchronous on stream, one launch, no workspace, bitwise repeatable. */
+ * operators; asynchronous on stream, one launch (two where max_rows leaves open whether few
+ * rows are routed: one of them returns at once), no workspace, bitwise repeatable. */
 #define MOK_MX_E4M3 0
 #define MOK_MX_E2M1 1
 #define MOK_MX_MAX_LD ((int64_t)1 << 22)

@@ -32,6 +32,20 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64
   *hi = min(int64_t(offsets[e + 1]), max_rows);
 }
 
+// Whether the few-rows kernel has the call, where both are launched (the choice is explained at
+// launch_grouped_mx4): no expert of more than 64 rows, 256 rows in all.
+__device__ __forceinline__ bool few_rows(const GroupedArgs& p) {
+  const int64_t first = max(int64_t(p.offsets[0]), int64_t(0));
+  bool few = min(int64_t(p.offsets[p.groups]), p.max_rows) - first <= 256;
+  for (int e0 = 0; few && e0 < p.groups; e0 += 64) {
+    int64_t l = 0, h = 0;
+    const int e = e0 + int(threadIdx.x & 63);
+    if (e < p.groups) expert_rows(p.offsets, e, p.max_rows, &l, &h);
+    few = !__any(h - l > 64);
+  }
+  return few;
+}
+
 __device__ __forceinline__ f32x4_t mfma16(i32x8_t w, i32x8_t a, f32x4_t c, int sw, int sa, bool a8) {
   return a8 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 0, 0, sw, 0, sa)
             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 4, 0, sw, 0, sa);
@@ -180,8 +194,9 @@ __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part,
 }
 
 template <bool A8, int SG, int NB, int W>
-__global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p) {
+__global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, bool both) {
   __shared__ f32x4_t s_part[W * 2 * NB * 64];
+  if (both && !few_rows(p)) return;
   // the blockIdx.y-th expert that has rows
   const int lane = threadIdx.x & 63;
   int want = blockIdx.y, e = -1;
@@ -279,7 +294,8 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
 // A workgroup's next tile: workgroups go to the eight XCDs in turn, and XCD x takes the x-th
 // eighth of the tiles, whose operands its L2 then holds; its workgroups take them in turn.
 template <bool A8, bool OUT32, int SG>
-__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt) {
+__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt, bool both) {
+  if (both && few_rows(p)) return;
   constexpr int TM = mx4::tile_rows<A8>();
   Tiling<TM> til;
   til.init(p);
@@ -315,60 +331,43 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int m
   }
 }
 
-}  // namespace
-
-// Which kernel: the tiles, where they fill the GPU whatever the rows (a tile an expert and 256
-// columns at least) or where there are more rows than the other kernel takes in a few passes
-// should one expert have them all: how they are spread is known on the device only.  Measured
-// on MI355X, weights from HBM, rows kernel / tile kernel, us:
-//   128 tiles (8 experts, N 4096, K 7168, MXFP8 rows), even, a share p ~ 1 / rank^1.2, all in one:
-//     64 rows  30 / 45, 33 / 45, 34 / 31
-//     128 rows 32 / 45, 48 / 46, 65 / 38
-//     256 rows 40 / 46, 78 / 53, 128 / 39
-//   64 tiles (16 experts, N 1024, K 2048), the same: 64 rows 7 / 12, 8 / 12, 11 / 10;
-//     256 rows 8 / 12, 20 / 15, 37 / 14
-//   16 tiles (1 expert, N 4096, K 7168): 32 rows 12 / 31, 64 rows 22 / 31
-//   224 tiles (8 experts, N 7168, K 2048, MXFP4 rows): 1 row each 17 / 16, 32 rows 22 / 17
-//   512 tiles (64 experts, N 2048, K 4096, MXFP8 rows): 4 rows each 64 / 55, 32 rows 91 / 61
-static bool use_tiles(const GroupedArgs& a) {
-  const int64_t tiles = (a.n + mx4::kTN - 1) / mx4::kTN * std::min<int64_t>(a.groups, a.max_rows);
-  return tiles >= 192 || a.max_rows > std::min<int64_t>(128, 64 * int64_t(a.groups));
+int64_t scales_align(const GroupedArgs& a) {
+  return int64_t(reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) |
+                 uintptr_t(a.ld_as) | uintptr_t(a.k / 32));
 }
 
-mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
-  if (use_tiles(a)) {
-    const int tm = a.a8 ? mx4::tile_rows<true>() : mx4::tile_rows<false>();
-    const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
-    // at most this many m-tiles: every expert may end inside one
-    const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
-    const dim3 grid(unsigned(std::min<int64_t>((mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, int(mt), nt); };
-    auto sg = [&](auto g) {
-      constexpr int SG = decltype(g)::value;
-      if (a.a8) {
-        if (a.out32) go(k_grouped_tile<true, true, SG>);
-        else go(k_grouped_tile<true, false, SG>);
-      } else {
-        if (a.out32) go(k_grouped_tile<false, true, SG>);
-        else go(k_grouped_tile<false, false, SG>);
-      }
-    };
-    const int64_t align = int64_t(reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) |
-                                  uintptr_t(a.ld_as) | uintptr_t(a.k / 32));
-    if (align % 16 == 0) sg(std::integral_constant<int, 16>());
-    else if (align % 4 == 0) sg(std::integral_constant<int, 4>());
-    else sg(std::integral_constant<int, 1>());
-    return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
-  }
-  const int64_t align = int64_t(reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) |
-                                uintptr_t(a.ld_as) | uintptr_t(a.k / 32));
-  const int64_t experts = std::min<int64_t>(a.groups, a.max_rows);  // at most these have rows
+void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
+  const int tm = a.a8 ? mx4::tile_rows<true>() : mx4::tile_rows<false>();
+  // at most this many m-tiles: every expert may end inside one
+  const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
+  const dim3 grid(unsigned(std::min<int64_t>((mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, int(mt), nt, both); };
+  auto sg = [&](auto g) {
+    constexpr int SG = decltype(g)::value;
+    if (a.a8) {
+      if (a.out32) go(k_grouped_tile<true, true, SG>);
+      else go(k_grouped_tile<true, false, SG>);
+    } else {
+      if (a.out32) go(k_grouped_tile<false, true, SG>);
+      else go(k_grouped_tile<false, false, SG>);
+    }
+  };
+  const int64_t align = scales_align(a);
+  if (align % 16 == 0) sg(std::integral_constant<int, 16>());
+  else if (align % 4 == 0) sg(std::integral_constant<int, 4>());
+  else sg(std::integral_constant<int, 1>());
+}
+
+// Columns a workgroup: the most that leave 512 workgroups, two a CU (64 rows over 8 experts, N
+// 4096, K 7168 in MXFP8: 64 columns 32 us, 32 39, 16 42); eight waves instead of four where
+// they have chunks for two rounds and the workgroups are few.
+void launch_rows(const GroupedArgs& a, int64_t experts, bool both, hipStream_t st) {
   auto enough = [&](int cols) { return (a.n + cols - 1) / cols * experts >= 512; };
   const int nb = enough(64) ? 4 : enough(32) ? 2 : 1;
   const bool deep = nb == 1 && a.k >= 16 * kChunk;
   const dim3 grid(unsigned((a.n + 16 * nb - 1) / (16 * nb)), unsigned(experts));
   const dim3 block(deep ? 512 : 256);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a); };
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, both); };
   auto shape = [&](auto a8, auto g) {
     constexpr bool A8 = decltype(a8)::value;
     constexpr int SG = decltype(g)::value;
@@ -381,9 +380,36 @@ mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
     if (a.a8) shape(std::true_type(), g);
     else shape(std::false_type(), g);
   };
+  const int64_t align = scales_align(a);
   if (align % 8 == 0) format(std::integral_constant<int, 8>());
   else if (align % 4 == 0) format(std::integral_constant<int, 4>());
   else format(std::integral_constant<int, 1>());
+}
+
+}  // namespace
+
+// Which kernel.  The tiles, where they fill the GPU whatever the rows (a tile an expert and 256
+// columns at least), and where max_rows leaves little hope that few rows are routed.  The
+// few-rows kernel, where max_rows is few itself.  Between them the routed rows and their
+// spread decide, which the device knows: both are launched and one of them returns at once
+// (2.2 us more, for the 13 us of 64 even rows or the 100 us of 256 rows of one expert below).
+// Measured on MI355X, weights from HBM, rows kernel / tile kernel, us:
+//   128 tiles (8 experts, N 4096, K 7168, MXFP8 rows), even, a share p ~ 1 / rank^1.2, all in one:
+//     64 rows  30 / 45, 33 / 45, 34 / 31
+//     128 rows 32 / 45, 48 / 46, 65 / 38
+//     256 rows 40 / 46, 78 / 53, 128 / 39
+//   64 tiles (16 experts, N 1024, K 2048), the same: 64 rows 7 / 12, 8 / 12, 11 / 10;
+//     256 rows 8 / 12, 20 / 15, 37 / 14
+//   16 tiles (1 expert, N 4096, K 7168): 32 rows 12 / 31, 64 rows 22 / 31
+//   224 tiles (8 experts, N 7168, K 2048, MXFP4 rows): 1 row each 17 / 16, 32 rows 22 / 17
+//   512 tiles (64 experts, N 2048, K 4096, MXFP8 rows): 4 rows each 64 / 55, 32 rows 91 / 61
+mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
+  const int64_t experts = std::min<int64_t>(a.groups, a.max_rows);  // at most these have rows
+  const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
+  const bool tiles = nt * experts >= 192 || a.max_rows > 4096;
+  const bool rows = a.max_rows <= std::min<int64_t>(128, 64 * int64_t(a.groups));
+  if (tiles || !rows) launch_tiles(a, nt, !tiles, st);
+  if (!tiles) launch_rows(a, experts, !rows, st);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
 }
 

@@ -238,13 +238,23 @@ def test_product_few_rows_of_many_columns(E, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMT)
-@pytest.mark.parametrize("rows", [64, 65, 128, 129])
-def test_product_around_the_choice_of_kernel(rows, fmt):
-    """One expert, and two of which one has every row, on both sides of the rows that the
-    few-rows kernel takes."""
-    say(f"[mx4] product choice {rows} {fmt}")
-    run_product([rows], 72, 608, fmt, torch.bfloat16, seed=rows, slack=0)
-    run_product([0, rows], 72, 608, fmt, torch.float32, seed=rows + 1, slack=0)
+@pytest.mark.parametrize("counts", [
+    [64], [65], [128], [129], [0, 64], [0, 65], [64, 64], [64, 65], [64] * 4, [64] * 4 + [1], [63] * 4 + [4],
+    [1] * 70 + [65] + [1] * 5, [1] * 70 + [64] + [1] * 5])
+@pytest.mark.parametrize("slack", [0, 300])
+def test_product_around_the_choice_of_kernel(counts, slack, fmt):
+    """Both sides of the rows that the few-rows kernel takes, of one expert and in all, in
+    matrices with and without rows behind the last expert's."""
+    say(f"[mx4] product choice {counts} {slack} {fmt}")
+    run_product(counts, 72, 608, fmt, torch.bfloat16, seed=sum(counts), slack=slack)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_product_rows_of_a_capacity(fmt):
+    """No rows, one and a few in a matrix for thousands; more than 4096."""
+    for counts, slack in (([0, 0], 700), ([0, 1], 700), ([3, 5, 0, 2], 4086), ([3, 5, 0, 2], 4087),
+                          ([2000, 1500], 900)):
+        run_product(counts, 24, 96, fmt, torch.float32, seed=len(counts) + slack, slack=slack)
 
 
 @pytest.mark.parametrize("fmt", FMT)
