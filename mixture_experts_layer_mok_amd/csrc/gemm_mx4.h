@@ -18,7 +18,10 @@
 //
 // Scales: a ring of eight steps (64 bytes a row) in LDS, refilled four steps at a time (32
 // bytes a row, so that a cache line is not fetched for a few bytes each step) once every wave
-// has read the four, by direct-to-LDS loads too where their alignment allows it.
+// has read the four, by direct-to-LDS loads too.  These take dword addresses; where a row's
+// scales start inside a dword, the ring holds the dwords from that one on, and a reader
+// shifts two of them together (16,384 rows, N 4096, K 7200 in MXFP4 on MI355X: 516 us with the
+// scales brought in by bytes, 287 so; 250 for the whole pieces of K 7168).
 //
 // LDS data rows: 128 bytes hold 8 chunks of 16, chunk c of row r at c ^ (r & 7) ^ ((r >> 3)
 // & 1); 256 bytes hold 16, at c ^ (r & 15): the 16 rows that one pass of a 16-byte read
@@ -50,12 +53,11 @@ constexpr int tile_rows() { return A8 ? 128 : 256; }
 
 static __shared__ __align__(1024) v4u g_a[2 * kStageB / 16];
 static __shared__ __align__(1024) v4u g_b[2 * kStageB / 16];
-// Scales: two dwords a row and step.  With 16-byte loads the two pieces (two steps each) of the
-// 32 bytes that a row has in half a ring are fetched by two lanes of one load, so that it
-// touches 32 lines and not 64; piece q of row r lies at 16-byte place
+// Scales: two dwords a row and step.  The two 16-byte pieces (two steps each) that a row has in
+// half a ring are fetched by two lanes of one load, so that it touches 32 lines and not 64;
+// piece q of row r lies at 16-byte place
 //   half * 2 rows + 2 (r & ~7) + (r & 7) + 8 (q ^ ((r >> 3) & 1)),
-// where reading one dword of 32 rows meets each bank twice.  Otherwise dword d (of sixteen) of
-// row r lies at dword place d * rows + r.
+// where reading one dword of 32 rows meets each bank twice.
 static __shared__ __align__(1024) uint32_t g_sa[2 * kRing * 256];
 static __shared__ __align__(1024) uint32_t g_sb[2 * kRing * 256];
 
@@ -80,18 +82,17 @@ __device__ __forceinline__ i32x4_t rsrc_2g(const void* base) {
                  0x00020000};
 }
 
-// Four scale bytes at byte `off` of r, of which `have` exist; the others are zeros.
-__device__ __forceinline__ uint32_t scale_bytes4(rsrc_t r, uint32_t off, int have) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int c = 0; c < 4; ++c)
-    w |= uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(r, have > c ? off + c : kPastRange, 0, 0)))
-         << (8 * c);
-  return w;
+// The same for `bytes` bytes, from the dword that the first lies in to the one that the last
+// lies in: what a load of several dwords has past it reads as zeros (each dword by itself).
+__device__ __forceinline__ i32x4_t rsrc_dwords(const uint8_t* base, uint32_t bytes) {
+  const uint32_t low = uint32_t(reinterpret_cast<uintptr_t>(base) & 3);
+  i32x4_t r = rsrc_2g(base - low);
+  r.z = scalar(int((low + bytes + 3) & ~3u));
+  return r;
 }
 
-// Direct-to-LDS loads of 16 or 4 bytes a lane: lane l's land at lds_wave_addr + 16 (4) l.  One
-// wait state lies between the write of M0 and the load that reads it.
+// Direct-to-LDS load of 16 bytes a lane: lane l's land at lds_wave_addr + 16 l.  One wait state
+// lies between the write of M0 and the load that reads it.
 __device__ __forceinline__ void lds_load16(const i32x4_t& rsrc, uint32_t voff, uint32_t soff,
                                            uint32_t lds_wave_addr) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
@@ -100,26 +101,19 @@ __device__ __forceinline__ void lds_load16(const i32x4_t& rsrc, uint32_t voff, u
                "s"(rsrc), "s"(soff), "s"(m0)
                : "memory", "m0");
 }
-__device__ __forceinline__ void lds_load4(const i32x4_t& rsrc, uint32_t voff, uint32_t lds_wave_addr) {
-  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(voff),
-               "s"(rsrc), "s"(m0)
-               : "memory", "m0");
-}
 
-// SG: bytes a scale load moves: 16 where every row's scales are whole 16-byte pieces at
-// 16-byte addresses, 4 where they are whole dwords, 1 otherwise (through registers).
+// SHIFT: some row's scales do not start at a 16-byte address or are not whole 16-byte pieces.
 //
 // Where a tile's operands come from, and its direct-to-LDS loads.
-template <bool A8, int SG>
+template <bool A8, bool SHIFT>
 struct Source {
   static constexpr int kTM = tile_rows<A8>();
   static constexpr int kSA = kTM / 128;  // 16-byte loads of A's scales a wave
   i32x4_t ra, rb;            // codes of A from the tile's first row, of the expert's B
   i32x4_t rsa, rsb;          // their scales
   uint32_t oa[8], ob[8];     // byte offsets of this lane's chunks in step 0
-  const uint8_t *psa, *psb;  // the scales' addresses (SG 1)
-  uint32_t osa[2], osb[2];   // the scales this thread fetches (SG 16: of kSA and 2 rows; else [0])
+  uint32_t osa[kSA], osb[2];  // this lane's pieces of the scales
+  uint32_t sha, shb;          // bytes of its rows' first dword before their first scale
   int nblk;                  // K blocks
   int ca, cb;                // this lane's chunk of an A and of a B row
 
@@ -138,21 +132,20 @@ struct Source {
       oa[q] = uint32_t(int64_t(min(ar, rows - 1)) * p.ld_a) + ca * 16;
       ob[q] = uint32_t(min(n0 + br, p.n - 1)) * uint32_t(kb) + cb * 16;
     }
-    psa = p.as + r0 * p.ld_as;
-    psb = p.bs + int64_t(e) * p.n * nblk;
-    rsa = rsrc_2g(psa);
-    rsb = rsrc_2g(psb);
-    if (SG == 16) {
-      const int row = 8 * (l >> 4) + (l & 7);
-      const uint32_t piece = 16u * (((l >> 3) ^ (l >> 4)) & 1);
+    const uint8_t *as = p.as + r0 * p.ld_as, *bs = p.bs + int64_t(e) * p.n * nblk;
+    rsa = rsrc_dwords(as, uint32_t((rows - 1) * p.ld_as) + nblk);
+    rsb = rsrc_dwords(bs, uint32_t(p.n) * nblk);
+    const uint32_t la = uint32_t(reinterpret_cast<uintptr_t>(as) & 3);
+    const uint32_t lb = uint32_t(reinterpret_cast<uintptr_t>(bs) & 3);
+    // (32 rows on the first dword starts at the same byte)
+    sha = (la + uint32_t(l & 31) * uint32_t(p.ld_as)) & 3;
+    shb = (lb + uint32_t(l & 31) * uint32_t(nblk)) & 3;
+    const int row = 8 * (l >> 4) + (l & 7);
+    const uint32_t piece = 16u * (((l >> 3) ^ (l >> 4)) & 1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        osa[i] = i < kSA ? uint32_t(min((w * kSA + i) * 32 + row, rows - 1) * p.ld_as) + piece : kPastRange;
-        osb[i] = uint32_t(min(n0 + w * 64 + i * 32 + row, p.n - 1)) * uint32_t(nblk) + piece;
-      }
-    } else {
-      osa[0] = t < kTM ? uint32_t(min(t, rows - 1) * p.ld_as) : kPastRange;
-      osb[0] = uint32_t(min(n0 + t, p.n - 1)) * uint32_t(nblk);
+    for (int i = 0; i < 2; ++i) {
+      if (i < kSA) osa[i] = ((la + uint32_t(min((w * kSA + i) * 32 + row, rows - 1) * p.ld_as)) & ~3u) + piece;
+      osb[i] = ((lb + uint32_t(min(n0 + w * 64 + i * 32 + row, p.n - 1)) * uint32_t(nblk)) & ~3u) + piece;
     }
   }
 
@@ -174,35 +167,15 @@ struct Source {
   // Part 0..3 of the scales of steps 4 quad .. 4 quad + 3 (32 bytes a row) into their half of the
   // ring; each wave moves those of a quarter of the rows.
   __device__ __forceinline__ void issue_scales(int quad, int part) const {
-    const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int at = quad * 32, half = quad & 1;
-    if (SG == 16) {
-      const uint32_t past = at + 16 * (((l >> 3) ^ (l >> 4)) & 1) < nblk ? 0u : kPastRange;
-      const int i = part & 1;
-      if (part >= 2)
-        lds_load16(rsb, (i ? osb[1] : osb[0]) | past, uint32_t(at),
-                   lds_addr(g_sb) + uint32_t(half * 512 + (2 * w + i) * 64) * 16);
-      else if (i < kSA)
-        lds_load16(rsa, (i ? osa[1] : osa[0]) | past, uint32_t(at),
-                   lds_addr(g_sa) + uint32_t(half * 2 * kTM + (kSA * w + i) * 64) * 16);
-    } else {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int i = 2 * part + x, have = nblk - at - 4 * i;
-        if (SG == 4) {
-          const uint32_t past = have > 0 ? 0u : kPastRange;
-          if (w * 64 < kTM)
-            lds_load4(rsa, (osa[0] + at + 4 * i) | past,
-                      lds_addr(g_sa) + uint32_t((half * 8 + i) * kTM + w * 64) * 4);
-          lds_load4(rsb, (osb[0] + at + 4 * i) | past,
-                    lds_addr(g_sb) + uint32_t((half * 8 + i) * 256 + w * 64) * 4);
-        } else {
-          if (w * 64 < kTM)
-            g_sa[(half * 8 + i) * kTM + t] = scale_bytes4(row_rsrc(psa, kPastRange), osa[0] + at + 4 * i, have);
-          g_sb[(half * 8 + i) * 256 + t] = scale_bytes4(row_rsrc(psb, kPastRange), osb[0] + at + 4 * i, have);
-        }
-      }
-    }
+    const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int at = quad * 32, half = quad & 1, i = part & 1;
+    const int last = SHIFT ? nblk + 3 : nblk;  // no scale of a row lies in a piece from here on
+    const uint32_t past = at + 16 * (((l >> 3) ^ (l >> 4)) & 1) < last ? 0u : kPastRange;
+    if (part >= 2)
+      lds_load16(rsb, (osb[i] + at) | past, 0, lds_addr(g_sb) + uint32_t(half * 512 + (2 * w + i) * 64) * 16);
+    else if (i < kSA)
+      lds_load16(rsa, (osa[i < kSA ? i : 0] + at) | past, 0,
+                 lds_addr(g_sa) + uint32_t(half * 2 * kTM + (kSA * w + i) * 64) * 16);
   }
 
   // The same with what is wave-uniform in scalar registers again (values that were chosen on
@@ -216,7 +189,9 @@ struct Source {
       s.rsa[i] = scalar(rsa[i]);
       s.rsb[i] = scalar(rsb[i]);
     }
-    s.ra.z = s.rb.z = s.rsa.z = s.rsb.z = int(kPastRange);
+    s.ra.z = s.rb.z = int(kPastRange);
+    s.rsa.z = scalar(rsa.z);
+    s.rsb.z = scalar(rsb.z);
     s.ra.w = s.rb.w = s.rsa.w = s.rsb.w = 0x00020000;
     s.nblk = scalar(nblk);
     return s;
@@ -254,9 +229,9 @@ __device__ __forceinline__ void wait_all_but(int n) {
   else wait_vmcnt<0>();
 }
 
-template <bool A8, int SG, int IB>
+template <bool A8, bool SHIFT, int IB>
 struct Tile {
-  typedef Source<A8, SG> Src;
+  typedef Source<A8, SHIFT> Src;
   static constexpr int kTM = tile_rows<A8>();
   static constexpr int kJB = 4;  // 32-row blocks of B a wave; IB: of A
   static constexpr int kQA = A8 ? 4 * IB : 2 * IB;  // A loads a step
@@ -286,20 +261,39 @@ struct Tile {
   struct Scales {
     uint32_t a[IB], b[kJB];
   };
-  __device__ __forceinline__ void read_scales(Scales& s, int ks) const {
-    const int t = threadIdx.x, l = t & 63, w = t >> 6;
-    const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
-    const int d = 2 * (ks & (kRing - 1)) + h;  // dword of the ring
-    const int ra_ = wm * 32 * IB + r, rb_ = wn * 128 + r;
-    // (a block of 32 rows is 64 places on)
+  // Place, in dwords, of dword d of this lane's row in block 0 of A's (B's) ring; a block of 32
+  // rows is 256 dwords on.
+  __device__ __forceinline__ int scale_place(int d, bool b) const {
+    const int t = threadIdx.x, l = t & 63, w = t >> 6, r = l & 31;
     const int place = 2 * (r & ~7) + (r & 7) + 8 * (((d >> 2) ^ (r >> 3)) & 1);
-    const int wa = 4 * ((d >> 3) * 2 * kTM + wm * 64 * IB + place) + (d & 3);
-    const int wb = 4 * ((d >> 3) * 512 + wn * 256 + place) + (d & 3);
-#pragma unroll
-    for (int i = 0; i < IB; ++i) s.a[i] = SG == 16 ? g_sa[wa + 256 * i] : g_sa[d * kTM + ra_ + 32 * i];
-#pragma unroll
-    for (int j = 0; j < kJB; ++j) s.b[j] = SG == 16 ? g_sb[wb + 256 * j] : g_sb[d * 256 + rb_ + 32 * j];
+    const int half = (d >> 3) & 1;
+    return 4 * ((b ? half * 512 + (w & 1) * 256 : half * 2 * kTM + (w >> 1) * 64 * IB) + place) + (d & 3);
   }
+  // Dwords of the ring for this lane's scales of step ks in N row blocks of A or of B, and, where
+  // they are shifted together, the next ones.
+  template <int N>
+  struct Dwords {
+    uint32_t w[N], w1[SHIFT ? N : 1];
+
+    __device__ __forceinline__ void read(const Tile& t, int ks, bool b) {
+      const uint32_t* ring = b ? g_sb : g_sa;
+      const int d = 2 * ks + int((threadIdx.x & 63) >> 5);
+      const int at = t.scale_place(d, b), at1 = t.scale_place(d + 1, b);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        w[i] = ring[at + 256 * i];
+        if (SHIFT) w1[SHIFT ? i : 0] = ring[at1 + 256 * i];
+      }
+    }
+    // The four bytes that start `low` bytes into the first dword, without those past the row.
+    __device__ __forceinline__ void scales(uint32_t (&s)[N], uint32_t low, int ks, int nblk) const {
+      const int have = nblk - 8 * ks - 4 * int((threadIdx.x & 63) >> 5);
+      const uint32_t keep = have >= 4 ? ~0u : have <= 0 ? 0u : ~(~0u << (8 * have));
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        s[i] = SHIFT ? __builtin_amdgcn_alignbyte(w1[SHIFT ? i : 0], w[i], low) & keep : w[i];
+    }
+  };
 
   __device__ __forceinline__ i32x8_t read_a(int s, int i, uint32_t stage) const {
     const uint32_t o = uint32_t(i) * 32 * (A8 ? 256 : 128) + stage;
@@ -358,7 +352,7 @@ struct Tile {
     const Src src = opened.uniform();
     init();
     wait_all_but(Src::kAhead + stores);  // step 0 and its scales
-    wait_lds();  // scales written through registers (SG 1); the last tile's results read back
+    wait_lds();  // the last tile's results read back
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     // f[s]: the fragments of slice s.  Those of slices 0..2 are read one step ahead, those of
@@ -366,7 +360,12 @@ struct Tile {
     // two steps ahead have the rest of the step to be issued in.
     Frag f[4];
     Scales sc, sn;
-    read_scales(sc, 0);
+    Dwords<IB> da;
+    Dwords<kJB> db;
+    da.read(*this, 0, false);
+    db.read(*this, 0, true);
+    da.scales(sc.a, src.sha, 0, src.nblk);
+    db.scales(sc.b, src.shb, 0, src.nblk);
 #pragma unroll
     for (int s = 0; s < 3; ++s)
 #pragma unroll
@@ -385,18 +384,25 @@ struct Tile {
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       const uint32_t nxt = cur ^ kStageB;
-      // A quarter of the scales of four steps each step, from the one on that finds their half of
-      // the ring read by all (of step 0 the half that the last tile's results went through).
-      if (!A8) {
-        if (ks == 0) src.issue_scales(1, 0);
-        src.issue_scales((ks + 1) / 4 + 1, (ks + 1) & 3);
-      } else if ((ks & 3) == 3 || ks == 0) {
-#pragma unroll
-        for (int part = 0; part < 4; ++part) src.issue_scales(ks == 0 ? 1 : ks / 4 + 2, part);
+      // Scales of the four steps that follow the ring's, once their half is read by all (from step
+      // ks = 4 q - 5 on for the q-th four; at step 0 it is the half that the last tile's results
+      // went through), and there at step 4 q - 2, where a shifted read takes their first dword.
+      // With 4-bit rows, whose steps are shorter, over three steps.
+      const int ph = (ks + 1) & 3, quad = (ks + 1) / 4 + 1;
+      if (ks == 0 || ph == 0) {
+        src.issue_scales(quad, 0);
+        src.issue_scales(quad, 1);
+        if (A8) src.issue_scales(quad, 2);
+        if (A8) src.issue_scales(quad, 3);
       }
-      read_scales(sn, ks + 1);
+      if (!A8 && ph == 1) src.issue_scales(quad, 2);
+      if (!A8 && ph == 2) src.issue_scales(quad, 3);
+      db.read(*this, ks + 1, true);
       slice<1, 0, 0, kD1>(src, f[1], f[0], sc, nxt, ks, cur);
+      db.scales(sn.b, src.shb, ks + 1, src.nblk);
+      da.read(*this, ks + 1, false);
       slice<2, 1, kD1, kD2>(src, f[2], f[1], sc, nxt, ks, cur);
+      da.scales(sn.a, src.sha, ks + 1, src.nblk);
       slice<3, 2, 0, 0>(src, f[3], f[2], sc, nxt, ks, cur);
       sc = sn;
       cur = nxt;
@@ -421,7 +427,9 @@ struct Tile {
 
   template <bool OUT32>
   __device__ __forceinline__ void store(const GroupedArgs& p, int64_t r0, int rows, int n0) const {
-    const int t = threadIdx.x, l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));  // the addresses below are not kept over the K loop
+    const int l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = w >> 1, wn = w & 1, r = l & 31, h = l >> 5;
     constexpr int kSize = OUT32 ? 4 : 2;
     constexpr int kJ = OUT32 ? 1 : 2;  // column blocks that make 128 bytes

@@ -62,41 +62,53 @@ __device__ __forceinline__ f32x4_t mfma16(i32x8_t w, i32x8_t a, f32x4_t c, int s
 // product).
 constexpr int kChunk = 256;
 
-// The eight scale bytes of a row's chunk, zeros past the row's end.  SG: bytes a load, 8 where
-// every row's scales are whole 8-byte pieces at 8-byte addresses, 4 or 1 otherwise.
-template <int SG>
-__device__ __forceinline__ void load_scales8(uint32_t (&s)[2], rsrc_t r, uint32_t off, int have) {
-  if (SG == 8) {
-    typedef uint32_t v2u_t __attribute__((ext_vector_type(2)));
-    const v2u_t v = __builtin_amdgcn_raw_buffer_load_b64(r, off | (have > 0 ? 0u : kOut), 0, 0);
-    s[0] = v.x;
-    s[1] = v.y;
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (SG == 4) {
-      s[i] = __builtin_amdgcn_raw_buffer_load_b32(r, (off + 4 * i) | (have > 4 * i ? 0u : kOut), 0, 0);
+// The eight scale bytes of a row's chunk: two dwords, or, where some row's scales do not start
+// at an 8-byte address or are not whole pieces of 8 (SHIFT), the three that they lie in (64 rows
+// over 8 experts, N 4096, K 7200 in MXFP8 on MI355X: 62 us by bytes, 34 so; 31 for K 7168).
+template <bool SHIFT>
+struct Scales8 {
+  uint32_t w[SHIFT ? 3 : 2];
+
+  __device__ __forceinline__ void load(rsrc_t r, uint32_t off, int have) {
+    const uint32_t past = have > 0 ? 0u : kOut;
+    if (SHIFT) {
+      typedef uint32_t v3u_t __attribute__((ext_vector_type(3)));
+      const v3u_t v = __builtin_amdgcn_raw_buffer_load_b96(r, (off & ~3u) | past, 0, 0);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[SHIFT ? 2 : 0] = v.z;
     } else {
-      s[i] = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        s[i] |= uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(
-                    r, (off + 4 * i + c) | (have > 4 * i + c ? 0u : kOut), 0, 0)))
-                << (8 * c);
+      typedef uint32_t v2u_t __attribute__((ext_vector_type(2)));
+      const v2u_t v = __builtin_amdgcn_raw_buffer_load_b64(r, off | past, 0, 0);
+      w[0] = v.x;
+      w[1] = v.y;
     }
   }
+  // Byte g of dword s, 0 past the row; `low`: bytes before the first in the first dword.
+  __device__ __forceinline__ int at(int s, int g, uint32_t low, int have) const {
+    if (!SHIFT) return int(w[s] >> (8 * g));
+    const uint32_t v = __builtin_amdgcn_alignbyte(w[SHIFT ? s + 1 : s], w[s], low) >> (8 * g);
+    return 4 * s + g < have ? int(v) : 0;
+  }
+};
+
+// A matrix's scales from the dword that the first byte lies in to the one that the last lies
+// in; loads read the dwords past it as zeros, each by itself.
+__device__ __forceinline__ rsrc_t scales_rsrc(const uint8_t* base, uint32_t bytes) {
+  const uint32_t low = uint32_t(reinterpret_cast<uintptr_t>(base) & 3);
+  return row_rsrc(base - low, (low + bytes + 3) & ~3u);
 }
 
-template <bool A8, int SG, int NB, int MB>
+template <bool A8, bool SHIFT, int NB, int MB>
 struct Chunk {
   v4u b[NB][2];         // a column block's codes, one 16-byte K block a step
-  uint32_t bs[NB][2];   // its scale dword of each step
+  Scales8<SHIFT> bs[NB];
   v4u a[MB][2][A8 ? 2 : 1];
-  uint32_t as[MB][2];
+  Scales8<SHIFT> as[MB];
 
-  __device__ __forceinline__ void load(const GroupedArgs& p, rsrc_t rb, rsrc_t rbs, rsrc_t ra, rsrc_t ras,
-                                       int valid, int ck) {
+  // lb, la: bytes of the scale resources before the first scale
+  __device__ __forceinline__ void load(const GroupedArgs& p, rsrc_t rb, rsrc_t rbs, uint32_t lb, rsrc_t ra,
+                                       rsrc_t ras, uint32_t la, int valid, int ck) {
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int kb = p.k / 2, nblk = p.k / 32, have = nblk - 8 * ck;
 #pragma unroll
@@ -106,7 +118,7 @@ struct Chunk {
       for (int s = 0; s < 2; ++s)
         b[j][s] = buf_ld16<kCpolPlain>(
             rb, (row * kb + (8 * ck + 4 * s + g) * 16) | (4 * s + g < have ? 0u : kOut));
-      load_scales8<SG>(bs[j], rbs, row * nblk + 8 * ck, have);
+      bs[j].load(rbs, lb + row * nblk + 8 * ck, have);
     }
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
@@ -125,13 +137,15 @@ struct Chunk {
               ra, (at + (8 * ck + 4 * s + g) * 16) | out_r | (4 * s + g < have ? 0u : kOut));
         }
       }
-      load_scales8<SG>(as[m], ras, (uint32_t(row * p.ld_as) + 8 * ck) | out_r, have);
+      as[m].load(ras, (la + uint32_t(row * p.ld_as) + 8 * ck) | out_r, have);
     }
   }
 
-  // The lane's K block of step s is 4 s + g: byte g of the step's scale dword.
-  __device__ __forceinline__ void multiply(f32x4_t (&acc)[MB][NB]) const {
-    const int sh = 8 * ((threadIdx.x & 63) >> 4);
+  // The lane's K block of step s is 4 s + g: byte g of the step's scale dword.  shb, sha: where
+  // the lane's rows start in their first dwords (16 rows on it is the same byte); `have`: the
+  // chunk's K blocks.
+  __device__ __forceinline__ void multiply(f32x4_t (&acc)[MB][NB], uint32_t shb, uint32_t sha, int have) const {
+    const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -142,30 +156,34 @@ struct Chunk {
         for (int j = 0; j < NB; ++j) {
           const v4u w = b[j][s];
           const i32x8_t wf = {int(w.x), int(w.y), int(w.z), int(w.w), 0, 0, 0, 0};
-          acc[m][j] = mfma16(wf, af, acc[m][j], int(bs[j][s] >> sh), int(as[m][s] >> sh), A8);
+          acc[m][j] = mfma16(wf, af, acc[m][j], bs[j].at(s, g, shb, have), as[m].at(s, g, sha, have), A8);
         }
       }
   }
 };
 
-template <bool A8, int SG, int NB, int W, int MB>
+template <bool A8, bool SHIFT, int NB, int W, int MB>
 __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part, int64_t r0, int valid,
-                                          rsrc_t rb, rsrc_t rbs, int n0) {
+                                          rsrc_t rb, rsrc_t rbs, uint32_t lb, int n0) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kb = p.k / 2, nblk = p.k / 32, chunks = (p.k + kChunk - 1) / kChunk;
   const rsrc_t ra = row_rsrc(p.a + r0 * p.ld_a, uint32_t((valid - 1) * p.ld_a + (A8 ? p.k : kb)));
-  const rsrc_t ras = row_rsrc(p.as + r0 * p.ld_as, uint32_t((valid - 1) * p.ld_as + nblk));
+  const uint8_t* as = p.as + r0 * p.ld_as;
+  const rsrc_t ras = scales_rsrc(as, uint32_t((valid - 1) * p.ld_as + nblk));
+  const uint32_t la = uint32_t(reinterpret_cast<uintptr_t>(as) & 3);
+  const uint32_t shb = (lb + uint32_t(lane & 15) * uint32_t(nblk)) & 3;
+  const uint32_t sha = (la + uint32_t(lane & 15) * uint32_t(p.ld_as)) & 3;
   f32x4_t acc[MB][NB];
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int j = 0; j < NB; ++j) acc[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   if (w < chunks) {
-    Chunk<A8, SG, NB, MB> cur, nxt;
-    cur.load(p, rb, rbs, ra, ras, valid, w);
+    Chunk<A8, SHIFT, NB, MB> cur, nxt;
+    cur.load(p, rb, rbs, lb, ra, ras, la, valid, w);
     for (int ck = w; ck < chunks; ck += W) {
-      nxt.load(p, rb, rbs, ra, ras, valid, ck + W);  // past the last: reads nothing
-      cur.multiply(acc);
+      nxt.load(p, rb, rbs, lb, ra, ras, la, valid, ck + W);  // past the last: reads nothing
+      cur.multiply(acc, shb, sha, nblk - 8 * ck);
       cur = nxt;
     }
   }
@@ -193,7 +211,7 @@ __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part,
   __syncthreads();  // s_part is rewritten by the next pass
 }
 
-template <bool A8, int SG, int NB, int W>
+template <bool A8, bool SHIFT, int NB, int W>
 __global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, bool both) {
   __shared__ f32x4_t s_part[W * 2 * NB * 64];
   if (both && !few_rows(p)) return;
@@ -220,13 +238,15 @@ __global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, bool bot
   const int n0 = blockIdx.x * 16 * NB, ncols = min(16 * NB, p.n - n0);
   const int64_t brow = int64_t(e) * p.n + n0;
   const rsrc_t rb = row_rsrc(p.b + brow * (p.k / 2), uint32_t(ncols * (p.k / 2)));
-  const rsrc_t rbs = row_rsrc(p.bs + brow * (p.k / 32), uint32_t(ncols * (p.k / 32)));
+  const uint8_t* bs = p.bs + brow * (p.k / 32);
+  const rsrc_t rbs = scales_rsrc(bs, uint32_t(ncols * (p.k / 32)));
+  const uint32_t lb = uint32_t(reinterpret_cast<uintptr_t>(bs) & 3);
   while (lo < hi) {
     if (hi - lo <= 16) {
-      rows_pass<A8, SG, NB, W, 1>(p, s_part, lo, int(hi - lo), rb, rbs, n0);
+      rows_pass<A8, SHIFT, NB, W, 1>(p, s_part, lo, int(hi - lo), rb, rbs, lb, n0);
       break;
     }
-    rows_pass<A8, SG, NB, W, 2>(p, s_part, lo, int(min(hi - lo, int64_t(32))), rb, rbs, n0);
+    rows_pass<A8, SHIFT, NB, W, 2>(p, s_part, lo, int(min(hi - lo, int64_t(32))), rb, rbs, lb, n0);
     lo += 32;
   }
 }
@@ -293,7 +313,7 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
 
 // A workgroup's next tile: workgroups go to the eight XCDs in turn, and XCD x takes the x-th
 // eighth of the tiles, whose operands its L2 then holds; its workgroups take them in turn.
-template <bool A8, bool OUT32, int SG>
+template <bool A8, bool OUT32, bool SHIFT>
 __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt, bool both) {
   if (both && few_rows(p)) return;
   constexpr int TM = mx4::tile_rows<A8>();
@@ -304,7 +324,7 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int m
   const int first = int(blockIdx.x & 7) * per, end = min(first + per, total);
   int t = first + int(blockIdx.x >> 3);
   if (t >= end) return;
-  mx4::Source<A8, SG> src;
+  mx4::Source<A8, SHIFT> src;
   int m, n, e, rows;
   int64_t r0;
   auto open = [&]() __attribute__((always_inline)) {
@@ -325,15 +345,16 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int m
     stores = tile.template kStores<OUT32>;
   };
   while (t < end) {
-    if (rows <= 64) run(mx4::Tile<A8, SG, 1>());
-    else if (A8 || rows <= 128) run(mx4::Tile<A8, SG, 2>());
-    else run(mx4::Tile<A8, SG, A8 ? 2 : 4>());
+    if (rows <= 64) run(mx4::Tile<A8, SHIFT, 1>());
+    else if (A8 || rows <= 128) run(mx4::Tile<A8, SHIFT, 2>());
+    else run(mx4::Tile<A8, SHIFT, A8 ? 2 : 4>());
   }
 }
 
-int64_t scales_align(const GroupedArgs& a) {
-  return int64_t(reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) |
-                 uintptr_t(a.ld_as) | uintptr_t(a.k / 32));
+// Whether every row's scales are whole pieces of `piece` bytes at multiples of it.
+bool scales_whole(const GroupedArgs& a, uintptr_t piece) {
+  return (reinterpret_cast<uintptr_t>(a.as) | reinterpret_cast<uintptr_t>(a.bs) | uintptr_t(a.ld_as) |
+          uintptr_t(a.k / 32)) % piece == 0;
 }
 
 void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
@@ -342,20 +363,17 @@ void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
   const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
   const dim3 grid(unsigned(std::min<int64_t>((mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, int(mt), nt, both); };
-  auto sg = [&](auto g) {
-    constexpr int SG = decltype(g)::value;
+  auto form = [&](auto shift) {
+    constexpr bool SHIFT = decltype(shift)::value;
     if (a.a8) {
-      if (a.out32) go(k_grouped_tile<true, true, SG>);
-      else go(k_grouped_tile<true, false, SG>);
+      if (a.out32) go(k_grouped_tile<true, true, SHIFT>);
+      else go(k_grouped_tile<true, false, SHIFT>);
     } else {
-      if (a.out32) go(k_grouped_tile<false, true, SG>);
-      else go(k_grouped_tile<false, false, SG>);
+      if (a.out32) go(k_grouped_tile<false, true, SHIFT>);
+      else go(k_grouped_tile<false, false, SHIFT>);
     }
   };
-  const int64_t align = scales_align(a);
-  if (align % 16 == 0) sg(std::integral_constant<int, 16>());
-  else if (align % 4 == 0) sg(std::integral_constant<int, 4>());
-  else sg(std::integral_constant<int, 1>());
+  scales_whole(a, 16) ? form(std::false_type()) : form(std::true_type());
 }
 
 // Columns a workgroup: the most that leave 512 workgroups, two a CU (64 rows over 8 experts, N
@@ -368,22 +386,18 @@ void launch_rows(const GroupedArgs& a, int64_t experts, bool both, hipStream_t s
   const dim3 grid(unsigned((a.n + 16 * nb - 1) / (16 * nb)), unsigned(experts));
   const dim3 block(deep ? 512 : 256);
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, both); };
-  auto shape = [&](auto a8, auto g) {
-    constexpr bool A8 = decltype(a8)::value;
-    constexpr int SG = decltype(g)::value;
-    if (nb == 4) go(k_grouped_rows<A8, SG, 4, 4>);
-    else if (nb == 2) go(k_grouped_rows<A8, SG, 2, 4>);
-    else if (deep) go(k_grouped_rows<A8, SG, 1, 8>);
-    else go(k_grouped_rows<A8, SG, 1, 4>);
+  auto shape = [&](auto a8, auto shift) {
+    constexpr bool A8 = decltype(a8)::value, SHIFT = decltype(shift)::value;
+    if (nb == 4) go(k_grouped_rows<A8, SHIFT, 4, 4>);
+    else if (nb == 2) go(k_grouped_rows<A8, SHIFT, 2, 4>);
+    else if (deep) go(k_grouped_rows<A8, SHIFT, 1, 8>);
+    else go(k_grouped_rows<A8, SHIFT, 1, 4>);
   };
-  auto format = [&](auto g) {
-    if (a.a8) shape(std::true_type(), g);
-    else shape(std::false_type(), g);
+  auto format = [&](auto shift) {
+    if (a.a8) shape(std::true_type(), shift);
+    else shape(std::false_type(), shift);
   };
-  const int64_t align = scales_align(a);
-  if (align % 8 == 0) format(std::integral_constant<int, 8>());
-  else if (align % 4 == 0) format(std::integral_constant<int, 4>());
-  else format(std::integral_constant<int, 1>());
+  scales_whole(a, 8) ? format(std::false_type()) : format(std::true_type());
 }
 
 }  // namespace
