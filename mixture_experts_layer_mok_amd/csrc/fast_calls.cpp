@@ -87,7 +87,7 @@ bool matrix(Call& c, const at::Tensor* t, Matrix* m, bool write) {
   m->ld = m->rows <= 1 ? m->cols : t->stride(0);
   // (the entry points take the sizes of a row as 32 bits)
   if (m->cols > INT32_MAX) return c.ok = false;
-  if ((m->cols > 1 && t->stride(1) != 1) || (write && m->ld < m->cols) || m->ld < 0) return c.ok = false;
+  if ((m->rows > 0 && m->cols > 1 && t->stride(1) != 1) || (write && m->ld < m->cols) || m->ld < 0) return c.ok = false;
   m->s = span(*t, m->rows && m->cols ? (m->rows - 1) * m->ld + m->cols : 0);
   m->p = t->data_ptr();
   return true;

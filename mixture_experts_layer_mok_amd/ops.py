@@ -55,7 +55,7 @@ def _matrix(name, t, rows=-1, cols=-1, dtype=None, write=False) -> tuple:
     if c > _MAX:
         raise ValueError(f"{name}: a row has at most {_MAX} elements")
     ld, step = t.stride()
-    if step != 1 and c > 1:
+    if step != 1 and c > 1 and r > 0:  # (of no rows the strides say nothing)
         raise ValueError(f"{name}: rows must be contiguous")
     if r <= 1:
         ld = c  # the stride of a single row says nothing
@@ -150,7 +150,7 @@ def _bind(lib) -> None:
 
     names = ("mok_permute", "mok_permute_bwd", "mok_unpermute", "mok_unpermute_bwd",
              "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4")
-    module.bind(torch._C._cuda_getDevice, _raw_stream,
+    module.bind(getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream,
                 *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
     _fast = module
 

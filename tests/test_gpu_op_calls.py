@@ -105,6 +105,11 @@ def test_three_axes_and_no_rows():
     assert ops.permute_backward(x[0], pos).shape == (0, 64)
     out = torch.full((4, 64), 3.0, device=DEV)
     assert (ops.permute(e, pos, out) == 3).all()
+    rows = torch.empty(0, 64, device=DEV).as_strided((0, 64), (1, 5))
+    pos = torch.full((3, 2), -1, dtype=torch.int32, device=DEV)
+    for stream in (None, torch.cuda.current_stream()):
+        y = ops.permute_backward(rows, pos, stream=stream)
+        assert y.shape == (3, 64) and not y.any()
 
 
 def wrong(t, how):

@@ -326,3 +326,11 @@ def test_the_layers_kernels_do_not_include_the_operators():
             with open(os.path.join(bench.CSRC, name)) as f:
                 included = re.findall(r'#include "([^"]+)"', f.read())
             assert not set(included) & set(bench.OPERATOR_SOURCES), name
+
+
+def test_strides_of_no_rows_say_nothing():
+    rows = torch.empty(0, 64).as_strided((0, 64), (1, 5))
+    with pytest.raises(ValueError, match="on a GPU"):
+        ops.permute_backward(rows, torch.full((3, 2), -1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="contiguous"):
+        ops.permute_backward(torch.empty(5, 64).t(), torch.full((3, 2), -1, dtype=torch.int32))
