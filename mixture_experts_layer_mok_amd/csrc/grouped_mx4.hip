@@ -32,29 +32,70 @@ __device__ __forceinline__ void expert_rows(const int32_t* offsets, int e, int64
   *hi = min(int64_t(offsets[e + 1]), max_rows);
 }
 
-// Whether the few-rows kernel has the call, where both are launched (the choice is explained at
-// launch_grouped_mx4): no expert of more than 64 rows, 256 rows in all.
-__device__ __forceinline__ bool few_rows(const GroupedArgs& p) {
-  const int64_t first = max(int64_t(p.offsets[0]), int64_t(0));
-  bool few = min(int64_t(p.offsets[p.groups]), p.max_rows) - first <= 256;
-  for (int e0 = 0; few && e0 < p.groups; e0 += 64) {
-    int64_t l = 0, h = 0;
-    const int e = e0 + int(threadIdx.x & 63);
-    if (e < p.groups) expert_rows(p.offsets, e, p.max_rows, &l, &h);
-    few = !__any(h - l > 64);
-  }
-  return few;
-}
-
 __device__ __forceinline__ f32x4_t mfma16(i32x8_t w, i32x8_t a, f32x4_t c, int sw, int sa, bool a8) {
   return a8 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 0, 0, sw, 0, sa)
             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, 4, 4, 0, sw, 0, sa);
 }
 
+// The m-tiles of all experts (each expert's rows cut from its first row on into tiles of
+// TM), numbered in expert order.  Every wave scans the experts, 64 at a time; with at most 64
+// of them they are read once.
+template <int TM>
+struct Tiling {
+  int lo, hi, incl;  // this lane's expert of the current 64: rows, m-tiles up to it
+  int total;         // m-tiles of all experts
+  int tiles;         // this lane's expert's
+
+  __device__ __forceinline__ void scan(const GroupedArgs& p, int e0) {
+    const int lane = threadIdx.x & 63;
+    int64_t l = 0, h = 0;
+    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &l, &h);
+    lo = int(l);
+    hi = int(h);
+    tiles = hi > lo ? (hi - lo + TM - 1) / TM : 0;
+    incl = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int u = __shfl_up(incl, d);
+      if (lane >= d) incl += u;
+    }
+  }
+  __device__ __forceinline__ void init(const GroupedArgs& p) {
+    total = 0;
+    for (int e0 = 0; e0 < p.groups; e0 += 64) {
+      scan(p, e0);
+      total += __builtin_amdgcn_readlane(incl, 63);
+    }
+  }
+  // m-tile m < total: its expert, first row and rows
+  __device__ __forceinline__ void find(const GroupedArgs& p, int m, int* e, int64_t* r0, int* rows) {
+    int e0 = 0;
+    if (p.groups > 64) {
+      for (;; e0 += 64) {
+        scan(p, e0);
+        const int n = __builtin_amdgcn_readlane(incl, 63);
+        if (m < n) break;
+        m -= n;
+      }
+    }
+    const int s = __ffsll((unsigned long long)__ballot(incl > m)) - 1;
+    *e = e0 + s;
+    const int first = __builtin_amdgcn_readlane(lo, s) +
+                      (m - __builtin_amdgcn_readlane(incl - tiles, s)) * TM;
+    *r0 = first;
+    *rows = min(__builtin_amdgcn_readlane(hi, s) - first, TM);
+  }
+};
+
+// Whether the few-rows kernel has the call: passes of at most 32 rows times 256-column blocks (the
+// bound is explained at launch_grouped_mx4).
+constexpr int kPass = 32, kFew = 128;
+__host__ __device__ __forceinline__ bool is_few(int64_t passes, int nt) { return passes * nt <= kFew; }
+
 // ------------------------------------------------------------------------------------
 // Few rows an expert (decoding): bound by reading the weights once.
 // ------------------------------------------------------------------------------------
-// One workgroup of W waves: 16 NB columns of one expert, all its rows in passes of 16 or 32.
+// One workgroup of W waves: 16 NB columns of one expert and at most 32 of its rows (a pass).
 // The K chunks of 256 (two MFMA steps) are dealt to the waves; each loads its next chunk
 // before it multiplies the current one, straight into registers (a weight is used by one
 // wave only, so LDS would add a copy), and the waves' sums are joined through LDS in wave
@@ -208,98 +249,43 @@ __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part,
             uint64_t(pack_bf16x2(c.x, c.y)) | (uint64_t(pack_bf16x2(c.z, c.w)) << 32);
     }
   }
-  __syncthreads();  // s_part is rewritten by the next pass
 }
 
+// Item t: passes of all experts times blocks of 16 NB columns, columns first, so that the passes
+// that read the same weights run on the same XCD, at about the same time.
 template <bool A8, bool SHIFT, int NB, int W>
-__global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, bool both) {
-  __shared__ f32x4_t s_part[W * 2 * NB * 64];
-  if (both && !few_rows(p)) return;
-  // the blockIdx.y-th expert that has rows
-  const int lane = threadIdx.x & 63;
-  int want = blockIdx.y, e = -1;
-  int64_t lo = 0, hi = 0;
-  for (int e0 = 0; e0 < p.groups; e0 += 64) {
-    int64_t l = 0, h = 0;
-    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &l, &h);
-    const uint64_t has = __ballot(h > l);
-    const int n = __popcll(has);
-    if (want < n) {
-      const int rank = __builtin_amdgcn_mbcnt_hi(uint32_t(has >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(has), 0u));
-      const int s = __ffsll((unsigned long long)__ballot(h > l && rank == want)) - 1;
-      e = e0 + s;
-      lo = __builtin_amdgcn_readlane(int(l), s);
-      hi = __builtin_amdgcn_readlane(int(h), s);
-      break;
-    }
-    want -= n;
-  }
-  if (e < 0) return;
-  const int n0 = blockIdx.x * 16 * NB, ncols = min(16 * NB, p.n - n0);
+__device__ __forceinline__ void rows_item(const GroupedArgs& p, Tiling<kPass>& til, f32x4_t* s_part, int t) {
+  const int ncb = (p.n + 16 * NB - 1) / (16 * NB);
+  const int m = t / ncb, n0 = (t - m * ncb) * 16 * NB, ncols = min(16 * NB, p.n - n0);
+  if (m >= til.total) return;
+  int e, rows;
+  int64_t r0;
+  til.find(p, m, &e, &r0, &rows);
   const int64_t brow = int64_t(e) * p.n + n0;
   const rsrc_t rb = row_rsrc(p.b + brow * (p.k / 2), uint32_t(ncols * (p.k / 2)));
   const uint8_t* bs = p.bs + brow * (p.k / 32);
   const rsrc_t rbs = scales_rsrc(bs, uint32_t(ncols * (p.k / 32)));
   const uint32_t lb = uint32_t(reinterpret_cast<uintptr_t>(bs) & 3);
-  while (lo < hi) {
-    if (hi - lo <= 16) {
-      rows_pass<A8, SHIFT, NB, W, 1>(p, s_part, lo, int(hi - lo), rb, rbs, lb, n0);
-      break;
-    }
-    rows_pass<A8, SHIFT, NB, W, 2>(p, s_part, lo, int(min(hi - lo, int64_t(32))), rb, rbs, lb, n0);
-    lo += 32;
-  }
+  if (rows <= 16) rows_pass<A8, SHIFT, NB, W, 1>(p, s_part, r0, rows, rb, rbs, lb, n0);
+  else rows_pass<A8, SHIFT, NB, W, 2>(p, s_part, r0, rows, rb, rbs, lb, n0);
 }
 
-// The m-tiles of all experts (each expert's rows cut from its first row on into tiles of
-// TM), numbered in expert order.  Every wave scans the experts, 64 at a time; with at most 64
-// of them they are read once.
-template <int TM>
-struct Tiling {
-  int lo, hi, incl;  // this lane's expert of the current 64: rows, m-tiles up to it
-  int total;         // m-tiles of all experts
-  int tiles;         // this lane's expert's
-
-  __device__ __forceinline__ void scan(const GroupedArgs& p, int e0) {
-    const int lane = threadIdx.x & 63;
-    int64_t l = 0, h = 0;
-    if (e0 + lane < p.groups) expert_rows(p.offsets, e0 + lane, p.max_rows, &l, &h);
-    lo = int(l);
-    hi = int(h);
-    tiles = hi > lo ? (hi - lo + TM - 1) / TM : 0;
-    incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(incl, d);
-      if (lane >= d) incl += u;
-    }
-  }
-  __device__ __forceinline__ void init(const GroupedArgs& p) {
-    total = 0;
-    for (int e0 = 0; e0 < p.groups; e0 += 64) {
-      scan(p, e0);
-      total += __builtin_amdgcn_readlane(incl, 63);
-    }
-  }
-  // m-tile m < total: its expert, first row and rows
-  __device__ __forceinline__ void find(const GroupedArgs& p, int m, int* e, int64_t* r0, int* rows) {
-    int e0 = 0;
-    if (p.groups > 64) {
-      for (;; e0 += 64) {
-        scan(p, e0);
-        const int n = __builtin_amdgcn_readlane(incl, 63);
-        if (m < n) break;
-        m -= n;
-      }
-    }
-    const int s = __ffsll((unsigned long long)__ballot(incl > m)) - 1;
-    *e = e0 + s;
-    const int first = __builtin_amdgcn_readlane(lo, s) +
-                      (m - __builtin_amdgcn_readlane(incl - tiles, s)) * TM;
-    *r0 = first;
-    *rows = min(__builtin_amdgcn_readlane(hi, s) - first, TM);
-  }
-};
+// Columns a workgroup: the most that leave an item a CU (every item reads its rows again).
+// Measured on MI355X with a bound of 256 / 512 items, us: 128 rows of one expert, N 4096, K 7168,
+// MXFP8 20 / 25 (45 with 16 columns); 256 rows of 8, N 2048, K 4096 15.6 / 19.2.  64 rows of 8
+// experts, N 4096, K 7168, MXFP8: 64 columns 32, 32 39, 16 42.
+template <bool A8, bool SHIFT, int W>
+__global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, int max_passes, int nt, bool both) {
+  __shared__ f32x4_t s_part[W * 2 * (W == 8 ? 1 : 4) * 64];
+  Tiling<kPass> til;
+  til.init(p);
+  til.total = min(til.total, max_passes);  // more only where ranges overlap
+  if (both && !is_few(til.total, nt)) return;
+  if (W == 8) return rows_item<A8, SHIFT, 1, W>(p, til, s_part, blockIdx.x);
+  if ((p.n + 63) / 64 * til.total >= 256) rows_item<A8, SHIFT, 4, 4>(p, til, s_part, blockIdx.x);
+  else if ((p.n + 31) / 32 * til.total >= 256) rows_item<A8, SHIFT, 2, 4>(p, til, s_part, blockIdx.x);
+  else rows_item<A8, SHIFT, 1, 4>(p, til, s_part, blockIdx.x);
+}
 
 // Tile t of mt x nt: groups of kGroupM m-tiles, inside them all m-tiles of an n-tile before the next,
 // so that the tiles that run at the same time share both operands' rows.
@@ -315,7 +301,11 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
 // eighth of the tiles, whose operands its L2 then holds; its workgroups take them in turn.
 template <bool A8, bool OUT32, bool SHIFT>
 __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt, bool both) {
-  if (both && few_rows(p)) return;
+  if (both) {
+    Tiling<kPass> passes;
+    passes.init(p);
+    if (is_few(passes.total, nt)) return;
+  }
   constexpr int TM = mx4::tile_rows<A8>();
   Tiling<TM> til;
   til.init(p);
@@ -376,54 +366,50 @@ void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
   scales_whole(a, 16) ? form(std::false_type()) : form(std::true_type());
 }
 
-// Columns a workgroup: the most that leave 512 workgroups, two a CU (64 rows over 8 experts, N
-// 4096, K 7168 in MXFP8: 64 columns 32 us, 32 39, 16 42); eight waves instead of four where
-// they have chunks for two rounds and the workgroups are few.
-void launch_rows(const GroupedArgs& a, int64_t experts, bool both, hipStream_t st) {
-  auto enough = [&](int cols) { return (a.n + cols - 1) / cols * experts >= 512; };
-  const int nb = enough(64) ? 4 : enough(32) ? 2 : 1;
-  const bool deep = nb == 1 && a.k >= 16 * kChunk;
-  const dim3 grid(unsigned((a.n + 16 * nb - 1) / (16 * nb)), unsigned(experts));
-  const dim3 block(deep ? 512 : 256);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, both); };
-  auto shape = [&](auto a8, auto shift) {
+// At most 512 items: few passes (is_few) of 64 columns, or fewer than 256 of twice the columns
+// of what is taken.  Eight waves instead of four where their chunks fill two rounds and the
+// items are at most one a CU (then of 16 columns).
+void launch_rows(const GroupedArgs& a, int64_t passes, int nt, bool both, hipStream_t st) {
+  const int64_t items = (a.n + 15) / 16 * passes;
+  const bool deep = a.k >= 16 * kChunk && items <= 256;
+  const dim3 grid(unsigned(std::min<int64_t>(items, 4 * kFew)));
+  auto go = [&](auto kern, int waves) {
+    hipLaunchKernelGGL(kern, grid, dim3(64 * waves), 0, st, a, int(passes), nt, both);
+  };
+  auto form = [&](auto a8, auto shift) {
     constexpr bool A8 = decltype(a8)::value, SHIFT = decltype(shift)::value;
-    if (nb == 4) go(k_grouped_rows<A8, SHIFT, 4, 4>);
-    else if (nb == 2) go(k_grouped_rows<A8, SHIFT, 2, 4>);
-    else if (deep) go(k_grouped_rows<A8, SHIFT, 1, 8>);
-    else go(k_grouped_rows<A8, SHIFT, 1, 4>);
+    if (deep) go(k_grouped_rows<A8, SHIFT, 8>, 8);
+    else go(k_grouped_rows<A8, SHIFT, 4>, 4);
   };
   auto format = [&](auto shift) {
-    if (a.a8) shape(std::true_type(), shift);
-    else shape(std::false_type(), shift);
+    if (a.a8) form(std::true_type(), shift);
+    else form(std::false_type(), shift);
   };
   scales_whole(a, 8) ? format(std::false_type()) : format(std::true_type());
 }
 
 }  // namespace
 
-// Which kernel.  The tiles, where they fill the GPU whatever the rows (a tile an expert and 256
-// columns at least), and where max_rows leaves little hope that few rows are routed.  The
-// few-rows kernel, where max_rows is few itself.  Between them the routed rows and their
-// spread decide, which the device knows: both are launched and one of them returns at once
-// (2.2 us more, for the 13 us of 64 even rows or the 100 us of 256 rows of one expert below).
-// Measured on MI355X, weights from HBM, rows kernel / tile kernel, us:
-//   128 tiles (8 experts, N 4096, K 7168, MXFP8 rows), even, a share p ~ 1 / rank^1.2, all in one:
-//     64 rows  30 / 45, 33 / 45, 34 / 31
-//     128 rows 32 / 45, 48 / 46, 65 / 38
-//     256 rows 40 / 46, 78 / 53, 128 / 39
-//   64 tiles (16 experts, N 1024, K 2048), the same: 64 rows 7 / 12, 8 / 12, 11 / 10;
-//     256 rows 8 / 12, 20 / 15, 37 / 14
-//   16 tiles (1 expert, N 4096, K 7168): 32 rows 12 / 31, 64 rows 22 / 31
-//   224 tiles (8 experts, N 7168, K 2048, MXFP4 rows): 1 row each 17 / 16, 32 rows 22 / 17
-//   512 tiles (64 experts, N 2048, K 4096, MXFP8 rows): 4 rows each 64 / 55, 32 rows 91 / 61
+// Which kernel.  The few-rows kernel reads the weights once for 32 rows, all passes at the same
+// time: its time grows with passes times columns; a tile takes its K loop's time however few
+// there are.  Measured on MI355X, weights from HBM, few-rows / tile kernel, us, by u = passes
+// times 256-column blocks:
+//   N 4096, K 7168: u 16 (32 rows, 1 expert) 13 / 31 with MXFP8 rows, 9 / 28 with MXFP4; u 64
+//     20 / 39, 16 / 31; u 128 33 / 40, 26 / 40 (8 experts: 39 / 46, 35 / 43); u 256 60 / 41, 48 / 41
+//   N 7168, K 2048: u 56 11 / 12, 9 / 11; u 112 14 / 15, 12 / 13; u 224 25 / 16, 21 / 17
+//   N 1024, K 2048: u 32 7 / 14, 6 / 16; u 128 14 / 15, 11 / 16
+//   N 2048, K 4096: u 64 15 / 24, 13 / 26; u 128 25 / 24, 21 / 26; u 256 45 / 25, 38 / 27
+//   64 experts, N 2048, K 4096, MXFP8: 4 rows each (u 512) 64 / 55, 32 rows 91 / 61
+// max_rows bounds the passes; where that leaves the choice open, both are launched, the routed
+// rows decide on the device, and one returns at once (2.2 us).  The tiles alone above 4096 rows
+// and where a pass an expert would already be too many: there are few passes then only if
+// nearly all of max_rows or most experts are unused.
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
-  const int64_t experts = std::min<int64_t>(a.groups, a.max_rows);  // at most these have rows
   const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
-  const bool tiles = nt * experts >= 192 || a.max_rows > 4096;
-  const bool rows = a.max_rows <= std::min<int64_t>(128, 64 * int64_t(a.groups));
-  if (tiles || !rows) launch_tiles(a, nt, !tiles, st);
-  if (!tiles) launch_rows(a, experts, !rows, st);
+  const int64_t passes = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kPass - 1)) / kPass);
+  const bool rows = is_few(passes, nt), tiles = !rows && (a.max_rows > 4096 || nt * std::min<int64_t>(a.groups, a.max_rows) >= 192);
+  if (!rows) launch_tiles(a, nt, !tiles, st);
+  if (!tiles) launch_rows(a, passes, nt, !rows, st);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
 }
 

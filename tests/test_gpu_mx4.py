@@ -227,7 +227,7 @@ def test_product_many_rows(counts, N, K, fmt):
 
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("K", [64, 512, 544, 640])  # scales by single bytes, 16 and 4 bytes
-@pytest.mark.parametrize("E,N", [(16, 2048), (16, 2040), (8, 2048), (8, 2056), (3, 40)])
+@pytest.mark.parametrize("E,N", [(16, 2048), (16, 2040), (8, 2048), (8, 1024), (8, 1032), (3, 40)])
 def test_product_few_rows_of_many_columns(E, N, K, fmt):
     """64, 32 and 16 columns a workgroup, whole and cut; an expert with several passes of rows
     among experts with a few or none."""
@@ -238,15 +238,15 @@ def test_product_few_rows_of_many_columns(E, N, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", FMT)
-@pytest.mark.parametrize("counts", [
-    [64], [65], [128], [129], [0, 64], [0, 65], [64, 64], [64, 65], [64] * 4, [64] * 4 + [1], [63] * 4 + [4],
-    [1] * 70 + [65] + [1] * 5, [1] * 70 + [64] + [1] * 5])
+@pytest.mark.parametrize("N,counts", [
+    (4104, [32] * 7), (4104, [32] * 8), (4104, [33] + [32] * 6), (4104, [224]), (4104, [225]), (4104, [1] * 7),
+    (4104, [0, 1, 1, 1, 1, 1, 1, 1, 0, 1]), (72, [64, 65]), (72, [4096]), (72, [1] * 70 + [65] + [1] * 5)])
 @pytest.mark.parametrize("slack", [0, 300])
-def test_product_around_the_choice_of_kernel(counts, slack, fmt):
-    """Both sides of the rows that the few-rows kernel takes, of one expert and in all, in
+def test_product_around_the_choice_of_kernel(N, counts, slack, fmt):
+    """Both sides of the passes of 32 rows times columns that the few-rows kernel takes, in
     matrices with and without rows behind the last expert's."""
-    say(f"[mx4] product choice {counts} {slack} {fmt}")
-    run_product(counts, 72, 608, fmt, torch.bfloat16, seed=sum(counts), slack=slack)
+    say(f"[mx4] product choice N={N} {counts} {slack} {fmt}")
+    run_product(counts, N, 96, fmt, torch.bfloat16, seed=sum(counts), slack=slack)
 
 
 @pytest.mark.parametrize("fmt", FMT)
