@@ -1,12 +1,15 @@
 // Tile of the grouped MX product for many rows: one workgroup of four waves computes
 // kTM x 256 outputs, 256 rows with MXFP4 activations and 128 with MXFP8, each wave half of
-// the rows by 128 columns (32 x 32 MFMA blocks of v_mfma_scale_f32_32x32x64_f8f6f4).
+// the rows by 128 columns (32 x 32 MFMA blocks of v_mfma_scale_f32_32x32x64_f8f6f4).  Bound
+// by the card's power: 16,384 rows, N 4096, K 7168 in MXFP4 on MI355X take 250-275 us (3.5-3.85
+// PFLOP/s) at 1.9 of 2.4 GHz with the matrix cores half busy; their instructions alone, on
+// random data, 162 us.
 //
 // A K step is 256 elements: 32 KB of A and 32 KB of B, whole 128-byte lines, moved by
 // direct-to-LDS loads through a ring of two stages.  Four waves of 128 x 128 read 128 KB of
 // LDS a step (eight waves of 128 x 64 would read 192 KB: with the 64 KB the loads write,
 // the LDS would then be as busy as the MFMA).  One wave a SIMD leaves 512 registers: 256
-// accumulators and the fragments of two slices.
+// accumulators and the fragments of the step's four slices.
 //
 // Operand layout of 32 x 32 x 64, as measured: lane l holds row l % 32; with h = l / 32, a
 // 4-bit operand's 16 bytes are K block h (32 elements), an 8-bit operand's first 16 bytes
@@ -30,8 +33,10 @@
 // Rows past the expert's last are read as its last one (never stored); weight rows past N
 // as the last one; chunks past K as zeros (an out-of-range offset reads no memory), with
 // zero scales.
+//
 // Tiles of few rows (the end of an expert's rows, or all of them) run with fewer row blocks
-// a wave: IB = 1 covers 64 rows, 2 covers 128, 4 covers 256.
+// a wave: IB = 1 covers 64 rows, 2 covers 128, 4 covers 256.  Where whole tiles would leave
+// CUs idle, tiles of half the rows and columns (JB = 2).
 //
 // A workgroup walks several tiles: the next one's first loads are in flight while the current
 // one's results are stored, through LDS that those loads leave free.
@@ -42,14 +47,15 @@ namespace mok {
 namespace mx4 {
 
 constexpr int kThr = 256;
-constexpr int kTN = 256;
-constexpr int kStep = 256;                // K elements a step
 constexpr int kRing = 8;                  // steps of scales in LDS
 constexpr uint32_t kStageB = 32768;       // bytes of one operand's stage
 constexpr uint32_t kPastRange = 0x80000000u;
 
-template <bool A8>
-constexpr int tile_rows() { return A8 ? 128 : 256; }
+// JB: blocks of 32 columns a wave, 4 for whole tiles, 2 for tiles of half the rows and columns.
+template <int JB>
+constexpr int tile_cols() { return 64 * JB; }
+template <bool A8, int JB>
+constexpr int tile_rows() { return (A8 ? 32 : 64) * JB; }
 
 static __shared__ __align__(1024) v4u g_a[2 * kStageB / 16];
 static __shared__ __align__(1024) v4u g_b[2 * kStageB / 16];
@@ -105,14 +111,16 @@ __device__ __forceinline__ void lds_load16(const i32x4_t& rsrc, uint32_t voff, u
 // SHIFT: some row's scales do not start at a 16-byte address or are not whole 16-byte pieces.
 //
 // Where a tile's operands come from, and its direct-to-LDS loads.
-template <bool A8, bool SHIFT>
+template <bool A8, bool SHIFT, int JB>
 struct Source {
-  static constexpr int kTM = tile_rows<A8>();
-  static constexpr int kSA = kTM / 128;  // 16-byte loads of A's scales a wave
+  static constexpr int kTM = tile_rows<A8, JB>(), kTN = tile_cols<JB>();
+  static constexpr int kSRows = kTM < 128 ? 128 : kTM;         // rows of A in the scale ring
+  static constexpr int kSA = kSRows / 128, kSB = kTN / 128;    // 16-byte loads of scales a wave
+  static constexpr int kQ = 2 * JB;                            // data loads of A, and of B, at most
   i32x4_t ra, rb;            // codes of A from the tile's first row, of the expert's B
   i32x4_t rsa, rsb;          // their scales
-  uint32_t oa[8], ob[8];     // byte offsets of this lane's chunks in step 0
-  uint32_t osa[kSA], osb[2];  // this lane's pieces of the scales
+  uint32_t oa[kQ], ob[kQ];   // byte offsets of this lane's chunks in step 0
+  uint32_t osa[kSA], osb[kSB];  // this lane's pieces of the scales
   uint32_t sha, shb;          // bytes of its rows' first dword before their first scale
   int nblk;                  // K blocks
   int ca, cb;                // this lane's chunk of an A and of a B row
@@ -126,7 +134,7 @@ struct Source {
     ca = A8 ? ((l & 15) ^ (((w & 3) * 4 + (l >> 4)) & 15)) : ((l & 7) ^ (l >> 3) ^ (w & 1));
     cb = (l & 7) ^ (l >> 3) ^ (w & 1);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kQ; ++q) {
       const int ar = A8 ? (q * 4 + w) * 4 + (l >> 4) : (q * 4 + w) * 8 + (l >> 3);
       const int br = (q * 4 + w) * 8 + (l >> 3);
       oa[q] = uint32_t(int64_t(min(ar, rows - 1)) * p.ld_a) + ca * 16;
@@ -145,7 +153,7 @@ struct Source {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (i < kSA) osa[i] = ((la + uint32_t(min((w * kSA + i) * 32 + row, rows - 1) * p.ld_as)) & ~3u) + piece;
-      osb[i] = ((lb + uint32_t(min(n0 + w * 64 + i * 32 + row, p.n - 1)) * uint32_t(nblk)) & ~3u) + piece;
+      if (i < kSB) osb[i] = ((lb + uint32_t(min(n0 + (w * kSB + i) * 32 + row, p.n - 1)) * uint32_t(nblk)) & ~3u) + piece;
     }
   }
 
@@ -171,11 +179,12 @@ struct Source {
     const int at = quad * 32, half = quad & 1, i = part & 1;
     const int last = SHIFT ? nblk + 3 : nblk;  // no scale of a row lies in a piece from here on
     const uint32_t past = at + 16 * (((l >> 3) ^ (l >> 4)) & 1) < last ? 0u : kPastRange;
-    if (part >= 2)
-      lds_load16(rsb, (osb[i] + at) | past, 0, lds_addr(g_sb) + uint32_t(half * 512 + (2 * w + i) * 64) * 16);
-    else if (i < kSA)
+    if (part >= 2 && i < kSB)
+      lds_load16(rsb, (osb[i < kSB ? i : 0] + at) | past, 0,
+                 lds_addr(g_sb) + uint32_t(half * 2 * kTN + (kSB * w + i) * 64) * 16);
+    if (part < 2 && i < kSA)
       lds_load16(rsa, (osa[i < kSA ? i : 0] + at) | past, 0,
-                 lds_addr(g_sa) + uint32_t(half * 2 * kTM + (kSA * w + i) * 64) * 16);
+                 lds_addr(g_sa) + uint32_t(half * 2 * kSRows + (kSA * w + i) * 64) * 16);
   }
 
   // The same with what is wave-uniform in scalar registers again (values that were chosen on
@@ -199,7 +208,7 @@ struct Source {
 
   // The scales of the first four steps, then the data of step 0, then of step 1: kAhead loads
   // a wave may be in flight when step 0 has landed.
-  static constexpr int kAhead = 16;
+  static constexpr int kAhead = 2 * kQ;
   __device__ __forceinline__ void begin() const {
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -207,7 +216,7 @@ struct Source {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) issue(ks, q, ks * kStageB);
+      for (int q = 0; q < 2 * kQ; ++q) issue(ks, q < kQ ? q : q - kQ + 8, ks * kStageB);
     asm volatile("" ::: "memory");
   }
 };
@@ -229,11 +238,11 @@ __device__ __forceinline__ void wait_all_but(int n) {
   else wait_vmcnt<0>();
 }
 
-template <bool A8, bool SHIFT, int IB>
+// IB, JB: 32-row blocks of A and of B a wave.
+template <bool A8, bool SHIFT, int IB, int JB>
 struct Tile {
-  typedef Source<A8, SHIFT> Src;
-  static constexpr int kTM = tile_rows<A8>();
-  static constexpr int kJB = 4;  // 32-row blocks of B a wave; IB: of A
+  typedef Source<A8, SHIFT, JB> Src;
+  static constexpr int kJB = JB;
   static constexpr int kQA = A8 ? 4 * IB : 2 * IB;  // A loads a step
 
   uint32_t la[4];  // LDS byte address of the A fragment of slice s, block 0, stage 0
@@ -248,7 +257,7 @@ struct Tile {
     for (int s = 0; s < 4; ++s) {
       la[s] = lds_addr(g_a) + (A8 ? uint32_t(wm * 32 * IB + r) * 256 + (((2 * s + h) ^ (r & 15)) * 16)
                                   : uint32_t(wm * 32 * IB + r) * 128 + (((4 * h + s) ^ sw) * 16));
-      lb[s] = lds_addr(g_b) + uint32_t(wn * 128 + r) * 128 + (((4 * h + s) ^ sw) * 16);
+      lb[s] = lds_addr(g_b) + uint32_t(wn * 32 * JB + r) * 128 + (((4 * h + s) ^ sw) * 16);
     }
 #pragma unroll
     for (int i = 0; i < IB; ++i)
@@ -267,7 +276,7 @@ struct Tile {
     const int t = threadIdx.x, l = t & 63, w = t >> 6, r = l & 31;
     const int place = 2 * (r & ~7) + (r & 7) + 8 * (((d >> 2) ^ (r >> 3)) & 1);
     const int half = (d >> 3) & 1;
-    return 4 * ((b ? half * 512 + (w & 1) * 256 : half * 2 * kTM + (w >> 1) * 64 * IB) + place) + (d & 3);
+    return 4 * ((b ? half * 2 * Src::kTN + (w & 1) * 64 * JB : half * 2 * Src::kSRows + (w >> 1) * 64 * IB) + place) + (d & 3);
   }
   // Dwords of the ring for this lane's scales of step ks in N row blocks of A or of B, and, where
   // they are shifted together, the next ones.
@@ -372,7 +381,7 @@ struct Tile {
       for (int r = 0; r < IB + kJB; ++r) read_one(f[s], s, r, 0);
     const int steps = (src.nblk + 7) / 8;
     uint32_t cur = 0;  // stage of step ks
-    constexpr int kD = kQA + 8;  // data loads a step
+    constexpr int kD = kQA + Src::kQ;  // data loads a step
     constexpr int kD1 = kD / 2, kD2 = kD - kD1;
     for (int ks = 0; ks < steps; ++ks) {
       slice<0, 3, 0, 0>(src, f[0], f[3], sc, cur, ks, cur);
@@ -461,7 +470,7 @@ struct Tile {
         for (int x = 0; x < 4; ++x) {
           const int row = (wm * IB + i) * 32 + 8 * x + rr;
           const int chunk = (l & 7) ^ rsw ^ (x & 1);
-          const int col = n0 + wn * 128 + 32 * j0 + chunk * (16 / kSize);
+          const int col = n0 + wn * 32 * JB + 32 * j0 + chunk * (16 / kSize);
           const v4u v = *reinterpret_cast<lds_v4u*>(uintptr_t(area + uint32_t(8 * x + rr) * 128 + (l & 7) * 16));
           const bool in = row < rows && col < p.n;
           buf_st16<kCpolStream>(ro, in ? uint32_t(row) * uint32_t(p.ld_out) * kSize + col * kSize : kPastRange, v);

@@ -44,6 +44,7 @@ template <int TM>
 struct Tiling {
   int lo, hi, incl;  // this lane's expert of the current 64: rows, m-tiles up to it
   int total;         // m-tiles of all experts
+  int active;        // experts with rows
   int tiles;         // this lane's expert's
 
   __device__ __forceinline__ void scan(const GroupedArgs& p, int e0) {
@@ -61,10 +62,11 @@ struct Tiling {
     }
   }
   __device__ __forceinline__ void init(const GroupedArgs& p) {
-    total = 0;
+    total = active = 0;
     for (int e0 = 0; e0 < p.groups; e0 += 64) {
       scan(p, e0);
       total += __builtin_amdgcn_readlane(incl, 63);
+      active += __popcll(__ballot(tiles > 0));
     }
   }
   // m-tile m < total: its expert, first row and rows
@@ -87,10 +89,12 @@ struct Tiling {
   }
 };
 
-// Whether the few-rows kernel has the call: passes of at most 32 rows times 256-column blocks (the
-// bound is explained at launch_grouped_mx4).
+// Whether the few-rows kernel has the call: passes of at most 32 rows times 256-column blocks, an
+// expert's passes after its first counted 4/3 (the bound is explained at launch_grouped_mx4).
 constexpr int kPass = 32, kFew = 128;
-__host__ __device__ __forceinline__ bool is_few(int64_t passes, int nt) { return passes * nt <= kFew; }
+__host__ __device__ __forceinline__ bool is_few(int64_t passes, int64_t active, int nt) {
+  return (4 * passes - active) * nt <= 3 * kFew;
+}
 
 // ------------------------------------------------------------------------------------
 // Few rows an expert (decoding): bound by reading the weights once.
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, int max_
   Tiling<kPass> til;
   til.init(p);
   til.total = min(til.total, max_passes);  // more only where ranges overlap
-  if (both && !is_few(til.total, nt)) return;
+  if (both && !is_few(til.total, til.active, nt)) return;
   if (W == 8) return rows_item<A8, SHIFT, 1, W>(p, til, s_part, blockIdx.x);
   if ((p.n + 63) / 64 * til.total >= 256) rows_item<A8, SHIFT, 4, 4>(p, til, s_part, blockIdx.x);
   else if ((p.n + 31) / 32 * til.total >= 256) rows_item<A8, SHIFT, 2, 4>(p, til, s_part, blockIdx.x);
@@ -297,30 +301,24 @@ __device__ __forceinline__ void tile_of(int t, int mt, int nt, int* m, int* n) {
   *m = g * kGroupM + r - *n * gm;
 }
 
-// A workgroup's next tile: workgroups go to the eight XCDs in turn, and XCD x takes the x-th
-// eighth of the tiles, whose operands its L2 then holds; its workgroups take them in turn.
-template <bool A8, bool OUT32, bool SHIFT>
-__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt, bool both) {
-  if (both) {
-    Tiling<kPass> passes;
-    passes.init(p);
-    if (is_few(passes.total, nt)) return;
-  }
-  constexpr int TM = mx4::tile_rows<A8>();
-  Tiling<TM> til;
-  til.init(p);
-  til.total = min(til.total, max_mt);  // more only where ranges overlap
+// The tiles of 64 JB columns and the rows of til, by workgroups that take several: workgroups go to
+// the eight XCDs in turn, and XCD x takes the x-th eighth of the tiles, whose operands its L2
+// then holds; its workgroups take them in turn.
+template <bool A8, bool OUT32, bool SHIFT, int JB>
+__device__ __forceinline__ void walk_tiles(const GroupedArgs& p, Tiling<mx4::tile_rows<A8, JB>()>& til) {
+  constexpr int TN = mx4::tile_cols<JB>(), kIB = A8 ? JB / 2 : JB;
+  const int nt = (p.n + TN - 1) / TN;
   const int total = til.total * nt, per = (total + 7) / 8;
   const int first = int(blockIdx.x & 7) * per, end = min(first + per, total);
   int t = first + int(blockIdx.x >> 3);
   if (t >= end) return;
-  mx4::Source<A8, SHIFT> src;
+  mx4::Source<A8, SHIFT, JB> src;
   int m, n, e, rows;
   int64_t r0;
   auto open = [&]() __attribute__((always_inline)) {
     tile_of(t, til.total, nt, &m, &n);
     til.find(p, m, &e, &r0, &rows);
-    src.init(p, e, r0, rows, n * mx4::kTN);
+    src.init(p, e, r0, rows, n * TN);
     src.begin();
   };
   open();
@@ -328,16 +326,39 @@ __global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int m
   auto run = [&](auto tile) __attribute__((always_inline)) {
     tile.run(src, stores);
     const int64_t r = r0;
-    const int have = rows, n0 = n * mx4::kTN;
+    const int have = rows, n0 = n * TN;
     t += int(gridDim.x >> 3);
     if (t < end) open();
     tile.template store<OUT32>(p, r, have, n0);
     stores = tile.template kStores<OUT32>;
   };
   while (t < end) {
-    if (rows <= 64) run(mx4::Tile<A8, SHIFT, 1>());
-    else if (A8 || rows <= 128) run(mx4::Tile<A8, SHIFT, 2>());
-    else run(mx4::Tile<A8, SHIFT, A8 ? 2 : 4>());
+    if (kIB == 1 || rows <= 64) run(mx4::Tile<A8, SHIFT, 1, JB>());
+    else if (kIB == 2 || rows <= 128) run(mx4::Tile<A8, SHIFT, kIB < 2 ? 1 : 2, JB>());
+    else run(mx4::Tile<A8, SHIFT, kIB, JB>());
+  }
+}
+
+// Tiles of half the rows and columns where these make one a CU at most: four times the
+// workgroups, each with a fourth of the work of a K step.  Measured on MI355X, whole tiles /
+// halves, us: 512 MXFP4 rows of one expert, N 4096, K 7168 43 / 27; 2000 rows of 4, N 2048, K 4096
+// 30.6 / 19.8 (MXFP8, 512 tiles of half the size, 29 / 32); 1024 rows of 8, N 4096, K 7168 50 / 39.
+template <bool A8, bool OUT32, bool SHIFT>
+__global__ __launch_bounds__(mx4::kThr) void k_grouped_tile(GroupedArgs p, int max_mt, int nt, bool both) {
+  if (both) {
+    Tiling<kPass> passes;
+    passes.init(p);
+    if (is_few(passes.total, passes.active, nt)) return;
+  }
+  Tiling<mx4::tile_rows<A8, 2>()> halves;
+  halves.init(p);
+  if (int64_t(halves.total) * ((p.n + mx4::tile_cols<2>() - 1) / mx4::tile_cols<2>()) <= 256) {
+    walk_tiles<A8, OUT32, SHIFT, 2>(p, halves);
+  } else {
+    Tiling<mx4::tile_rows<A8, 4>()> til;
+    til.init(p);
+    til.total = min(til.total, max_mt);  // more only where ranges overlap
+    walk_tiles<A8, OUT32, SHIFT, 4>(p, til);
   }
 }
 
@@ -348,10 +369,11 @@ bool scales_whole(const GroupedArgs& a, uintptr_t piece) {
 }
 
 void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
-  const int tm = a.a8 ? mx4::tile_rows<true>() : mx4::tile_rows<false>();
+  const int tm = a.a8 ? mx4::tile_rows<true, 4>() : mx4::tile_rows<false, 4>();
   // at most this many m-tiles: every expert may end inside one
   const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
-  const dim3 grid(unsigned(std::min<int64_t>((mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
+  // (a tile makes four at most of half the rows and columns)
+  const dim3 grid(unsigned(std::min<int64_t>((4 * mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
   auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, int(mt), nt, both); };
   auto form = [&](auto shift) {
     constexpr bool SHIFT = decltype(shift)::value;
@@ -399,15 +421,17 @@ void launch_rows(const GroupedArgs& a, int64_t passes, int nt, bool both, hipStr
 //   N 7168, K 2048: u 56 11 / 12, 9 / 11; u 112 14 / 15, 12 / 13; u 224 25 / 16, 21 / 17
 //   N 1024, K 2048: u 32 7 / 14, 6 / 16; u 128 14 / 15, 11 / 16
 //   N 2048, K 4096: u 64 15 / 24, 13 / 26; u 128 25 / 24, 21 / 26; u 256 45 / 25, 38 / 27
+//   (since then the tiles of half the size take that last tile time to 19, 18, and of 40, 40 to
+//   about 29, 27: an expert's later passes, which the tiles do not repeat, count 4/3)
 //   64 experts, N 2048, K 4096, MXFP8: 4 rows each (u 512) 64 / 55, 32 rows 91 / 61
 // max_rows bounds the passes; where that leaves the choice open, both are launched, the routed
 // rows decide on the device, and one returns at once (2.2 us).  The tiles alone above 4096 rows
 // and where a pass an expert would already be too many: there are few passes then only if
 // nearly all of max_rows or most experts are unused.
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
-  const int nt = (a.n + mx4::kTN - 1) / mx4::kTN;
+  const int nt = (a.n + mx4::tile_cols<4>() - 1) / mx4::tile_cols<4>();
   const int64_t passes = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kPass - 1)) / kPass);
-  const bool rows = is_few(passes, nt), tiles = !rows && (a.max_rows > 4096 || nt * std::min<int64_t>(a.groups, a.max_rows) >= 192);
+  const bool rows = is_few(passes, 0, nt), tiles = !rows && (a.max_rows > 4096 || nt * std::min<int64_t>(a.groups, a.max_rows) >= 192);
   if (!rows) launch_tiles(a, nt, !tiles, st);
   if (!tiles) launch_rows(a, passes, nt, !rows, st);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;

@@ -240,7 +240,8 @@ def test_product_few_rows_of_many_columns(E, N, K, fmt):
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("N,counts", [
     (4104, [32] * 7), (4104, [32] * 8), (4104, [33] + [32] * 6), (4104, [224]), (4104, [225]), (4104, [1] * 7),
-    (4104, [0, 1, 1, 1, 1, 1, 1, 1, 0, 1]), (72, [64, 65]), (72, [4096]), (72, [1] * 70 + [65] + [1] * 5)])
+    (4104, [0, 1, 1, 1, 1, 1, 1, 1, 0, 1]), (72, [64, 65]), (72, [4096]), (72, [1] * 70 + [65] + [1] * 5),
+    (4104, [160]), (4104, [192]), (2048, [32] * 16), (2048, [64] * 8), (2048, [256, 64, 32])])
 @pytest.mark.parametrize("slack", [0, 300])
 def test_product_around_the_choice_of_kernel(N, counts, slack, fmt):
     """Both sides of the passes of 32 rows times columns that the few-rows kernel takes, in
@@ -271,6 +272,17 @@ def test_product_several_tiles_a_workgroup(N, K, dtype, fmt):
     """More tiles than the GPU has workgroups for, of 1 to 256 rows, one after the other."""
     say(f"[mx4] product tiles N={N} K={K} {dtype} {fmt}")
     run_product([700, 3, 0, 129, 65, 1000, 257, 12], N, K, fmt, dtype, seed=N + K + 4, pad=K == 288)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("K", [96, 512, 1056, 2080])
+@pytest.mark.parametrize("counts,N", [([500, 70, 0, 129, 64, 1], 1000), ([128] * 8, 4096), ([128] * 8 + [1], 4096),
+                                      ([1000], 520), ([64] * 16, 2040)])
+def test_product_tiles_of_half_the_size(counts, N, K, dtype, fmt):
+    """One of them a CU at most, on both sides of that."""
+    say(f"[mx4] product halves {counts} N={N} K={K} {dtype} {fmt}")
+    run_product(counts, N, K, fmt, dtype, seed=N + K + 5)
 
 
 @pytest.mark.parametrize("fmt", FMT)
