@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <initializer_list>
@@ -212,6 +213,11 @@ PyObject* do_unpermute_bwd(PyObject* const* a) {
   return r ? Py_BuildValue("(ON)", a[4], r) : nullptr;
 }
 
+// The element type that a torch dtype names; Undefined where it is none.
+at::ScalarType dtype_of(PyObject* o) {
+  return THPDtype_Check(o) ? reinterpret_cast<THPDtype*>(o)->scalar_type : at::ScalarType::Undefined;
+}
+
 std::vector<int64_t> with_last(const at::Tensor& t, int64_t last) {
   std::vector<int64_t> s = t.sizes().vec();
   s.back() = last;
@@ -242,51 +248,59 @@ PyObject* do_quantize(PyObject* const* a) {
   return x && y ? Py_BuildValue("(NN)", x, y) : nullptr;
 }
 
-// codes, scales, out
+// codes, scales, dtype (of an output made here), out
 PyObject* do_dequantize(PyObject* const* a) {
-  const at::Tensor *codes = tensor(a[0]), *scales = tensor(a[1]), *out = tensor(a[2]);
+  const at::Tensor *codes = tensor(a[0]), *scales = tensor(a[1]);
   Call c(codes);
   Matrix mc, mq, mo;
   void* st;
-  if (!rows_of(c, codes, &mc, false) || !rows_of(c, scales, &mq, false) || !rows_of(c, out, &mo, true))
+  const at::ScalarType type = dtype_of(a[2]);
+  if (!rows_of(c, codes, &mc, false) || !rows_of(c, scales, &mq, false) || mc.cols > INT32_MAX / 2 ||
+      (a[3] == Py_None && type == at::ScalarType::Undefined) || !c.stream(&st))
     return none();
-  const int ty = type_of(*out);
+  Output out(a[3], [&] { return at::empty(with_last(*codes, 2 * mc.cols), codes->options().dtype(type)); });
+  if (!rows_of(c, out.t, &mo, true)) return none();
+  const int ty = type_of(*out.t);
   if (ty < 0 || codes->scalar_type() != at::kByte || scales->scalar_type() != at::kByte || mc.cols == 0 ||
       mc.cols % 16 || mq.cols != mc.cols / 16 || mo.cols != 2 * mc.cols || mq.rows != mc.rows ||
-      mo.rows != mc.rows || !apart(mo.s, {mc.s, mq.s}) || !c.stream(&st))
+      mo.rows != mc.rows || !apart(mo.s, {mc.s, mq.s}))
     return none();
   if (g_fn.dequantize_mx4(static_cast<uint8_t*>(mc.p), mc.ld, static_cast<uint8_t*>(mq.p), mq.ld, mc.rows,
                           int32_t(mo.cols), ty, mo.p, mo.ld, st) != MOK_OK)
     return none();
-  return same(a[2]);
+  return out.result();
 }
 
-// a, a_scales, offsets, b, b_scales, out
+// a, a_scales, offsets, b, b_scales, dtype (of an output made here), out
 PyObject* do_grouped(PyObject* const* v) {
   const at::Tensor *a = tensor(v[0]), *as = tensor(v[1]), *off = tensor(v[2]), *b = tensor(v[3]),
-                   *bs = tensor(v[4]), *out = tensor(v[5]);
+                   *bs = tensor(v[4]);
   Call c(a);
   Matrix ma, mas, mo;
   Span so, sb, sbs;
   if (!c.on_device(b) || b->dim() != 3) return none();
   const int64_t E = b->size(0), N = b->size(1), half = b->size(2), K = 2 * half;
   if (half == 0 || half % 16 || !matrix(c, a, &ma, false) || !matrix(c, as, &mas, false) ||
-      !matrix(c, out, &mo, true) || !flat(c, b, {E, N, half}, at::kByte, &sb) ||
-      !flat(c, bs, {E, N, K / 32}, at::kByte, &sbs) || !flat(c, off, {E + 1}, at::kInt, &so))
+      !flat(c, b, {E, N, half}, at::kByte, &sb) || !flat(c, bs, {E, N, K / 32}, at::kByte, &sbs) ||
+      !flat(c, off, {E + 1}, at::kInt, &so))
     return none();
-  const int ty = type_of(*out);
   void* st;
+  const at::ScalarType type = dtype_of(v[5]);
+  if ((v[6] == Py_None && type != at::kBFloat16 && type != at::kFloat) || !c.stream(&st)) return none();
+  Output out(v[6], [&] { return at::empty({ma.rows, N}, a->options().dtype(type)); });
+  if (!matrix(c, out.t, &mo, true)) return none();
+  const int ty = type_of(*out.t);
   if ((ty != MOK_TYPE_BF16 && ty != MOK_TYPE_FP32) || a->scalar_type() != at::kByte ||
       as->scalar_type() != at::kByte || (ma.cols != half && ma.cols != K) || mas.rows != ma.rows ||
       mas.cols != K / 32 || mo.rows != ma.rows || mo.cols != N || E > INT32_MAX || N > INT32_MAX ||
-      K > INT32_MAX || !apart(mo.s, {ma.s, mas.s, so, sb, sbs}) || !c.stream(&st))
+      K > INT32_MAX || !apart(mo.s, {ma.s, mas.s, so, sb, sbs}))
     return none();
   if (g_fn.grouped_mx4(ma.cols == half ? MOK_MX_E2M1 : MOK_MX_E4M3, static_cast<uint8_t*>(ma.p), ma.ld,
                        static_cast<uint8_t*>(mas.p), mas.ld, ma.rows, at_ptr<int32_t>(so), int32_t(E),
                        at_ptr<uint8_t>(sb), at_ptr<uint8_t>(sbs), int32_t(N), int32_t(K), ty, mo.p, mo.ld,
                        st) != MOK_OK)
     return none();
-  return same(v[5]);
+  return out.result();
 }
 
 // A call with `want` arguments; a C++ exception (a tensor without strides or storage) is a
@@ -346,8 +360,8 @@ PyMethodDef g_methods[] = {
     {"unpermute", method<entry<4, f_unpermute>>(), METH_FASTCALL, nullptr},
     {"unpermute_backward", method<entry<6, do_unpermute_bwd>>(), METH_FASTCALL, nullptr},
     {"quantize_mx4", method<entry<3, do_quantize>>(), METH_FASTCALL, nullptr},
-    {"dequantize_mx4", method<entry<3, do_dequantize>>(), METH_FASTCALL, nullptr},
-    {"grouped_mx4", method<entry<6, do_grouped>>(), METH_FASTCALL, nullptr},
+    {"dequantize_mx4", method<entry<4, do_dequantize>>(), METH_FASTCALL, nullptr},
+    {"grouped_mx4", method<entry<7, do_grouped>>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

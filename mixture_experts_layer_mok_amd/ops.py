@@ -305,8 +305,8 @@ def quantize_mx4(src, codes=None, scales=None, stream=None):
 def dequantize_mx4(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values of MXFP4 codes [..., K / 2] and scales [..., K / 32], [..., K] in `dtype` (or
     in out's)."""
-    if stream is None and out is not None and _fast is not None:
-        done = _fast.dequantize_mx4(codes, scales, out)
+    if stream is None and _fast is not None:
+        done = _fast.dequantize_mx4(codes, scales, dtype, out)
         if done is not None:
             return done
     if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or codes.shape[-1] % 16 or \
@@ -338,8 +338,8 @@ def grouped_mx4(a, a_scales, offsets, b, b_scales, out=None, dtype=torch.bfloat1
     (mok_quantize_mx), uint8, with a_scales [max_rows, K / 32]; offsets [E + 1] int32, on the
     device; b [E, N, K / 2] MXFP4 codes with b_scales [E, N, K / 32], contiguous; out
     [max_rows, N] bf16 or fp32."""
-    if stream is None and out is not None and _fast is not None:
-        done = _fast.grouped_mx4(a, a_scales, offsets, b, b_scales, out)
+    if stream is None and _fast is not None:
+        done = _fast.grouped_mx4(a, a_scales, offsets, b, b_scales, dtype, out)
         if done is not None:
             return done
     if not isinstance(b, torch.Tensor) or b.dim() != 3 or b.shape[2] % 16 or b.shape[2] == 0:

@@ -334,3 +334,21 @@ def test_strides_of_no_rows_say_nothing():
         ops.permute_backward(rows, torch.full((3, 2), -1, dtype=torch.int32))
     with pytest.raises(ValueError, match="contiguous"):
         ops.permute_backward(torch.empty(5, 64).t(), torch.full((3, 2), -1, dtype=torch.int32))
+
+
+def test_the_extension_module_passes_on_what_is_not_in_order():
+    from mixture_experts_layer_mok_amd import _fast
+
+    x, i = torch.zeros(4, 64), torch.zeros(4, 2, dtype=torch.int32)
+    counts = dict(permute=3, permute_backward=3, unpermute=4, unpermute_backward=6, quantize_mx4=3,
+                  dequantize_mx4=4, grouped_mx4=7)
+    for name, n in counts.items():
+        f = getattr(_fast, name)
+        assert f() is None and f(*[None] * n) is None and f(*[3] * n) is None
+        assert f(*[x] * n) is None and f(*[i] * n) is None and f(*[x] * (n + 1)) is None
+    with pytest.raises(TypeError):
+        _fast.bind(1, 2)
+    with pytest.raises(TypeError):
+        _fast.bind(len, len, *["a"] * 7)
+    with pytest.raises(ValueError):
+        _fast.bind(len, len, *[0] * 7)
