@@ -99,13 +99,13 @@ __host__ __device__ __forceinline__ bool is_few(int64_t passes, int64_t active, 
 // ------------------------------------------------------------------------------------
 // Few rows an expert (decoding): bound by reading the weights once.
 // ------------------------------------------------------------------------------------
-// One workgroup of W waves: 16 NB columns of one expert and at most 32 of its rows (a pass).
+// One workgroup of four waves: 16 NB columns of one expert and at most 32 of its rows (a pass).
 // The K chunks of 256 (two MFMA steps) are dealt to the waves; each loads its next chunk
 // before it multiplies the current one, straight into registers (a weight is used by one
 // wave only, so LDS would add a copy), and the waves' sums are joined through LDS in wave
 // order.  Loads past K, past the rows and past N read zeros (zero codes, zero scales: no
 // product).
-constexpr int kChunk = 256;
+constexpr int kChunk = 256, kWaves = 4;
 
 // The eight scale bytes of a row's chunk: two dwords, or, where some row's scales do not start
 // at an 8-byte address or are not whole pieces of 8 (SHIFT), the three that they lie in (64 rows
@@ -207,7 +207,7 @@ struct Chunk {
   }
 };
 
-template <bool A8, bool SHIFT, int NB, int W, int MB>
+template <bool A8, bool SHIFT, int NB, int MB>
 __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part, int64_t r0, int valid,
                                           rsrc_t rb, rsrc_t rbs, uint32_t lb, int n0) {
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -226,8 +226,8 @@ __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part,
   if (w < chunks) {
     Chunk<A8, SHIFT, NB, MB> cur, nxt;
     cur.load(p, rb, rbs, lb, ra, ras, la, valid, w);
-    for (int ck = w; ck < chunks; ck += W) {
-      nxt.load(p, rb, rbs, lb, ra, ras, la, valid, ck + W);  // past the last: reads nothing
+    for (int ck = w; ck < chunks; ck += kWaves) {
+      nxt.load(p, rb, rbs, lb, ra, ras, la, valid, ck + kWaves);  // past the last: reads nothing
       cur.multiply(acc, shb, sha, nblk - 8 * ck);
       cur = nxt;
     }
@@ -238,11 +238,11 @@ __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part,
 #pragma unroll
     for (int j = 0; j < NB; ++j) s_part[(w * MB * NB + m * NB + j) * 64 + lane] = acc[m][j];
   __syncthreads();
-  for (int i = threadIdx.x; i < MB * NB * 64; i += W * 64) {
+  for (int i = threadIdx.x; i < MB * NB * 64; i += kWaves * 64) {
     const int blk = i >> 6, l = i & 63, m = blk / NB, j = blk % NB;
     f32x4_t c = s_part[i];
 #pragma unroll
-    for (int u = 1; u < W; ++u) c += s_part[u * MB * NB * 64 + i];
+    for (int u = 1; u < kWaves; ++u) c += s_part[u * MB * NB * 64 + i];
     const int row = 16 * m + (l & 15), col = n0 + 16 * j + 4 * (l >> 4);
     if (row < valid && col < p.n) {
       const int64_t at = (r0 + row) * p.ld_out + col;
@@ -257,7 +257,7 @@ __device__ __forceinline__ void rows_pass(const GroupedArgs& p, f32x4_t* s_part,
 
 // Item t: passes of all experts times blocks of 16 NB columns, columns first, so that the passes
 // that read the same weights run on the same XCD, at about the same time.
-template <bool A8, bool SHIFT, int NB, int W>
+template <bool A8, bool SHIFT, int NB>
 __device__ __forceinline__ void rows_item(const GroupedArgs& p, Tiling<kPass>& til, f32x4_t* s_part, int t) {
   const int ncb = (p.n + 16 * NB - 1) / (16 * NB);
   const int m = t / ncb, n0 = (t - m * ncb) * 16 * NB, ncols = min(16 * NB, p.n - n0);
@@ -270,25 +270,24 @@ __device__ __forceinline__ void rows_item(const GroupedArgs& p, Tiling<kPass>& t
   const uint8_t* bs = p.bs + brow * (p.k / 32);
   const rsrc_t rbs = scales_rsrc(bs, uint32_t(ncols * (p.k / 32)));
   const uint32_t lb = uint32_t(reinterpret_cast<uintptr_t>(bs) & 3);
-  if (rows <= 16) rows_pass<A8, SHIFT, NB, W, 1>(p, s_part, r0, rows, rb, rbs, lb, n0);
-  else rows_pass<A8, SHIFT, NB, W, 2>(p, s_part, r0, rows, rb, rbs, lb, n0);
+  if (rows <= 16) rows_pass<A8, SHIFT, NB, 1>(p, s_part, r0, rows, rb, rbs, lb, n0);
+  else rows_pass<A8, SHIFT, NB, 2>(p, s_part, r0, rows, rb, rbs, lb, n0);
 }
 
 // Columns a workgroup: the most that leave an item a CU (every item reads its rows again).
 // Measured on MI355X with a bound of 256 / 512 items, us: 128 rows of one expert, N 4096, K 7168,
 // MXFP8 20 / 25 (45 with 16 columns); 256 rows of 8, N 2048, K 4096 15.6 / 19.2.  64 rows of 8
 // experts, N 4096, K 7168, MXFP8: 64 columns 32, 32 39, 16 42.
-template <bool A8, bool SHIFT, int W>
-__global__ __launch_bounds__(W * 64) void k_grouped_rows(GroupedArgs p, int max_passes, int nt, bool both) {
-  __shared__ f32x4_t s_part[W * 2 * (W == 8 ? 1 : 4) * 64];
+template <bool A8, bool SHIFT>
+__global__ __launch_bounds__(kWaves * 64) void k_grouped_rows(GroupedArgs p, int max_passes, int nt, bool both) {
+  __shared__ f32x4_t s_part[kWaves * 2 * 4 * 64];
   Tiling<kPass> til;
   til.init(p);
   til.total = min(til.total, max_passes);  // more only where ranges overlap
   if (both && !is_few(til.total, til.active, nt)) return;
-  if (W == 8) return rows_item<A8, SHIFT, 1, W>(p, til, s_part, blockIdx.x);
-  if ((p.n + 63) / 64 * til.total >= 256) rows_item<A8, SHIFT, 4, 4>(p, til, s_part, blockIdx.x);
-  else if ((p.n + 31) / 32 * til.total >= 256) rows_item<A8, SHIFT, 2, 4>(p, til, s_part, blockIdx.x);
-  else rows_item<A8, SHIFT, 1, 4>(p, til, s_part, blockIdx.x);
+  if ((p.n + 63) / 64 * til.total >= 256) rows_item<A8, SHIFT, 4>(p, til, s_part, blockIdx.x);
+  else if ((p.n + 31) / 32 * til.total >= 256) rows_item<A8, SHIFT, 2>(p, til, s_part, blockIdx.x);
+  else rows_item<A8, SHIFT, 1>(p, til, s_part, blockIdx.x);
 }
 
 // Tile t of mt x nt: groups of kGroupM m-tiles, inside them all m-tiles of an n-tile before the next,
@@ -389,25 +388,15 @@ void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
 }
 
 // At most 512 items: few passes (is_few) of 64 columns, or fewer than 256 of twice the columns
-// of what is taken.  Eight waves instead of four where their chunks fill two rounds and the
-// items are at most one a CU (then of 16 columns).
+// of what is taken.
 void launch_rows(const GroupedArgs& a, int64_t passes, int nt, bool both, hipStream_t st) {
-  const int64_t items = (a.n + 15) / 16 * passes;
-  const bool deep = a.k >= 16 * kChunk && items <= 256;
-  const dim3 grid(unsigned(std::min<int64_t>(items, 4 * kFew)));
-  auto go = [&](auto kern, int waves) {
-    hipLaunchKernelGGL(kern, grid, dim3(64 * waves), 0, st, a, int(passes), nt, both);
+  const dim3 grid(unsigned(std::min<int64_t>((a.n + 15) / 16 * passes, 4 * kFew)));
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, grid, dim3(64 * kWaves), 0, st, a, int(passes), nt, both);
   };
-  auto form = [&](auto a8, auto shift) {
-    constexpr bool A8 = decltype(a8)::value, SHIFT = decltype(shift)::value;
-    if (deep) go(k_grouped_rows<A8, SHIFT, 8>, 8);
-    else go(k_grouped_rows<A8, SHIFT, 4>, 4);
-  };
-  auto format = [&](auto shift) {
-    if (a.a8) form(std::true_type(), shift);
-    else form(std::false_type(), shift);
-  };
-  scales_whole(a, 8) ? format(std::false_type()) : format(std::true_type());
+  const bool whole = scales_whole(a, 8);
+  if (a.a8) whole ? go(k_grouped_rows<true, false>) : go(k_grouped_rows<true, true>);
+  else whole ? go(k_grouped_rows<false, false>) : go(k_grouped_rows<false, true>);
 }
 
 }  // namespace
