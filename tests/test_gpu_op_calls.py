@@ -244,3 +244,30 @@ def test_two_graphs_replayed_on_two_streams():
             for name in NAMES:
                 for g, r in zip(d[name][-OUTS[name]:], w[name]):
                     assert torch.equal(g, r)
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_a_given_stream(raw):
+    """Work goes to the stream that is given, a torch stream or its handle, behind what is on it."""
+    for name, args in data(seed=5, T=200, k=2, D=256).items():
+        want = through_python(name, args)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        n = OUTS[name]
+        late = [t.clone() for t in args[:-n]]
+        kept = [t.clone() for t in late]
+        for t in late:
+            t.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):  # the inputs are there only once the stream is at this point
+            torch.cuda._sleep(2_000_000)
+            for t, k in zip(late, kept):
+                t.copy_(k)
+        s = side.cuda_stream if raw else side
+        if name in ("permute", "unpermute_backward", "quantize_mx4"):
+            getattr(ops, name)(*late, *args[-n:], stream=s)
+        else:
+            getattr(ops, name)(*late, out=args[-1], stream=s)
+        side.synchronize()
+        for g, w in zip(args[-n:], want):
+            assert torch.equal(g, w), name
