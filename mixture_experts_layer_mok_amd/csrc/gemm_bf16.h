@@ -87,18 +87,20 @@ __device__ __forceinline__ i32x4_t rsrc_or_empty(const i32x4_t& r, bool empty) {
 
 // Direct-to-LDS load of 16 bytes per lane from rsrc + voff + soff: lane l's bytes land
 // at LDS address lds_wave_base + 16 * l (the wave-uniform base travels in M0).  COH adds
-// sc1 (device scope).
+// sc1 (device scope).  The compiler places no wait states before or inside inline asm: the
+// load needs one after the write of M0, and five after a vector instruction that wrote a
+// scalar it reads (v_readlane, which reloads a spilled one, may come right before).
 template <bool COH>
 __device__ __forceinline__ void dma16_at(const i32x4_t& rsrc, uint32_t voff, uint32_t soff,
                                          uint32_t lds_wave_addr) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
   soff = __builtin_amdgcn_readfirstlane(soff);  // uniform; kept in an SGPR for the asm
   if (COH)
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen sc1 lds" ::"v"(voff),
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen sc1 lds" ::"v"(voff),
                  "s"(rsrc), "s"(soff), "s"(m0)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
                  "s"(rsrc), "s"(soff), "s"(m0)
                  : "memory", "m0");
 }

@@ -35,15 +35,16 @@ static __shared__ uint32_t g_lds_sb[2 * 256];  // B scale dwords, two stages
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // Direct-to-LDS load of one dword per lane from a per-lane address: lane l's dword
-// lands at lds_wave_base + 4 l.  COH adds sc1 (device scope).
+// lands at lds_wave_base + 4 l.  COH adds sc1 (device scope).  One wait state lies between
+// the write of M0 and the load that reads it (the address is in vector registers).
 template <bool COH>
 __device__ __forceinline__ void dma4(const void* src, const uint32_t* lds_wave_base) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_addr(lds_wave_base));
   if (COH)
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off sc1" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off sc1" ::"v"(src), "s"(m0)
                  : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(m0)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(src), "s"(m0)
                  : "memory", "m0");
 }
 
