@@ -97,13 +97,14 @@ __device__ __forceinline__ i32x4_t rsrc_dwords(const uint8_t* base, uint32_t byt
   return r;
 }
 
-// Direct-to-LDS load of 16 bytes a lane: lane l's land at lds_wave_addr + 16 l.  One wait state
-// lies between the write of M0 and the load that reads it.
+// Direct-to-LDS load of 16 bytes a lane: lane l's land at lds_wave_addr + 16 l.  The string has
+// the wait states itself: one after the write of M0, and five after whatever vector instruction
+// may have written a scalar that the load reads (v_readlane reloads spilled ones).
 __device__ __forceinline__ void lds_load16(const i32x4_t& rsrc, uint32_t voff, uint32_t soff,
                                            uint32_t lds_wave_addr) {
   const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
   soff = __builtin_amdgcn_readfirstlane(soff);
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff),
                "s"(rsrc), "s"(soff), "s"(m0)
                : "memory", "m0");
 }
