@@ -1,7 +1,8 @@
 // The calls of ops.py for ordinary arguments, as a CPython extension: the checks of the Python
 // functions over at::Tensor, and the C entry point.  A call that is not plainly in order (a check that fails, a
 // tensor of another device, a refusal of the entry point) returns None with nothing
-// enqueued; the Python function then repeats it with its own checks and messages.
+// enqueued; the Python function then repeats it with its own checks and messages.  A launch
+// that fails raises MokError here: part of the call may be enqueued, so it is not repeated.
 //
 // The entry points' addresses come from the library that _lib.py has loaded (bind), the
 // current device and stream from torch's own functions.
@@ -123,6 +124,18 @@ template <typename T>
 T* at_ptr(const Span& s) { return reinterpret_cast<T*>(const_cast<char*>(s.lo)); }
 
 PyObject* none() { Py_RETURN_NONE; }
+// What a call gives that entry point `fn` returned `code` for, other than MOK_OK.
+PyObject* refused(const char* fn, mok_status_t code) {
+  if (code != MOK_E_LAUNCH) return none();
+  PyObject* lib = PyImport_ImportModule("mixture_experts_layer_mok_amd._lib");
+  PyObject* cls = lib ? PyObject_GetAttrString(lib, "MokError") : nullptr;
+  PyObject* err = cls ? PyObject_CallFunction(cls, "si", fn, int(code)) : nullptr;
+  if (err) PyErr_SetObject(cls, err);
+  Py_XDECREF(err);
+  Py_XDECREF(cls);
+  Py_XDECREF(lib);
+  return nullptr;
+}
 PyObject* same(PyObject* o) {
   Py_INCREF(o);
   return o;
@@ -155,10 +168,9 @@ PyObject* do_permute(PyObject* const* a) {
       !pos->is_contiguous() || mp.rows != mx.rows || mo.cols != mx.cols || !apart(mo.s, {mx.s, mp.s}) ||
       !c.stream(&st))
     return none();
-  if (g_fn.permute(ty, mx.p, mx.ld, at_ptr<int32_t>(mp.s), mp.rows, int32_t(mp.cols), int32_t(mx.cols), mo.p,
-                   mo.ld, mo.rows, st) != MOK_OK)
-    return none();
-  return same(a[2]);
+  const auto s = g_fn.permute(ty, mx.p, mx.ld, at_ptr<int32_t>(mp.s), mp.rows, int32_t(mp.cols),
+                              int32_t(mx.cols), mo.p, mo.ld, mo.rows, st);
+  return s == MOK_OK ? same(a[2]) : refused("mok_permute", s);
 }
 
 // rows, pos, weights (None: without), out
@@ -182,7 +194,7 @@ PyObject* do_sum(PyObject* const* a, bool weighted) {
                                            mp.rows, int32_t(mp.cols), int32_t(mr.cols), mo.p, mo.ld, st)
                           : g_fn.permute_bwd(ty, mr.p, mr.ld, mr.rows, at_ptr<int32_t>(mp.s), mp.rows,
                                              int32_t(mp.cols), int32_t(mr.cols), mo.p, mo.ld, st);
-  return s == MOK_OK ? out.result() : none();
+  return s == MOK_OK ? out.result() : refused(weighted ? "mok_unpermute" : "mok_permute_bwd", s);
 }
 
 // dy, rows, pos, weights, d_rows, d_weights
@@ -205,10 +217,10 @@ PyObject* do_unpermute_bwd(PyObject* const* a) {
   if (!flat(c, dw.t, {mp.rows, mp.cols}, at::kFloat, &sdw) || !apart(md.s, {my.s, mr.s, mp.s, sw}) ||
       !apart(sdw, {my.s, mr.s, mp.s, sw, md.s}))
     return none();
-  if (g_fn.unpermute_bwd(ty, my.p, my.ld, mr.p, mr.ld, mr.rows, at_ptr<int32_t>(mp.s), at_ptr<float>(sw),
-                         mp.rows, int32_t(mp.cols), int32_t(mr.cols), md.p, md.ld, at_ptr<float>(sdw),
-                         st) != MOK_OK)
-    return none();
+  const auto s = g_fn.unpermute_bwd(ty, my.p, my.ld, mr.p, mr.ld, mr.rows, at_ptr<int32_t>(mp.s),
+                                    at_ptr<float>(sw), mp.rows, int32_t(mp.cols), int32_t(mr.cols), md.p, md.ld,
+                                    at_ptr<float>(sdw), st);
+  if (s != MOK_OK) return refused("mok_unpermute_bwd", s);
   PyObject* r = dw.result();
   return r ? Py_BuildValue("(ON)", a[4], r) : nullptr;
 }
@@ -241,9 +253,9 @@ PyObject* do_quantize(PyObject* const* a) {
       mq.rows != ms.rows || mc.cols != ms.cols / 2 || mq.cols != ms.cols / 32 || !apart(mc.s, {ms.s}) ||
       !apart(mq.s, {ms.s, mc.s}))
     return none();
-  if (g_fn.quantize_mx4(ty, ms.p, ms.ld, ms.rows, int32_t(ms.cols), static_cast<uint8_t*>(mc.p), mc.ld,
-                        static_cast<uint8_t*>(mq.p), mq.ld, st) != MOK_OK)
-    return none();
+  const auto s = g_fn.quantize_mx4(ty, ms.p, ms.ld, ms.rows, int32_t(ms.cols), static_cast<uint8_t*>(mc.p),
+                                   mc.ld, static_cast<uint8_t*>(mq.p), mq.ld, st);
+  if (s != MOK_OK) return refused("mok_quantize_mx4", s);
   PyObject *x = codes.result(), *y = scales.result();
   return x && y ? Py_BuildValue("(NN)", x, y) : nullptr;
 }
@@ -265,10 +277,9 @@ PyObject* do_dequantize(PyObject* const* a) {
       mc.cols % 16 || mq.cols != mc.cols / 16 || mo.cols != 2 * mc.cols || mq.rows != mc.rows ||
       mo.rows != mc.rows || !apart(mo.s, {mc.s, mq.s}))
     return none();
-  if (g_fn.dequantize_mx4(static_cast<uint8_t*>(mc.p), mc.ld, static_cast<uint8_t*>(mq.p), mq.ld, mc.rows,
-                          int32_t(mo.cols), ty, mo.p, mo.ld, st) != MOK_OK)
-    return none();
-  return out.result();
+  const auto s = g_fn.dequantize_mx4(static_cast<uint8_t*>(mc.p), mc.ld, static_cast<uint8_t*>(mq.p), mq.ld,
+                                     mc.rows, int32_t(mo.cols), ty, mo.p, mo.ld, st);
+  return s == MOK_OK ? out.result() : refused("mok_dequantize_mx4", s);
 }
 
 // a, a_scales, offsets, b, b_scales, dtype (of an output made here), out
@@ -295,12 +306,11 @@ PyObject* do_grouped(PyObject* const* v) {
       mas.cols != K / 32 || mo.rows != ma.rows || mo.cols != N || E > INT32_MAX || N > INT32_MAX ||
       K > INT32_MAX || !apart(mo.s, {ma.s, mas.s, so, sb, sbs}))
     return none();
-  if (g_fn.grouped_mx4(ma.cols == half ? MOK_MX_E2M1 : MOK_MX_E4M3, static_cast<uint8_t*>(ma.p), ma.ld,
-                       static_cast<uint8_t*>(mas.p), mas.ld, ma.rows, at_ptr<int32_t>(so), int32_t(E),
-                       at_ptr<uint8_t>(sb), at_ptr<uint8_t>(sbs), int32_t(N), int32_t(K), ty, mo.p, mo.ld,
-                       st) != MOK_OK)
-    return none();
-  return out.result();
+  const auto s = g_fn.grouped_mx4(ma.cols == half ? MOK_MX_E2M1 : MOK_MX_E4M3, static_cast<uint8_t*>(ma.p),
+                                  ma.ld, static_cast<uint8_t*>(mas.p), mas.ld, ma.rows, at_ptr<int32_t>(so),
+                                  int32_t(E), at_ptr<uint8_t>(sb), at_ptr<uint8_t>(sbs), int32_t(N),
+                                  int32_t(K), ty, mo.p, mo.ld, st);
+  return s == MOK_OK ? out.result() : refused("mok_grouped_mx4", s);
 }
 
 // A call with `want` arguments; a C++ exception (a tensor without strides or storage) is a

@@ -367,36 +367,29 @@ bool scales_whole(const GroupedArgs& a, uintptr_t piece) {
           uintptr_t(a.k / 32)) % piece == 0;
 }
 
-void launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
+mok_status_t launch_tiles(const GroupedArgs& a, int nt, bool both, hipStream_t st) {
   const int tm = a.a8 ? mx4::tile_rows<true, 4>() : mx4::tile_rows<false, 4>();
   // at most this many m-tiles: every expert may end inside one
   const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (tm - 1)) / tm);
   // (a tile makes four at most of half the rows and columns)
   const dim3 grid(unsigned(std::min<int64_t>((4 * mt * nt + 7) / 8 * 8, 256))), block(mx4::kThr);
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, st, a, int(mt), nt, both); };
+  auto go = [&](auto kern) { return launch(kern, grid, block, st, a, int(mt), nt, both); };
   auto form = [&](auto shift) {
     constexpr bool SHIFT = decltype(shift)::value;
-    if (a.a8) {
-      if (a.out32) go(k_grouped_tile<true, true, SHIFT>);
-      else go(k_grouped_tile<true, false, SHIFT>);
-    } else {
-      if (a.out32) go(k_grouped_tile<false, true, SHIFT>);
-      else go(k_grouped_tile<false, false, SHIFT>);
-    }
+    if (a.a8) return a.out32 ? go(k_grouped_tile<true, true, SHIFT>) : go(k_grouped_tile<true, false, SHIFT>);
+    return a.out32 ? go(k_grouped_tile<false, true, SHIFT>) : go(k_grouped_tile<false, false, SHIFT>);
   };
-  scales_whole(a, 16) ? form(std::false_type()) : form(std::true_type());
+  return scales_whole(a, 16) ? form(std::false_type()) : form(std::true_type());
 }
 
 // At most 512 items: few passes (is_few) of 64 columns, or fewer than 256 of twice the columns
 // of what is taken.
-void launch_rows(const GroupedArgs& a, int64_t passes, int nt, bool both, hipStream_t st) {
+mok_status_t launch_rows(const GroupedArgs& a, int64_t passes, int nt, bool both, hipStream_t st) {
   const dim3 grid(unsigned(std::min<int64_t>((a.n + 15) / 16 * passes, 4 * kFew)));
-  auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, grid, dim3(64 * kWaves), 0, st, a, int(passes), nt, both);
-  };
+  auto go = [&](auto kern) { return launch(kern, grid, dim3(64 * kWaves), st, a, int(passes), nt, both); };
   const bool whole = scales_whole(a, 8);
-  if (a.a8) whole ? go(k_grouped_rows<true, false>) : go(k_grouped_rows<true, true>);
-  else whole ? go(k_grouped_rows<false, false>) : go(k_grouped_rows<false, true>);
+  if (a.a8) return whole ? go(k_grouped_rows<true, false>) : go(k_grouped_rows<true, true>);
+  return whole ? go(k_grouped_rows<false, false>) : go(k_grouped_rows<false, true>);
 }
 
 }  // namespace
@@ -421,9 +414,10 @@ mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
   const int nt = (a.n + mx4::tile_cols<4>() - 1) / mx4::tile_cols<4>();
   const int64_t passes = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kPass - 1)) / kPass);
   const bool rows = is_few(passes, 0, nt), tiles = !rows && (a.max_rows > 4096 || nt * std::min<int64_t>(a.groups, a.max_rows) >= 192);
-  if (!rows) launch_tiles(a, nt, !tiles, st);
-  if (!tiles) launch_rows(a, passes, nt, !rows, st);
-  return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH;
+  mok_status_t s = MOK_OK;
+  if (!rows) s = launch_tiles(a, nt, !tiles, st);
+  if (!tiles && s == MOK_OK) s = launch_rows(a, passes, nt, !rows, st);
+  return s;
 }
 
 }  // namespace mok

@@ -202,8 +202,6 @@ __global__ __launch_bounds__(256) void k_dequantize_mx4(const uint8_t* codes, co
   }
 }
 
-mok_status_t launched() { return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH; }
-
 Mat mat_of(const Mx4Args& a, int elems) {
   const int es = a.type == MOK_TYPE_FP32 ? 4 : 2;
   return Mat{a.rows * (a.cols / elems), a.cols / elems, a.ld_val * es, a.ld_codes, a.ld_scales};
@@ -216,13 +214,13 @@ unsigned grid_of(const Mat& m) {
 }
 // Calls f with the element type and density as compile-time values.
 template <typename F>
-void with_form(const Mx4Args& a, F f) {
+mok_status_t with_form(const Mx4Args& a, F f) {
   auto form = [&](auto type) {
-    dense(a) ? f(type, std::true_type()) : f(type, std::false_type());
+    return dense(a) ? f(type, std::true_type()) : f(type, std::false_type());
   };
-  if (a.type == MOK_TYPE_BF16) form(std::integral_constant<int, MOK_TYPE_BF16>());
-  else if (a.type == MOK_TYPE_FP16) form(std::integral_constant<int, MOK_TYPE_FP16>());
-  else form(std::integral_constant<int, MOK_TYPE_FP32>());
+  if (a.type == MOK_TYPE_BF16) return form(std::integral_constant<int, MOK_TYPE_BF16>());
+  if (a.type == MOK_TYPE_FP16) return form(std::integral_constant<int, MOK_TYPE_FP16>());
+  return form(std::integral_constant<int, MOK_TYPE_FP32>());
 }
 
 }  // namespace
@@ -233,27 +231,24 @@ mok_status_t launch_quantize_mx4(const Mx4Args& a, hipStream_t st) {
   // non-temporally ([16384, 7168] bf16 53 -> 47 us; [4096, 7168] 12.9 plain, 14.0 so).
   const int64_t moved = a.rows * a.cols * (a.type == MOK_TYPE_FP32 ? 4 : 2) + a.rows * (a.cols / 2);
   const bool nt = moved > (int64_t(256) << 20);
-  with_form(a, [&](auto type, auto flat) {
+  return with_form(a, [&](auto type, auto flat) {
     constexpr int kType = decltype(type)::value;
     constexpr bool kFlat = decltype(flat)::value;
     auto go = [&](auto kern) {
-      hipLaunchKernelGGL(kern, dim3(grid_of(m)), dim3(256), 0, st, static_cast<const uint8_t*>(a.src), m,
-                         a.codes, a.scales);
+      return launch(kern, dim3(grid_of(m)), dim3(256), st, static_cast<const uint8_t*>(a.src), m, a.codes,
+                    a.scales);
     };
-    if (nt) go(k_quantize_mx4<kType, kFlat, true>);
-    else go(k_quantize_mx4<kType, kFlat, false>);
+    return nt ? go(k_quantize_mx4<kType, kFlat, true>) : go(k_quantize_mx4<kType, kFlat, false>);
   });
-  return launched();
 }
 
 mok_status_t launch_dequantize_mx4(const Mx4Args& a, hipStream_t st) {
   const Mat m = mat_of(a, a.type == MOK_TYPE_FP32 ? 4 : 8);
-  with_form(a, [&](auto type, auto flat) {
-    hipLaunchKernelGGL((k_dequantize_mx4<decltype(type)::value, decltype(flat)::value>), dim3(grid_of(m)),
-                       dim3(256), 0, st, static_cast<const uint8_t*>(a.codes),
-                       static_cast<const uint8_t*>(a.scales), m, static_cast<uint8_t*>(a.dst));
+  return with_form(a, [&](auto type, auto flat) {
+    return launch(k_dequantize_mx4<decltype(type)::value, decltype(flat)::value>, dim3(grid_of(m)), dim3(256),
+                  st, static_cast<const uint8_t*>(a.codes), static_cast<const uint8_t*>(a.scales), m,
+                  static_cast<uint8_t*>(a.dst));
   });
-  return launched();
 }
 
 }  // namespace mok

@@ -1,9 +1,29 @@
 // Arguments and launchers of the row operators and the MXFP4 operators (rows.hip, mx4.hip,
 // grouped_mx4.hip), called by ops_api.hip after its checks.
 #pragma once
+#include <cstddef>
+#include <tuple>
+#include <utility>
+
 #include "launch.h"
 
 namespace mok {
+
+// Launches a kernel and gives the launch's own result.  (hipGetLastError would also report, and
+// take away, an error that an earlier call of someone else left behind.)
+template <typename... P, size_t... I>
+hipError_t launch_with(void (*kern)(P...), dim3 grid, dim3 block, hipStream_t st, std::tuple<P...>& args,
+                       std::index_sequence<I...>) {
+  void* at[] = {static_cast<void*>(&std::get<I>(args))...};
+  return hipLaunchKernel(reinterpret_cast<const void*>(kern), grid, block, at, 0, st);
+}
+template <typename... P, typename... A>
+mok_status_t launch(void (*kern)(P...), dim3 grid, dim3 block, hipStream_t st, A... args) {
+  std::tuple<P...> p(args...);
+  if (launch_with(kern, grid, block, st, p, std::index_sequence_for<P...>()) == hipSuccess) return MOK_OK;
+  (void)hipGetLastError();  // reported here, not by the next caller's check
+  return MOK_E_LAUNCH;
+}
 
 // Row operators (rows.hip).  tok: the operand with a row per token that is read (x, dy);
 // rows: the routed rows that are read; out: what is written, of ld_out elements a row.

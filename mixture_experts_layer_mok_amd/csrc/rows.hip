@@ -251,8 +251,6 @@ __global__ __launch_bounds__(threads_of<W>()) void k_unpermute_bwd(RowGeom g, co
   if (lane < g.k) dw[t * g.k + lane] = my_dw;
 }
 
-mok_status_t launched() { return hipGetLastError() == hipSuccess ? MOK_OK : MOK_E_LAUNCH; }
-
 // Launch shape.
 //   W: waves a token: one where the tokens alone fill the GPU (or the row is one chunk a lane),
 //     else four, or sixteen for long rows, so that a lane holds one chunk of its row.  Measured
@@ -284,20 +282,22 @@ unsigned grid_for(int64_t T, int W) { return unsigned(W >= 4 ? T : (T + 3) / 4);
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <int UMAX, typename F>
-void with_shape(const Shape& s, F f) {
+mok_status_t with_shape(const Shape& s, F f) {
   if (s.W == 4) return f(Int<4>(), Int<1>(), std::false_type());
   if (s.W == 16) return f(Int<16>(), Int<1>(), std::false_type());
-  auto nt = [&](auto u) { s.nt ? f(Int<1>(), u, std::true_type()) : f(Int<1>(), u, std::false_type()); };
+  auto nt = [&](auto u) {
+    return s.nt ? f(Int<1>(), u, std::true_type()) : f(Int<1>(), u, std::false_type());
+  };
   if (s.U == 2) return nt(Int<2>());
   if (s.U == 4) return nt(Int<4>());
   if (UMAX == 8 || s.U == 8) return nt(Int<8>());
-  nt(Int<UMAX>());
+  return nt(Int<UMAX>());
 }
 template <typename F>
-void with_type(int32_t type, F f) {
-  if (type == MOK_TYPE_BF16) f(Int<MOK_TYPE_BF16>());
-  else if (type == MOK_TYPE_FP16) f(Int<MOK_TYPE_FP16>());
-  else f(Int<MOK_TYPE_FP32>());
+mok_status_t with_type(int32_t type, F f) {
+  if (type == MOK_TYPE_BF16) return f(Int<MOK_TYPE_BF16>());
+  if (type == MOK_TYPE_FP16) return f(Int<MOK_TYPE_FP16>());
+  return f(Int<MOK_TYPE_FP32>());
 }
 
 RowGeom geom_of(const RowArgs& a) {
@@ -313,39 +313,36 @@ mok_status_t launch_permute(const RowArgs& a, hipStream_t st) {
   g.ld_rows = g.ld_out;
   Shape s = shape_of(g, 16);
   s.nt = false;
-  with_shape<16>(s, [&](auto w, auto u, auto) {
+  return with_shape<16>(s, [&](auto w, auto u, auto) {
     constexpr int W = decltype(w)::value, U = decltype(u)::value;
-    hipLaunchKernelGGL((k_permute<W, U>), dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
-                       static_cast<const uint8_t*>(a.tok), a.pos, static_cast<uint8_t*>(a.out));
+    return launch(k_permute<W, U>, dim3(grid_for(g.T, W)), dim3(threads_of<W>()), st, g,
+                  static_cast<const uint8_t*>(a.tok), a.pos, static_cast<uint8_t*>(a.out));
   });
-  return launched();
 }
 
 mok_status_t launch_sum_rows(const RowArgs& a, hipStream_t st) {
   const RowGeom g = geom_of(a);
-  with_type(a.type, [&](auto type) {
-    with_shape<8>(shape_of(g, 8), [&](auto w, auto u, auto nt) {
+  return with_type(a.type, [&](auto type) {
+    return with_shape<8>(shape_of(g, 8), [&](auto w, auto u, auto nt) {
       constexpr int W = decltype(w)::value, U = decltype(u)::value;
-      hipLaunchKernelGGL((k_sum_rows<decltype(type)::value, W, U, decltype(nt)::value>),
-                         dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
-                         static_cast<const uint8_t*>(a.rows), a.pos, a.w, static_cast<uint8_t*>(a.out));
+      return launch(k_sum_rows<decltype(type)::value, W, U, decltype(nt)::value>, dim3(grid_for(g.T, W)),
+                    dim3(threads_of<W>()), st, g, static_cast<const uint8_t*>(a.rows), a.pos, a.w,
+                    static_cast<uint8_t*>(a.out));
     });
   });
-  return launched();
 }
 
 mok_status_t launch_unpermute_bwd(const RowArgs& a, hipStream_t st) {
   const RowGeom g = geom_of(a);
-  with_type(a.type, [&](auto type) {
-    with_shape<16>(shape_of(g, 16), [&](auto w, auto u, auto nt) {
+  return with_type(a.type, [&](auto type) {
+    return with_shape<16>(shape_of(g, 16), [&](auto w, auto u, auto nt) {
       constexpr int W = decltype(w)::value, U = decltype(u)::value;
-      hipLaunchKernelGGL((k_unpermute_bwd<decltype(type)::value, W, U, decltype(nt)::value>),
-                         dim3(grid_for(g.T, W)), dim3(threads_of<W>()), 0, st, g,
-                         static_cast<const uint8_t*>(a.tok), static_cast<const uint8_t*>(a.rows), a.pos,
-                         a.w, static_cast<uint8_t*>(a.out), a.dw);
+      return launch(k_unpermute_bwd<decltype(type)::value, W, U, decltype(nt)::value>,
+                    dim3(grid_for(g.T, W)), dim3(threads_of<W>()), st, g,
+                    static_cast<const uint8_t*>(a.tok), static_cast<const uint8_t*>(a.rows), a.pos, a.w,
+                    static_cast<uint8_t*>(a.out), a.dw);
     });
   });
-  return launched();
 }
 
 }  // namespace mok
