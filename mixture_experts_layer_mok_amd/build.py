@@ -4,7 +4,8 @@
 
 Every .hip file under csrc/ is compiled to an object (in parallel), then linked into
 mixture_experts_layer_mok_amd/libmok.so; csrc/fast_calls.cpp is compiled by the host
-compiler to the extension module _fast.so.  All device code is built with packed-FP32
+compiler to the extension module _fast.so, which the package also works without (where the
+host compiler, Python's headers or torch are missing).  All device code is built with packed-FP32
 instructions disabled (the compiler would otherwise form v_pk_* fp32 ops on its own).
 """
 from __future__ import annotations
@@ -66,7 +67,8 @@ def _build_fast() -> None:
                for d in ("-I", p)]
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *include,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DMOK_TORCH_VERSION="{torch.__version__}"', *include,
            os.path.join(CSRC, "fast_calls.cpp"), "-o", FAST + ".tmp", "-L", libs, "-ltorch_python",
            "-ltorch", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -75,14 +77,26 @@ def _build_fast() -> None:
     os.replace(FAST + ".tmp", FAST)
 
 
+def _try_fast() -> bool:
+    """_build_fast; where it fails, the reason on stderr and no module of an earlier build left."""
+    try:
+        _build_fast()
+        return True
+    except (ImportError, OSError, RuntimeError) as e:
+        sys.stderr.write(f"_fast.so is not built (the operators' calls run without it): {e}\n")
+        if os.path.exists(FAST):
+            os.remove(FAST)
+        return False
+
+
 def build(jobs: int | None = None, verbose: bool = True) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs) + 1, os.cpu_count() or 4, 8)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        fast = ex.submit(_build_fast)
+        fast = ex.submit(_try_fast)
         objs = list(ex.map(_compile, srcs))
-        fast.result()
+        with_fast = fast.result()
     tmp = OUT + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -90,7 +104,7 @@ def build(jobs: int | None = None, verbose: bool = True) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, OUT)
     if verbose:
-        print(f"built {OUT} from {len(srcs)} sources")
+        print(f"built {OUT} from {len(srcs)} sources" + (f", and {FAST}" if with_fast else ""))
     return OUT
 
 

@@ -378,4 +378,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, g_methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&g_module); }
+// torch_version: the torch whose headers it is compiled against, the only one that it fits.
+PyMODINIT_FUNC PyInit__fast() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", MOK_TORCH_VERSION) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -12,7 +12,7 @@ are not the layer's own:
 
 Ordinary calls run through the extension module _fast (the same checks and the same C entry
 point in native code); what it does not take runs through the code here, which has the
-messages.
+messages.  Without an extension module that fits the running torch, every call does.
 
 Every function checks its tensors (ValueError), makes one call of the C entry point of the
 same name (MokError for what that refuses) on the tensors' device and returns without
@@ -24,6 +24,7 @@ passed in; those allocated here belong to the stream the work runs on.
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 import torch
 
@@ -133,21 +134,32 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def _call(fn: str, *args) -> None:
     lib = L.load()
-    if _fast is None:
+    if not _bound:
         _bind(lib)
     code = getattr(lib, fn)(*args)
     if code:
         raise L.MokError(fn, code)
 
 
-_fast = None  # the extension module, from the first call on
+_fast = None  # the extension module, from the first call on, where there is one that fits
+_bound = False  # it has been looked for
 
 
 def _bind(lib) -> None:
     """Gives the extension module the library's entry points."""
-    global _fast
-    from . import _fast as module
+    global _fast, _bound
+    _bound = True
+    try:
+        from . import _fast as module
 
+        fits = getattr(module, "torch_version", "unknown")
+        if fits != torch.__version__:
+            raise ImportError(f"it is built for torch {fits}")
+    except ImportError as e:
+        warnings.warn(f"the extension module _fast is not used ({e}); calls take a few microseconds "
+                      "more of host time.  `python -m mixture_experts_layer_mok_amd.build` makes it",
+                      RuntimeWarning, stacklevel=2)
+        return
     names = ("mok_permute", "mok_permute_bwd", "mok_unpermute", "mok_unpermute_bwd",
              "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4")
     module.bind(getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream,

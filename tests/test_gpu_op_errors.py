@@ -1,10 +1,13 @@
 """Errors around the row and MXFP4 functions' launches, on a GPU: a launch that fails is raised and
-not repeated; an error that another call left behind is not taken for the launch's."""
+not repeated; an error that another call left behind is not taken for the launch's; without the
+extension module every function runs."""
 import ctypes
+import sys
 
 import pytest
 import torch
 
+import mixture_experts_layer_mok_amd as package
 from mixture_experts_layer_mok_amd import _lib as L
 from mixture_experts_layer_mok_amd import ops
 from tests.test_gpu_op_calls import NAMES, OUTS, data, through_python
@@ -51,6 +54,25 @@ def test_a_failed_launch_is_raised_once(name):
     assert calls == [ENTRIES[name]]
     torch.cuda.synchronize()
     assert all((t == 5).all() for t in outs)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_without_the_extension_module(name, monkeypatch):
+    args = data()[name]
+    n = OUTS[name]
+    want = through_python(name, args)
+    torch.cuda.synchronize()
+    monkeypatch.delattr(package, "_fast", raising=False)
+    monkeypatch.setitem(sys.modules, package.__name__ + "._fast", None)
+    monkeypatch.setattr(ops, "_fast", None)
+    monkeypatch.setattr(ops, "_bound", False)
+    with pytest.warns(RuntimeWarning, match="_fast is not used"):
+        call(name, args)
+    call(name, args)
+    assert ops._fast is None
+    torch.cuda.synchronize()
+    for g, w in zip(args[-n:], want):
+        assert torch.equal(g, w)
 
 
 @pytest.mark.parametrize("name", NAMES)
