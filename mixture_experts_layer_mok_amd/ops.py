@@ -133,12 +133,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 
 def _call(fn: str, *args) -> None:
-    lib = L.load()
     if not _bound:
-        _bind(lib)
-    code = getattr(lib, fn)(*args)
-    if code:
-        raise L.MokError(fn, code)
+        _bind(L.load())
+    getattr(L, fn)(*args)
 
 
 _fast = None  # the extension module, from the first call on, where there is one that fits
