@@ -140,6 +140,10 @@ PyObject* same(PyObject* o) {
   Py_INCREF(o);
   return o;
 }
+// A graph that saved an output passed in finds it changed.
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
 // The output passed in (borrowed) or, for None, one made here; null where it is neither.
 struct Output {
   at::Tensor made;
@@ -154,7 +158,11 @@ struct Output {
       t = tensor(given);
     }
   }
-  PyObject* result() const { return o == Py_None ? THPVariable_Wrap(made) : same(o); }
+  PyObject* result() const {
+    if (o == Py_None) return THPVariable_Wrap(made);
+    written(*t);
+    return same(o);
+  }
 };
 
 PyObject* do_permute(PyObject* const* a) {
@@ -170,7 +178,9 @@ PyObject* do_permute(PyObject* const* a) {
     return none();
   const auto s = g_fn.permute(ty, mx.p, mx.ld, at_ptr<int32_t>(mp.s), mp.rows, int32_t(mp.cols),
                               int32_t(mx.cols), mo.p, mo.ld, mo.rows, st);
-  return s == MOK_OK ? same(a[2]) : refused("mok_permute", s);
+  if (s != MOK_OK) return refused("mok_permute", s);
+  written(*out);
+  return same(a[2]);
 }
 
 // rows, pos, weights (None: without), out
@@ -221,6 +231,7 @@ PyObject* do_unpermute_bwd(PyObject* const* a) {
                                     at_ptr<float>(sw), mp.rows, int32_t(mp.cols), int32_t(mr.cols), md.p, md.ld,
                                     at_ptr<float>(sdw), st);
   if (s != MOK_OK) return refused("mok_unpermute_bwd", s);
+  written(*d_rows);
   PyObject* r = dw.result();
   return r ? Py_BuildValue("(ON)", a[4], r) : nullptr;
 }

@@ -16,7 +16,9 @@ messages.  Without an extension module that fits the running torch, every call d
 
 Every function checks its tensors (ValueError), makes one call of the C entry point of the
 same name (MokError for what that refuses) on the tensors' device and returns without
-synchronising.  Value tensors are bf16, fp16 or fp32 matrices whose rows are contiguous;
+synchronising.  Autograd records none of them: inputs may require grad, results do not, and the
+gradients are functions of their own (for an autograd.Function to call).  Outputs that are
+passed in count as changed in place, so that a backward pass which saved one raises.  Value tensors are bf16, fp16 or fp32 matrices whose rows are contiguous;
 the distance between rows may be any multiple of 8 elements.  `stream` is a torch stream
 or a raw handle; by default the current stream of the tensors' device.  Outputs may be
 passed in; those allocated here belong to the stream the work runs on.
@@ -164,6 +166,13 @@ def _bind(lib) -> None:
     _fast = module
 
 
+def _written(*outs) -> None:
+    """Outputs passed in (None: made by the call): a graph that saved one finds it changed."""
+    for t in outs:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def _pos(pos) -> tuple:
     if not isinstance(pos, torch.Tensor) or pos.dim() != 2 or pos.dtype is not torch.int32 or \
             not pos.is_contiguous():
@@ -193,6 +202,7 @@ def permute(x, pos, out, stream=None):
     _same_device(dev, pos, out)
     with _On(dev, stream) as st:
         _call("mok_permute", ty, px, ld_x, pp, T, k, D, po, ld_o, n, st)
+    _written(out)
     return out
 
 
@@ -210,6 +220,7 @@ def _sum_rows(fn, rows, pos, weights, out, stream):
         pw = (w,)
         _same_device(dev, weights)
     _same_device(dev, pos)
+    given = out
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty(T, D, dtype=rows.dtype, device=dev)
@@ -217,6 +228,7 @@ def _sum_rows(fn, rows, pos, weights, out, stream):
         _apart("out", po, oe, inputs)
         _same_device(dev, out)
         _call(fn, ty, pr, ld_r, n, pp, *pw, T, k, D, po, ld_o, st)
+    _written(given)
     return out
 
 
@@ -258,6 +270,7 @@ def unpermute_backward(dy, rows, pos, weights, d_rows, d_weights=None, stream=No
     pw, we = _flat("weights", weights, (T, k), torch.float32)
     dev = rows.device
     _same_device(dev, dy, pos, weights, d_rows)
+    given = d_weights
     with _On(dev, stream) as st:
         if d_weights is None:
             d_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
@@ -267,6 +280,7 @@ def unpermute_backward(dy, rows, pos, weights, d_rows, d_weights=None, stream=No
         _apart("d_rows", pd, de, inputs)
         _apart("d_weights", pdw, dwe, inputs + (("d_rows", pd, de),))
         _call("mok_unpermute_bwd", ty, py, ld_y, pr, ld_r, n, pp, pw, T, k, D, pd, ld_d, pdw, st)
+    _written(d_rows, given)
     return d_rows, d_weights
 
 
@@ -297,6 +311,7 @@ def quantize_mx4(src, codes=None, scales=None, stream=None):
     ps, ld_s, se, n = _rows_of("src", src, K)
     dev = src.device
     _same_device(dev)
+    given = codes, scales
     with _On(dev, stream) as st:
         if codes is None:
             codes = torch.empty(*src.shape[:-1], K // 2, dtype=torch.uint8, device=dev)
@@ -308,6 +323,7 @@ def quantize_mx4(src, codes=None, scales=None, stream=None):
         _apart("codes", pc, ce, (("src", ps, se),))
         _apart("scales", pq, qe, (("src", ps, se), ("codes", pc, ce)))
         _call("mok_quantize_mx4", ty, ps, ld_s, n, K, pc, ld_c, pq, ld_q, st)
+    _written(*given)
     return codes, scales
 
 
@@ -328,6 +344,7 @@ def dequantize_mx4(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
         raise ValueError("dtype: bfloat16, float16 or float32 is wanted")
     dev = codes.device
     _same_device(dev, scales)
+    given = out
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty(*codes.shape[:-1], K, dtype=dtype, device=dev)
@@ -336,6 +353,7 @@ def dequantize_mx4(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
         _same_device(dev, out)
         _apart("out", po, oe, (("codes", pc, ce), ("scales", pq, qe)))
         _call("mok_dequantize_mx4", pc, ld_c, pq, ld_q, n, K, ty, po, ld_o, st)
+    _written(given)
     return out
 
 
@@ -369,6 +387,7 @@ def grouped_mx4(a, a_scales, offsets, b, b_scales, out=None, dtype=torch.bfloat1
         raise ValueError("dtype: bfloat16 or float32 is wanted")
     dev = a.device
     _same_device(dev, a_scales, offsets, b, b_scales)
+    given = out
     with _On(dev, stream) as st:
         if out is None:
             out = torch.empty(n, N, dtype=dtype, device=dev)
@@ -380,4 +399,5 @@ def grouped_mx4(a, a_scales, offsets, b, b_scales, out=None, dtype=torch.bfloat1
                                ("b", pb, be), ("b_scales", pq, qe)))
         _call("mok_grouped_mx4", L.MOK_MX_E2M1 if width == half else L.MOK_MX_E4M3, pa, ld_a, pas,
               ld_as, n, pf, E, pb, pq, N, K, _TYPES[out.dtype], po, ld_o, st)
+    _written(given)
     return out
