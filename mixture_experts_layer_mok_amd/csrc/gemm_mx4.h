@@ -1,9 +1,10 @@
 // Tile of the grouped MX product for many rows: one workgroup of four waves computes
 // kTM x 256 outputs, 256 rows with MXFP4 activations and 128 with MXFP8, each wave half of
 // the rows by 128 columns (32 x 32 MFMA blocks of v_mfma_scale_f32_32x32x64_f8f6f4).  Bound
-// by the card's power: 16,384 rows, N 4096, K 7168 in MXFP4 on MI355X take 250-275 us (3.5-3.85
-// PFLOP/s) at 1.9 of 2.4 GHz with the matrix cores half busy; their instructions alone, on
-// random data, 162 us.
+// by the card's power and by moving the data: 16,384 rows, N 4096, K 7168 in MXFP4 on MI355X take
+// 250 us in a captured loop over one input and 280 over changing ones (3.4-3.9 PFLOP/s, by card),
+// at 1.9 of 2.4 GHz with the matrix cores half busy; the kernel without its loads and stores 188
+// at the same clock, its matrix instructions alone, on random data, 162.
 //
 // A K step is 256 elements: 32 KB of A and 32 KB of B, whole 128-byte lines, moved by
 // direct-to-LDS loads through a ring of two stages.  Four waves of 128 x 128 read 128 KB of

@@ -100,10 +100,12 @@ __host__ __device__ __forceinline__ bool is_few(int64_t passes, int64_t active, 
 // Few rows an expert (decoding): bound by reading the weights once.
 // ------------------------------------------------------------------------------------
 // One workgroup of four waves: 16 NB columns of one expert and at most 32 of its rows (a pass).
-// The K chunks of 256 (two MFMA steps) are dealt to the waves; each loads its next chunk
-// before it multiplies the current one, straight into registers (a weight is used by one
-// wave only, so LDS would add a copy), and the waves' sums are joined through LDS in wave
-// order.  Loads past K, past the rows and past N read zeros (zero codes, zero scales: no
+// The K chunks of 256 (two MFMA steps) are dealt to the waves; each issues its next chunk's
+// loads before it multiplies the current one, straight into registers (a weight is used by one
+// wave only, so LDS would add a copy).  The copy of the chunk's registers at the end of an
+// iteration waits for those loads, so they overlap one chunk's products; the rest of their
+// latency is covered by the CU's other waves.  The waves' sums are joined through LDS in
+// wave order.  Loads past K, past the rows and past N read zeros (zero codes, zero scales: no
 // product).
 constexpr int kChunk = 256, kWaves = 4;
 
@@ -396,20 +398,24 @@ mok_status_t launch_rows(const GroupedArgs& a, int64_t passes, int nt, bool both
 
 // Which kernel.  The few-rows kernel reads the weights once for 32 rows, all passes at the same
 // time: its time grows with passes times columns; a tile takes its K loop's time however few
-// there are.  Measured on MI355X, weights from HBM, few-rows / tile kernel, us, by u = passes
-// times 256-column blocks:
-//   N 4096, K 7168: u 16 (32 rows, 1 expert) 13 / 31 with MXFP8 rows, 9 / 28 with MXFP4; u 64
-//     20 / 39, 16 / 31; u 128 33 / 40, 26 / 40 (8 experts: 39 / 46, 35 / 43); u 256 60 / 41, 48 / 41
-//   N 7168, K 2048: u 56 11 / 12, 9 / 11; u 112 14 / 15, 12 / 13; u 224 25 / 16, 21 / 17
-//   N 1024, K 2048: u 32 7 / 14, 6 / 16; u 128 14 / 15, 11 / 16
-//   N 2048, K 4096: u 64 15 / 24, 13 / 26; u 128 25 / 24, 21 / 26; u 256 45 / 25, 38 / 27
-//   (since then the tiles of half the size take that last tile time to 19, 18, and of 40, 40 to
-//   about 29, 27: an expert's later passes, which the tiles do not repeat, count 4/3)
-//   64 experts, N 2048, K 4096, MXFP8: 4 rows each (u 512) 64 / 55, 32 rows 91 / 61
+// there are.  Measured on MI355X, weights from HBM, few-rows / tile kernel alone, us, by u =
+// passes times 256-column blocks, MXFP8 rows and then MXFP4:
+//   N 4096, K 7168, one expert: u 16 13 / 23, 9 / 22; u 32 15 / 24, 11 / 22; u 64 20 / 24, 17 / 24;
+//     u 128 34 / 24, 28 / 24.  8 experts, u 128: 8 rows each 30 / 34, 28 / 33; 32 rows each 42 / 35,
+//     36 / 34.  u 256 72 / 36, 61 / 34
+//   N 7168, K 2048: u 56 11 / 10, 10 / 10; u 112 17 / 12, 15 / 11; u 224 32 / 19, 28 / 18
+//   N 1024, K 2048: u 32 8 / 10, 7 / 9; u 128 17 / 10, 15 / 10
+//   N 2048, K 4096: u 64, one expert 15 / 15, 12 / 16; u 128, 8 experts 28 / 19, 24 / 17, 16 experts
+//     31 / 22, 27 / 21; 64 experts of 4 rows (u 512) 71 / 54, 66 / 54
+// The bound is 128, an expert's passes after its first counted 4/3 (the tiles do not repeat those).
+// It was set against tiles of one size; the half-size tiles have since moved the crossing: they
+// are ahead from u of about 60 on, bar experts of few rows with long K, so that calls of u 60 to
+// 128 may take the slower kernel, by at most the 10 us above.
 // max_rows bounds the passes; where that leaves the choice open, both are launched, the routed
-// rows decide on the device, and one returns at once (2.2 us).  The tiles alone above 4096 rows
-// and where a pass an expert would already be too many: there are few passes then only if
-// nearly all of max_rows or most experts are unused.
+// rows decide on the device, and one returns at once (2.2-2.5 us in a captured loop; 2.3-4.8 in a
+// trace of single calls).  The tiles alone above 4096 rows and where a pass an expert would
+// already be too many: there are few passes then only if nearly all of max_rows or most experts
+// are unused.
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st) {
   const int nt = (a.n + mx4::tile_cols<4>() - 1) / mx4::tile_cols<4>();
   const int64_t passes = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kPass - 1)) / kPass);

@@ -72,7 +72,8 @@ struct Elem<MOK_TYPE_FP32> {
   }
 };
 
-// W waves of a workgroup share a token; a workgroup holds kWg / W tokens.
+// W waves of a workgroup share a token; a workgroup has four waves, 4 / W tokens, or, for W of 16,
+// one token.
 constexpr int kMaxWaves = 16;
 
 struct RowGeom {
@@ -126,9 +127,11 @@ __global__ __launch_bounds__(threads_of<W>()) void k_permute(RowGeom g, const ui
   }
 }
 
-// dst[t] = sum_j g_j rows[pos[t,j]], g_j = w[t,j], or 1 without weights.  The rows of kSlots
-// pairs are loaded before any is added; missing ones get an empty range, whose loads read
-// nothing.
+// dst[t] = sum_j g_j rows[pos[t,j]], g_j = w[t,j], or 1 without weights, kSlots pairs at a time;
+// missing ones get an empty range, whose loads read nothing.  As compiled, a row's load stands
+// right before its addition (below the branch that leaves the slots), so a wave has one row
+// in flight: with many tokens the other waves cover that (86,552 rows of 7168 at 5.4 TB/s), a few
+// tokens take a round trip a row (64 tokens of eight rows of 7168: 5 us).
 template <int TYPE, int W, int U, bool NT>
 __global__ __launch_bounds__(threads_of<W>()) void k_sum_rows(RowGeom g, const uint8_t* rows,
                                                               const int32_t* pos, const float* w,

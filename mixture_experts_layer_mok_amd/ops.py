@@ -18,10 +18,12 @@ Every function checks its tensors (ValueError), makes one call of the C entry po
 same name (MokError for what that refuses) on the tensors' device and returns without
 synchronising.  Autograd records none of them: inputs may require grad, results do not, and the
 gradients are functions of their own (for an autograd.Function to call).  Outputs that are
-passed in count as changed in place, so that a backward pass which saved one raises.  Value tensors are bf16, fp16 or fp32 matrices whose rows are contiguous;
-the distance between rows may be any multiple of 8 elements.  `stream` is a torch stream
-or a raw handle; by default the current stream of the tensors' device.  Outputs may be
-passed in; those allocated here belong to the stream the work runs on.
+passed in count as changed in place, so that a backward pass which saved one raises.
+
+Value tensors are bf16, fp16 or fp32 matrices whose rows are contiguous; the first lies at a
+multiple of 16 bytes, the distance between them may be any multiple of 8 elements.  `stream` is
+a torch stream or a raw handle; by default the current stream of the tensors' device.  Outputs
+may be passed in; those allocated here belong to the stream the work runs on.
 """
 from __future__ import annotations
 
