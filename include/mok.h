@@ -397,6 +397,97 @@ mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t l
                              const uint8_t* b_scales, int32_t n, int32_t k, int32_t out_type,
                              void* out, int64_t ld_out, void* stream);
 
+/* ---------------------------------------------------------------------------------
+ * Grouped product of 16-bit rows, with its two gradients: the experts' matrix products
+ * between mok_permute and mok_unpermute.  `type` (MOK_TYPE_BF16 or MOK_TYPE_FP16) is the
+ * type of every 16-bit operand; sums run in fp32 on the matrix cores and are rounded once
+ * to out_type: `type` or MOK_TYPE_FP32.
+ *
+ * Common rules.  offsets [groups + 1] int32 stays on the device, as for mok_grouped_mx4:
+ * expert e (of `groups`, 1..1024) has the rows [offsets[e], offsets[e+1]) cut to [0,
+ * max_rows); ranges must not overlap; max_rows 0..2^24.  b [groups, n, k], contiguous.
+ * n a multiple of 8, 8..2^20; k a multiple of 8, 8..65536; n * k below 2^31.  Row
+ * operands have ld elements from row to row: a multiple of 8, at least the row's elements
+ * and at most 2^21 (a read one may have ld 0: every row the same).  Bases 16-byte aligned,
+ * offsets 4-byte.  Rows of no range are neither read nor written.  With max_rows 0 the row
+ * pointers may be NULL.  Outputs must not overlap inputs.  Errors: MOK_E_NULL,
+ * MOK_E_SHAPE, MOK_E_UNSUPPORTED (types), MOK_E_LAUNCH.  Asynchronous on stream, no
+ * workspace, fixed-order sums, bitwise repeatable. */
+
+/* out[r, c] = sum over i < k of a[r, i] * b[e][c, i] for the rows r of every expert e,
+ * c < n.  a [max_rows, k], out [max_rows, n]. */
+mok_status_t mok_grouped_mm(int32_t type, const void* a, int64_t ld_a, int64_t max_rows,
+                            const int32_t* offsets, int32_t groups, const void* b, int32_t n,
+                            int32_t k, int32_t out_type, void* out, int64_t ld_out,
+                            void* stream);
+
+/* Its gradient with respect to a: d_a[r, i] = sum over c < n of d_out[r, c] * b[e][c, i].
+ * d_out [max_rows, n], d_a [max_rows, k] in out_type. */
+mok_status_t mok_grouped_mm_bwd_rows(int32_t type, const void* d_out, int64_t ld_d_out,
+                                     int64_t max_rows, const int32_t* offsets, int32_t groups,
+                                     const void* b, int32_t n, int32_t k, int32_t out_type,
+                                     void* d_a, int64_t ld_d_a, void* stream);
+
+/* Its gradient with respect to b: d_b[e][c, i] = sum over the rows r of expert e of
+ * d_out[r, c] * a[r, i]; 0 for an expert without rows.  d_b [groups, n, k], contiguous.
+ * With accumulate (MOK_TYPE_FP32 only) the sums are added to what d_b holds.
+ * a_scales NULL: a [max_rows, k] in `type`.  Otherwise a is held in 8 bits: e4m3 codes
+ * [max_rows, k] of ld_a bytes from row to row (a multiple of 16) with scales
+ * [max_rows, k / 32] of ld_a_scales bytes (at least k / 32, at most 2^21), as
+ * mok_quantize_mx8 writes them, k a multiple of 32; a value enters the product in
+ * `type` (rounded to nearest even where its range needs it; NaN for the blocks of scale 255). */
+mok_status_t mok_grouped_mm_bwd_weights(int32_t type, const void* d_out, int64_t ld_d_out,
+                                        const void* a, int64_t ld_a, const uint8_t* a_scales,
+                                        int64_t ld_a_scales, int64_t max_rows,
+                                        const int32_t* offsets, int32_t groups, int32_t n,
+                                        int32_t k, int32_t out_type, void* d_b,
+                                        int32_t accumulate, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Activations held in 8 bits between the forward and the backward pass: MXFP8, e4m3 codes
+ * in blocks of 32 along a row with one e8m0 scale each.
+ *
+ * Common rules.  Values are in `type` (MOK_TYPE_*), rows of ld elements, a multiple of 8.
+ * Codes: one byte an element, ld_codes bytes from row to row, a multiple of 16; scales one
+ * byte a block, ld_scales bytes from row to row.  Every ld at least the row's elements and
+ * at most 2^30.  Bases of values and codes 16-byte aligned.  rows 0..2^31-1 (0: nothing is
+ * done); cols a multiple of 32, 32..65536.  Outputs must not overlap inputs.  Errors as for
+ * the row operators; asynchronous on stream, one launch each, no workspace. */
+
+/* The rule of mok_quantize_mx, and its codes for finite rows.  A block that holds a NaN or
+ * an infinity gets the NaN scale (255) and zero codes. */
+mok_status_t mok_quantize_mx8(int32_t type, const void* src, int64_t ld_src, int64_t rows,
+                              int32_t cols, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                              int64_t ld_scales, void* stream);
+
+/* The values back: dst = code * 2^(scale - 127) in `type` (rounded to nearest even where
+ * its range needs it; NaN for the blocks of scale 255). */
+mok_status_t mok_dequantize_mx8(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
+                                int64_t ld_scales, int64_t rows, int32_t cols, int32_t type,
+                                void* dst, int64_t ld_dst, void* stream);
+
+/* SwiGLU that holds its inputs in 8 bits.  ab [rows, 2 * inter]: gate values a, then up
+ * values b (inter a multiple of 32, 32..32768).  h [rows, inter] = silu(a) * b, in fp32 and
+ * rounded once; codes [rows, 2 * inter] and scales [rows, inter / 16] hold ab as
+ * mok_quantize_mx8 does.  offsets [groups + 1] (groups 1..1024) as the schedule has them:
+ * only rows below offsets[groups] are read and written; NULL: all rows. */
+mok_status_t mok_swiglu_mx8(int32_t type, const void* ab, int64_t ld_ab, int64_t rows,
+                            int32_t inter, const int32_t* offsets, int32_t groups, void* h,
+                            int64_t ld_h, uint8_t* codes, int64_t ld_codes, uint8_t* scales,
+                            int64_t ld_scales, void* stream);
+
+/* Its backward pass from what is held: with a, b the values of codes and scales and
+ * s = 1 / (1 + e^-a),
+ *   d_ab = [dh * b * s * (1 + a * (1 - s)) | dh * a * s],   h = a * s * b
+ * in fp32, rounded once to `type`.  dh [rows, inter], d_ab [rows, 2 * inter], h [rows,
+ * inter] or NULL (not made): the activation again, for the next product's weight gradient.
+ * offsets as above. */
+mok_status_t mok_swiglu_mx8_bwd(int32_t type, const void* dh, int64_t ld_dh,
+                                const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
+                                int64_t ld_scales, int64_t rows, int32_t inter,
+                                const int32_t* offsets, int32_t groups, void* d_ab,
+                                int64_t ld_d_ab, void* h, int64_t ld_h, void* stream);
+
 /* Synchronise `stream`, then read the sticky device status word (MOK_DEV_* bits). */
 mok_status_t mok_read_device_status(const void* ws, void* stream, uint32_t* out);
 

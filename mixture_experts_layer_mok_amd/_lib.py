@@ -46,6 +46,8 @@ EXPORTS = (
     "mok_device_cus", "mok_trace_layout", "mok_moe_fwd_noalloc", "mok_quantize_mx_t",
     "mok_moe_bwd_mx", "mok_schedule_layout", "mok_permute", "mok_permute_bwd", "mok_unpermute",
     "mok_unpermute_bwd", "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4",
+    "mok_grouped_mm", "mok_grouped_mm_bwd_rows", "mok_grouped_mm_bwd_weights", "mok_quantize_mx8",
+    "mok_dequantize_mx8", "mok_swiglu_mx8", "mok_swiglu_mx8_bwd",
 )
 
 
@@ -119,6 +121,18 @@ def load() -> ctypes.CDLL:
         "mok_dequantize_mx4": (ctypes.c_int, [u8p, i64, u8p, i64, i64, i32, i32, vp, i64, vp]),
         "mok_grouped_mx4": (ctypes.c_int, [i32, u8p, i64, u8p, i64, i64, i32p, i32, u8p, u8p, i32,
                                            i32, i32, vp, i64, vp]),
+        "mok_grouped_mm": (ctypes.c_int, [i32, vp, i64, i64, i32p, i32, vp, i32, i32, i32, vp, i64,
+                                          vp]),
+        "mok_grouped_mm_bwd_rows": (ctypes.c_int, [i32, vp, i64, i64, i32p, i32, vp, i32, i32, i32,
+                                                   vp, i64, vp]),
+        "mok_grouped_mm_bwd_weights": (ctypes.c_int, [i32, vp, i64, vp, i64, u8p, i64, i64, i32p,
+                                                      i32, i32, i32, i32, vp, i32, vp]),
+        "mok_quantize_mx8": (ctypes.c_int, [i32, vp, i64, i64, i32, u8p, i64, u8p, i64, vp]),
+        "mok_dequantize_mx8": (ctypes.c_int, [u8p, i64, u8p, i64, i64, i32, i32, vp, i64, vp]),
+        "mok_swiglu_mx8": (ctypes.c_int, [i32, vp, i64, i64, i32, i32p, i32, vp, i64, u8p, i64, u8p,
+                                          i64, vp]),
+        "mok_swiglu_mx8_bwd": (ctypes.c_int, [i32, vp, i64, u8p, i64, u8p, i64, i64, i32, i32p, i32,
+                                              vp, i64, vp, i64, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -300,6 +314,56 @@ def mok_grouped_mx4(a_format, a_codes, ld_a, a_scales, ld_a_scales, max_rows, of
         a_format, _ptr(a_codes), ld_a, _ptr(a_scales), ld_a_scales, max_rows, _ptr(offsets),
         groups, _ptr(b_codes), _ptr(b_scales), n, k, out_type, _ptr(out), ld_out,
         _stream(stream)))
+
+
+def mok_grouped_mm(type, a, ld_a, max_rows, offsets, groups, b, n, k, out_type, out, ld_out,
+                   stream=None) -> None:
+    _check("mok_grouped_mm", load().mok_grouped_mm(
+        type, _ptr(a), ld_a, max_rows, _ptr(offsets), groups, _ptr(b), n, k, out_type, _ptr(out),
+        ld_out, _stream(stream)))
+
+
+def mok_grouped_mm_bwd_rows(type, d_out, ld_d_out, max_rows, offsets, groups, b, n, k, out_type,
+                            d_a, ld_d_a, stream=None) -> None:
+    _check("mok_grouped_mm_bwd_rows", load().mok_grouped_mm_bwd_rows(
+        type, _ptr(d_out), ld_d_out, max_rows, _ptr(offsets), groups, _ptr(b), n, k, out_type,
+        _ptr(d_a), ld_d_a, _stream(stream)))
+
+
+def mok_grouped_mm_bwd_weights(type, d_out, ld_d_out, a, ld_a, a_scales, ld_a_scales, max_rows,
+                               offsets, groups, n, k, out_type, d_b, accumulate=0,
+                               stream=None) -> None:
+    _check("mok_grouped_mm_bwd_weights", load().mok_grouped_mm_bwd_weights(
+        type, _ptr(d_out), ld_d_out, _ptr(a), ld_a, _ptr(a_scales), ld_a_scales, max_rows,
+        _ptr(offsets), groups, n, k, out_type, _ptr(d_b), int(accumulate), _stream(stream)))
+
+
+def mok_quantize_mx8(type, src, ld_src, rows, cols, codes, ld_codes, scales, ld_scales,
+                     stream=None) -> None:
+    _check("mok_quantize_mx8", load().mok_quantize_mx8(
+        type, _ptr(src), ld_src, rows, cols, _ptr(codes), ld_codes, _ptr(scales), ld_scales,
+        _stream(stream)))
+
+
+def mok_dequantize_mx8(codes, ld_codes, scales, ld_scales, rows, cols, type, dst, ld_dst,
+                       stream=None) -> None:
+    _check("mok_dequantize_mx8", load().mok_dequantize_mx8(
+        _ptr(codes), ld_codes, _ptr(scales), ld_scales, rows, cols, type, _ptr(dst), ld_dst,
+        _stream(stream)))
+
+
+def mok_swiglu_mx8(type, ab, ld_ab, rows, inter, offsets, groups, h, ld_h, codes, ld_codes, scales,
+                   ld_scales, stream=None) -> None:
+    _check("mok_swiglu_mx8", load().mok_swiglu_mx8(
+        type, _ptr(ab), ld_ab, rows, inter, _ptr(offsets), groups, _ptr(h), ld_h, _ptr(codes),
+        ld_codes, _ptr(scales), ld_scales, _stream(stream)))
+
+
+def mok_swiglu_mx8_bwd(type, dh, ld_dh, codes, ld_codes, scales, ld_scales, rows, inter, offsets,
+                       groups, d_ab, ld_d_ab, h, ld_h, stream=None) -> None:
+    _check("mok_swiglu_mx8_bwd", load().mok_swiglu_mx8_bwd(
+        type, _ptr(dh), ld_dh, _ptr(codes), ld_codes, _ptr(scales), ld_scales, rows, inter,
+        _ptr(offsets), groups, _ptr(d_ab), ld_d_ab, _ptr(h), ld_h, _stream(stream)))
 
 
 def mok_read_device_status(ws, stream=None) -> int:

@@ -28,6 +28,15 @@ struct Entries {
   decltype(&mok_dequantize_mx4) dequantize_mx4;
   decltype(&mok_grouped_mx4) grouped_mx4;
 } g_fn;
+struct MoreEntries {
+  decltype(&mok_grouped_mm) grouped_mm;
+  decltype(&mok_grouped_mm_bwd_rows) grouped_mm_bwd_rows;
+  decltype(&mok_grouped_mm_bwd_weights) grouped_mm_bwd_weights;
+  decltype(&mok_quantize_mx8) quantize_mx8;
+  decltype(&mok_dequantize_mx8) dequantize_mx8;
+  decltype(&mok_swiglu_mx8) swiglu_mx8;
+  decltype(&mok_swiglu_mx8_bwd) swiglu_mx8_bwd;
+} g_more;  // null until bind_more
 PyObject* g_device = nullptr;  // torch: the current device's index
 PyObject* g_stream = nullptr;  // torch: the current raw stream of a device index
 
@@ -247,8 +256,11 @@ std::vector<int64_t> with_last(const at::Tensor& t, int64_t last) {
   return s;
 }
 
-// src, codes, scales
+// src, codes, scales; PER: elements a byte of codes
+template <int PER>
 PyObject* do_quantize(PyObject* const* a) {
+  const auto fn = PER == 2 ? g_fn.quantize_mx4 : g_more.quantize_mx8;
+  if (!fn) return none();
   const at::Tensor* src = tensor(a[0]);
   Call c(src);
   Matrix ms, mc, mq;
@@ -257,40 +269,43 @@ PyObject* do_quantize(PyObject* const* a) {
   const int ty = type_of(*src);
   if (ty < 0 || !c.stream(&st)) return none();
   const auto u8 = src->options().dtype(at::kByte).requires_grad(false);
-  Output codes(a[1], [&] { return at::empty(with_last(*src, ms.cols / 2), u8); });
+  Output codes(a[1], [&] { return at::empty(with_last(*src, ms.cols / PER), u8); });
   Output scales(a[2], [&] { return at::empty(with_last(*src, ms.cols / 32), u8); });
   if (!rows_of(c, codes.t, &mc, true) || !rows_of(c, scales.t, &mq, true) ||
       codes.t->scalar_type() != at::kByte || scales.t->scalar_type() != at::kByte || mc.rows != ms.rows ||
-      mq.rows != ms.rows || mc.cols != ms.cols / 2 || mq.cols != ms.cols / 32 || !apart(mc.s, {ms.s}) ||
+      mq.rows != ms.rows || mc.cols != ms.cols / PER || mq.cols != ms.cols / 32 || !apart(mc.s, {ms.s}) ||
       !apart(mq.s, {ms.s, mc.s}))
     return none();
-  const auto s = g_fn.quantize_mx4(ty, ms.p, ms.ld, ms.rows, int32_t(ms.cols), static_cast<uint8_t*>(mc.p),
-                                   mc.ld, static_cast<uint8_t*>(mq.p), mq.ld, st);
-  if (s != MOK_OK) return refused("mok_quantize_mx4", s);
+  const auto s = fn(ty, ms.p, ms.ld, ms.rows, int32_t(ms.cols), static_cast<uint8_t*>(mc.p), mc.ld,
+                    static_cast<uint8_t*>(mq.p), mq.ld, st);
+  if (s != MOK_OK) return refused(PER == 2 ? "mok_quantize_mx4" : "mok_quantize_mx8", s);
   PyObject *x = codes.result(), *y = scales.result();
   return x && y ? Py_BuildValue("(NN)", x, y) : nullptr;
 }
 
 // codes, scales, dtype (of an output made here), out
+template <int PER>
 PyObject* do_dequantize(PyObject* const* a) {
+  const auto fn = PER == 2 ? g_fn.dequantize_mx4 : g_more.dequantize_mx8;
+  if (!fn) return none();
   const at::Tensor *codes = tensor(a[0]), *scales = tensor(a[1]);
   Call c(codes);
   Matrix mc, mq, mo;
   void* st;
   const at::ScalarType type = dtype_of(a[2]);
-  if (!rows_of(c, codes, &mc, false) || !rows_of(c, scales, &mq, false) || mc.cols > INT32_MAX / 2 ||
+  if (!rows_of(c, codes, &mc, false) || !rows_of(c, scales, &mq, false) || mc.cols > INT32_MAX / PER ||
       (a[3] == Py_None && type == at::ScalarType::Undefined) || !c.stream(&st))
     return none();
-  Output out(a[3], [&] { return at::empty(with_last(*codes, 2 * mc.cols), codes->options().dtype(type)); });
+  Output out(a[3], [&] { return at::empty(with_last(*codes, PER * mc.cols), codes->options().dtype(type)); });
   if (!rows_of(c, out.t, &mo, true)) return none();
   const int ty = type_of(*out.t);
   if (ty < 0 || codes->scalar_type() != at::kByte || scales->scalar_type() != at::kByte || mc.cols == 0 ||
-      mc.cols % 16 || mq.cols != mc.cols / 16 || mo.cols != 2 * mc.cols || mq.rows != mc.rows ||
+      mc.cols % (32 / PER) || mq.cols != mc.cols / (32 / PER) || mo.cols != PER * mc.cols || mq.rows != mc.rows ||
       mo.rows != mc.rows || !apart(mo.s, {mc.s, mq.s}))
     return none();
-  const auto s = g_fn.dequantize_mx4(static_cast<uint8_t*>(mc.p), mc.ld, static_cast<uint8_t*>(mq.p), mq.ld,
-                                     mc.rows, int32_t(mo.cols), ty, mo.p, mo.ld, st);
-  return s == MOK_OK ? out.result() : refused("mok_dequantize_mx4", s);
+  const auto s = fn(static_cast<uint8_t*>(mc.p), mc.ld, static_cast<uint8_t*>(mq.p), mq.ld, mc.rows,
+                    int32_t(mo.cols), ty, mo.p, mo.ld, st);
+  return s == MOK_OK ? out.result() : refused(PER == 2 ? "mok_dequantize_mx4" : "mok_dequantize_mx8", s);
 }
 
 // a, a_scales, offsets, b, b_scales, dtype (of an output made here), out
@@ -322,6 +337,154 @@ PyObject* do_grouped(PyObject* const* v) {
                                   int32_t(E), at_ptr<uint8_t>(sb), at_ptr<uint8_t>(sbs), int32_t(N),
                                   int32_t(K), ty, mo.p, mo.ld, st);
   return s == MOK_OK ? out.result() : refused("mok_grouped_mx4", s);
+}
+
+// A flag; what has no truth value turns the call down.
+bool flag(Call& c, PyObject* o) {
+  const int t = PyObject_IsTrue(o);
+  if (t < 0) {
+    PyErr_Clear();
+    c.ok = false;
+  }
+  return t > 0;
+}
+bool half_type(at::ScalarType t) { return t == at::kBFloat16 || t == at::kHalf; }
+
+// rows (a or d_out), offsets, b, dtype (of an output made here; None: b's), out
+template <bool FORWARD>
+PyObject* do_product(PyObject* const* v) {
+  const auto fn = FORWARD ? g_more.grouped_mm : g_more.grouped_mm_bwd_rows;
+  const at::Tensor *r = tensor(v[0]), *off = tensor(v[1]), *b = tensor(v[2]);
+  Call c(r);
+  Matrix mr, mo;
+  Span so, sb;
+  if (!fn || !c.on_device(b) || b->dim() != 3) return none();
+  const int64_t E = b->size(0), N = b->size(1), K = b->size(2);
+  const at::ScalarType held = b->scalar_type();
+  const at::ScalarType type = v[3] == Py_None ? held : dtype_of(v[3]);
+  void* st;
+  if (!half_type(held) || E > INT32_MAX || N > INT32_MAX || K > INT32_MAX || !matrix(c, r, &mr, false) ||
+      !flat(c, b, {E, N, K}, held, &sb) || !flat(c, off, {E + 1}, at::kInt, &so) || r->scalar_type() != held ||
+      mr.cols != (FORWARD ? K : N) || (v[4] == Py_None && type != held && type != at::kFloat) || !c.stream(&st))
+    return none();
+  const int64_t cols = FORWARD ? N : K;
+  Output out(v[4], [&] { return at::empty({mr.rows, cols}, r->options().dtype(type).requires_grad(false)); });
+  if (!matrix(c, out.t, &mo, true) || (out.t->scalar_type() != held && out.t->scalar_type() != at::kFloat) ||
+      mo.rows != mr.rows || mo.cols != cols || !apart(mo.s, {mr.s, so, sb}))
+    return none();
+  const auto s = fn(type_of(*r), mr.p, mr.ld, mr.rows, at_ptr<int32_t>(so), int32_t(E), at_ptr<void>(sb), int32_t(N),
+                    int32_t(K), type_of(*out.t), mo.p, mo.ld, st);
+  return s == MOK_OK ? out.result() : refused(FORWARD ? "mok_grouped_mm" : "mok_grouped_mm_bwd_rows", s);
+}
+
+// d_out, a, offsets, a_scales (None: a is not in 8 bits), dtype (of an output made here), out, accumulate
+PyObject* do_product_weights(PyObject* const* v) {
+  const at::Tensor *d = tensor(v[0]), *a = tensor(v[1]), *off = tensor(v[2]),
+                   *as = v[3] == Py_None ? nullptr : tensor(v[3]);
+  Call c(d);
+  Matrix md, ma, ms = {nullptr, 0, 0, 0, {nullptr, nullptr}};
+  Span so, sb;
+  const bool add = flag(c, v[6]);
+  if (!g_more.grouped_mm_bwd_weights || (v[3] != Py_None && !as) || !matrix(c, d, &md, false) ||
+      !matrix(c, a, &ma, false) || (as && !matrix(c, as, &ms, false)) || !c.on_device(off) || off->dim() != 1)
+    return none();
+  const int64_t E = off->size(0) - 1, N = md.cols, K = ma.cols;
+  const at::ScalarType held = d->scalar_type(), type = dtype_of(v[4]);
+  void* st;
+  if (!half_type(held) || a->scalar_type() != (as ? at::kByte : held) || ma.rows != md.rows || E < 1 ||
+      E > INT32_MAX || !flat(c, off, {E + 1}, at::kInt, &so) ||
+      (as && (as->scalar_type() != at::kByte || K % 32 || ms.rows != md.rows || ms.cols != K / 32)) ||
+      (v[5] == Py_None && (add || (type != held && type != at::kFloat))) || !c.stream(&st))
+    return none();
+  Output out(v[5], [&] { return at::empty({E, N, K}, d->options().dtype(type).requires_grad(false)); });
+  if (!out.t) return none();
+  const at::ScalarType made = out.t->scalar_type();
+  if ((made != at::kFloat && (add || made != held)) || !flat(c, out.t, {E, N, K}, made, &sb) ||
+      !apart(sb, {md.s, ma.s, so, ms.s}))
+    return none();
+  const auto s = g_more.grouped_mm_bwd_weights(
+      type_of(*d), md.p, md.ld, ma.p, ma.ld, static_cast<uint8_t*>(ms.p), ms.ld, md.rows, at_ptr<int32_t>(so),
+      int32_t(E), int32_t(N), int32_t(K), type_of(*out.t), at_ptr<void>(sb), add, st);
+  return s == MOK_OK ? out.result() : refused("mok_grouped_mm_bwd_weights", s);
+}
+
+// The offsets whose last says how many rows there are, or None; false where they are neither.
+bool covered(Call& c, PyObject* o, Span* s, int32_t* groups) {
+  *s = {nullptr, nullptr};
+  *groups = 0;
+  if (o == Py_None) return c.ok;
+  const at::Tensor* t = tensor(o);
+  if (!c.on_device(t) || t->dim() != 1 || t->size(0) < 2 || t->size(0) > INT32_MAX ||
+      !flat(c, t, t->sizes(), at::kInt, s))
+    return c.ok = false;
+  *groups = int32_t(t->size(0) - 1);
+  return true;
+}
+
+// ab, offsets, h, codes, scales
+PyObject* do_swiglu(PyObject* const* v) {
+  const at::Tensor* ab = tensor(v[0]);
+  Call c(ab);
+  Matrix ma, mh, mc, mq;
+  Span so;
+  int32_t groups;
+  void* st;
+  if (!g_more.swiglu_mx8 || !matrix(c, ab, &ma, false) || ma.cols == 0 || ma.cols % 64 ||
+      !covered(c, v[1], &so, &groups))
+    return none();
+  const int ty = type_of(*ab);
+  if (ty < 0 || !c.stream(&st)) return none();
+  const int64_t n = ma.rows, I = ma.cols / 2;
+  const auto u8 = ab->options().dtype(at::kByte).requires_grad(false);
+  Output h(v[2], [&] { return at::empty({n, I}, ab->options().requires_grad(false)); });
+  Output codes(v[3], [&] { return at::empty({n, 2 * I}, u8); });
+  Output scales(v[4], [&] { return at::empty({n, I / 16}, u8); });
+  if (!matrix(c, h.t, &mh, true) || !matrix(c, codes.t, &mc, true) || !matrix(c, scales.t, &mq, true) ||
+      h.t->scalar_type() != ab->scalar_type() || codes.t->scalar_type() != at::kByte ||
+      scales.t->scalar_type() != at::kByte || mh.rows != n || mh.cols != I || mc.rows != n || mc.cols != 2 * I ||
+      mq.rows != n || mq.cols != I / 16 || !apart(mh.s, {ma.s, so}) || !apart(mc.s, {ma.s, so, mh.s}) ||
+      !apart(mq.s, {ma.s, so, mh.s, mc.s}))
+    return none();
+  const auto s = g_more.swiglu_mx8(ty, ma.p, ma.ld, n, int32_t(I), at_ptr<int32_t>(so), groups, mh.p, mh.ld,
+                                   static_cast<uint8_t*>(mc.p), mc.ld, static_cast<uint8_t*>(mq.p), mq.ld, st);
+  if (s != MOK_OK) return refused("mok_swiglu_mx8", s);
+  PyObject *x = h.result(), *y = codes.result(), *z = scales.result();
+  return x && y && z ? Py_BuildValue("(NNN)", x, y, z) : nullptr;
+}
+
+// dh, codes, scales, offsets, d_ab, h, with_h
+PyObject* do_swiglu_bwd(PyObject* const* v) {
+  const at::Tensor *dh = tensor(v[0]), *codes = tensor(v[1]), *scales = tensor(v[2]);
+  Call c(dh);
+  Matrix md, mc, mq, ma, mh = {nullptr, 0, 0, 0, {nullptr, nullptr}};
+  Span so;
+  int32_t groups;
+  void* st;
+  const bool with_h = flag(c, v[6]);
+  if (!g_more.swiglu_mx8_bwd || !matrix(c, dh, &md, false) || !matrix(c, codes, &mc, false) ||
+      !matrix(c, scales, &mq, false) || md.cols == 0 || md.cols % 32 || !covered(c, v[3], &so, &groups))
+    return none();
+  const int64_t n = md.rows, I = md.cols;
+  const int ty = type_of(*dh);
+  if (ty < 0 || codes->scalar_type() != at::kByte || scales->scalar_type() != at::kByte || mc.rows != n ||
+      mc.cols != 2 * I || mq.rows != n || mq.cols != I / 16 || !c.stream(&st))
+    return none();
+  const auto as = dh->options().requires_grad(false);
+  Output d_ab(v[4], [&] { return at::empty({n, 2 * I}, as); });
+  if (!matrix(c, d_ab.t, &ma, true) || d_ab.t->scalar_type() != dh->scalar_type() || ma.rows != n ||
+      ma.cols != 2 * I || !apart(ma.s, {md.s, mc.s, mq.s, so}))
+    return none();
+  // (without h, a tensor of no elements that is not returned)
+  Output h(v[5], [&] { return at::empty({with_h ? n : 0, I}, as); });
+  if (with_h && (!matrix(c, h.t, &mh, true) || h.t->scalar_type() != dh->scalar_type() || mh.rows != n ||
+                 mh.cols != I || !apart(mh.s, {md.s, mc.s, mq.s, so, ma.s})))
+    return none();
+  const auto s = g_more.swiglu_mx8_bwd(ty, md.p, md.ld, static_cast<uint8_t*>(mc.p), mc.ld,
+                                       static_cast<uint8_t*>(mq.p), mq.ld, n, int32_t(I), at_ptr<int32_t>(so),
+                                       groups, ma.p, ma.ld, with_h ? mh.p : nullptr, mh.ld, st);
+  if (s != MOK_OK) return refused("mok_swiglu_mx8_bwd", s);
+  PyObject *x = d_ab.result(), *y = with_h ? h.result() : same(Py_None);
+  return x && y ? Py_BuildValue("(NN)", x, y) : nullptr;
 }
 
 // A call with `want` arguments; a C++ exception (a tensor without strides or storage) is a
@@ -370,6 +533,28 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return none();
 }
 
+// bind_more(addresses of the entry points in the order of MoreEntries)
+PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "bind_more: seven addresses are wanted");
+    return nullptr;
+  }
+  void* p[7];
+  for (int i = 0; i < 7; ++i)
+    if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_more: a null address");
+      return nullptr;
+    }
+  g_more = {reinterpret_cast<decltype(g_more.grouped_mm)>(p[0]),
+            reinterpret_cast<decltype(g_more.grouped_mm_bwd_rows)>(p[1]),
+            reinterpret_cast<decltype(g_more.grouped_mm_bwd_weights)>(p[2]),
+            reinterpret_cast<decltype(g_more.quantize_mx8)>(p[3]),
+            reinterpret_cast<decltype(g_more.dequantize_mx8)>(p[4]),
+            reinterpret_cast<decltype(g_more.swiglu_mx8)>(p[5]),
+            reinterpret_cast<decltype(g_more.swiglu_mx8_bwd)>(p[6])};
+  return none();
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 constexpr PyCFunction method() {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F));
@@ -380,9 +565,17 @@ PyMethodDef g_methods[] = {
     {"permute_backward", method<entry<3, f_permute_bwd>>(), METH_FASTCALL, nullptr},
     {"unpermute", method<entry<4, f_unpermute>>(), METH_FASTCALL, nullptr},
     {"unpermute_backward", method<entry<6, do_unpermute_bwd>>(), METH_FASTCALL, nullptr},
-    {"quantize_mx4", method<entry<3, do_quantize>>(), METH_FASTCALL, nullptr},
-    {"dequantize_mx4", method<entry<4, do_dequantize>>(), METH_FASTCALL, nullptr},
+    {"quantize_mx4", method<entry<3, do_quantize<2>>>(), METH_FASTCALL, nullptr},
+    {"dequantize_mx4", method<entry<4, do_dequantize<2>>>(), METH_FASTCALL, nullptr},
     {"grouped_mx4", method<entry<7, do_grouped>>(), METH_FASTCALL, nullptr},
+    {"bind_more", method<bind_more>(), METH_FASTCALL, nullptr},
+    {"grouped_mm", method<entry<5, do_product<true>>>(), METH_FASTCALL, nullptr},
+    {"grouped_mm_backward_rows", method<entry<5, do_product<false>>>(), METH_FASTCALL, nullptr},
+    {"grouped_mm_backward_weights", method<entry<7, do_product_weights>>(), METH_FASTCALL, nullptr},
+    {"quantize_mx8", method<entry<3, do_quantize<1>>>(), METH_FASTCALL, nullptr},
+    {"dequantize_mx8", method<entry<4, do_dequantize<1>>>(), METH_FASTCALL, nullptr},
+    {"swiglu_mx8", method<entry<5, do_swiglu>>(), METH_FASTCALL, nullptr},
+    {"swiglu_mx8_backward", method<entry<7, do_swiglu_bwd>>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

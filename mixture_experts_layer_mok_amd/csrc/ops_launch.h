@@ -1,5 +1,6 @@
-// Arguments and launchers of the row operators and the MXFP4 operators (rows.hip, mx4.hip,
-// grouped_mx4.hip), called by ops_api.hip after its checks.
+// Arguments and launchers of the row operators, the MXFP4 operators, the grouped product of
+// 16-bit rows and the activations in 8 bits (rows.hip, mx4.hip, grouped_mx4.hip, grouped_mm.hip,
+// mx8.hip), called by ops_api.hip after its checks.
 #pragma once
 #include <cstddef>
 #include <tuple>
@@ -79,5 +80,62 @@ struct GroupedArgs {
   int64_t ld_out;
 };
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st);
+
+// Grouped product of 16-bit rows (grouped_mm.hip): C = A B summed over one axis.
+//   kMmOut      out[r, c]  = sum_i a[r, i] b[e][c, i]      left a, right b
+//   kMmRows     d_a[r, i]  = sum_c d_out[r, c] b[e][c, i]  left d_out, right b
+//   kMmWeights  d_b[e][c, i] = sum_r d_out[r, c] a[r, i]   left d_out, right a
+enum MmKind { kMmOut = 0, kMmRows = 1, kMmWeights = 2 };
+struct MmArgs {
+  int32_t type;
+  const void* left;
+  int64_t ld_left;
+  const void* right;  // b [groups, n, k], or a (ld_right; with scales: e4m3 codes, in bytes)
+  int64_t ld_right;
+  const uint8_t* scales;
+  int64_t ld_scales;
+  int64_t max_rows;
+  const int32_t* offsets;
+  int32_t groups, n, k;
+  bool out32, add;
+  void* out;
+  int64_t ld_out;
+};
+mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st);
+
+// Activations in 8 bits (mx8.hip).  ld_val: elements from row to row of src or dst.
+struct Mx8Args {
+  int32_t type;
+  int64_t rows;
+  int32_t cols;
+  const void* src;
+  void* dst;
+  int64_t ld_val;
+  uint8_t* codes;
+  int64_t ld_codes;
+  uint8_t* scales;
+  int64_t ld_scales;
+};
+mok_status_t launch_quantize_mx8(const Mx8Args& a, hipStream_t st);
+mok_status_t launch_dequantize_mx8(const Mx8Args& a, hipStream_t st);
+
+struct SwigluArgs {
+  int32_t type;
+  int64_t rows;
+  int32_t inter;
+  const int32_t* total;  // rows on the device, or null: all
+  const void* in;        // ab, or dh
+  int64_t ld_in;
+  uint8_t* codes;
+  int64_t ld_codes;
+  uint8_t* scales;
+  int64_t ld_scales;
+  void* h;
+  int64_t ld_h;
+  void* d_ab;
+  int64_t ld_d_ab;
+};
+mok_status_t launch_swiglu_mx8(const SwigluArgs& a, hipStream_t st);
+mok_status_t launch_swiglu_mx8_bwd(const SwigluArgs& a, hipStream_t st);
 
 }  // namespace mok

@@ -133,6 +133,29 @@ class MoKLayer:
         return ops.grouped_mx4(a, a_scales, self.schedule_tables()[1], b, b_scales, out=out,
                                dtype=dtype, stream=stream)
 
+    def grouped_mm(self, a, b, out=None, dtype=None, stream=None):
+        """Expert-ordered 16-bit rows times each expert's weights (ops.grouped_mm)."""
+        return ops.grouped_mm(a, self.schedule_tables()[1], b, out=out, dtype=dtype, stream=stream)
+
+    def grouped_mm_backward_rows(self, d_out, b, out=None, dtype=None, stream=None):
+        return ops.grouped_mm_backward_rows(d_out, self.schedule_tables()[1], b, out=out,
+                                            dtype=dtype, stream=stream)
+
+    def grouped_mm_backward_weights(self, d_out, a, a_scales=None, out=None, dtype=torch.float32,
+                                    accumulate=False, stream=None):
+        return ops.grouped_mm_backward_weights(d_out, a, self.schedule_tables()[1],
+                                               a_scales=a_scales, out=out, dtype=dtype,
+                                               accumulate=accumulate, stream=stream)
+
+    def swiglu_mx8(self, ab, h=None, codes=None, scales=None, stream=None):
+        """SwiGLU of the routed rows, its inputs held in 8 bits (ops.swiglu_mx8)."""
+        return ops.swiglu_mx8(ab, self.schedule_tables()[1], h=h, codes=codes, scales=scales,
+                              stream=stream)
+
+    def swiglu_mx8_backward(self, dh, codes, scales, d_ab=None, h=None, with_h=True, stream=None):
+        return ops.swiglu_mx8_backward(dh, codes, scales, self.schedule_tables()[1], d_ab=d_ab, h=h,
+                                       with_h=with_h, stream=stream)
+
     def status(self, stream=None) -> int:
         return L.mok_read_device_status(self.ws, stream)
 

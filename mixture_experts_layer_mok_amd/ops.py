@@ -1,5 +1,5 @@
-"""Torch-facing row operators and MXFP4 operators over the C ABI, for expert functions that
-are not the layer's own:
+"""Torch-facing operators over the C ABI, for expert functions that are not the layer's own: rows
+to expert order and back, grouped products of 16-bit and of MX rows, activations held in 8 bits:
 
     pos, offsets = layer.schedule_tables()             # views of the schedule's tables
     rows = permute(x, pos, torch.empty(max_rows, D))   # tokens to expert order
@@ -9,6 +9,19 @@ are not the layer's own:
     y = unpermute(rows, pos, weights)                  # and back, weighted
     d_rows, d_weights = unpermute_backward(dy, rows, pos, weights, d_rows)
     dx = permute_backward(d_rows, pos)
+
+and with 16-bit products, trained, the activations between the passes in 8 bits:
+
+    held = quantize_mx8(rows)                            # codes, scales
+    ab = grouped_mm(rows, offsets, w_gate_up)            # gate | up
+    h, *held_ab = swiglu_mx8(ab, offsets)
+    y_rows = grouped_mm(h, offsets, w_down)
+    ...
+    dh = grouped_mm_backward_rows(d_y_rows, offsets, w_down)
+    d_ab, h = swiglu_mx8_backward(dh, *held_ab, offsets)
+    d_w_down = grouped_mm_backward_weights(d_y_rows, h, offsets)
+    d_w_gate_up = grouped_mm_backward_weights(d_ab, held[0], offsets, a_scales=held[1])
+    d_rows = grouped_mm_backward_rows(d_ab, offsets, w_gate_up)
 
 Ordinary calls run through the extension module _fast (the same checks and the same C entry
 point in native code); what it does not take runs through the code here, which has the
@@ -20,7 +33,8 @@ synchronising.  Autograd records none of them: inputs may require grad, results 
 gradients are functions of their own (for an autograd.Function to call).  Outputs that are
 passed in count as changed in place, so that a backward pass which saved one raises.
 
-Value tensors are bf16, fp16 or fp32 matrices whose rows are contiguous; the first lies at a
+Value tensors are bf16, fp16 or fp32 (the 16-bit products' operands: bf16 or fp16) matrices whose
+rows are contiguous; the first lies at a
 multiple of 16 bytes, the distance between them may be any multiple of 8 elements.  `stream` is
 a torch stream or a raw handle; by default the current stream of the tensors' device.  Outputs
 may be passed in; those allocated here belong to the stream the work runs on.
@@ -165,6 +179,9 @@ def _bind(lib) -> None:
              "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4")
     module.bind(getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream,
                 *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
+    more = ("mok_grouped_mm", "mok_grouped_mm_bwd_rows", "mok_grouped_mm_bwd_weights",
+            "mok_quantize_mx8", "mok_dequantize_mx8", "mok_swiglu_mx8", "mok_swiglu_mx8_bwd")
+    module.bind_more(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in more))
     _fast = module
 
 
@@ -403,3 +420,265 @@ def grouped_mx4(a, a_scales, offsets, b, b_scales, out=None, dtype=torch.bfloat1
               ld_as, n, pf, E, pb, pq, N, K, _TYPES[out.dtype], po, ld_o, st)
     _written(given)
     return out
+
+
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _experts(b) -> tuple:
+    """The weights of a 16-bit product: experts, columns, elements a row, address, end."""
+    if not isinstance(b, torch.Tensor) or b.dim() != 3 or b.dtype not in _HALVES or \
+            not b.is_contiguous():
+        raise ValueError("b: a contiguous bfloat16 or float16 tensor [E, N, K] is wanted")
+    if max(b.shape) > _MAX:
+        raise ValueError(f"b: at most {_MAX} experts, columns and elements a row")
+    return (*b.shape, *_flat("b", b, b.shape, b.dtype))
+
+
+def _product(fn, name, rows, offsets, b, forward, out, dtype, stream):
+    E, N, K, pb, be = _experts(b)
+    pf, fe = _flat("offsets", offsets, (E + 1,), torch.int32)
+    pr, ld_r, re = _matrix(name, rows, -1, K if forward else N, b.dtype)
+    n, cols = rows.shape[0], N if forward else K
+    if out is None and dtype is not None and dtype not in (b.dtype, torch.float32):
+        raise ValueError(f"dtype: {b.dtype} or float32 is wanted")
+    dev = rows.device
+    _same_device(dev, offsets, b)
+    given = out
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(n, cols, dtype=dtype or b.dtype, device=dev)
+        po, ld_o, oe = _matrix("out", out, n, cols, None, True)
+        if out.dtype is not b.dtype and out.dtype is not torch.float32:
+            raise ValueError(f"out: {b.dtype} or float32 is wanted")
+        _same_device(dev, out)
+        _apart("out", po, oe, ((name, pr, re), ("offsets", pf, fe), ("b", pb, be)))
+        _call(fn, _TYPES[b.dtype], pr, ld_r, n, pf, E, pb, N, K, _TYPES[out.dtype], po, ld_o, st)
+    _written(given)
+    return out
+
+
+def grouped_mm(a, offsets, b, out=None, dtype=None, stream=None):
+    """out[r] = b[e] @ a[r] for the rows r of [offsets[e], offsets[e + 1]), every expert e; the
+    other rows of out stay as they are (undefined where out is allocated here).
+
+    a [max_rows, K] and b [E, N, K], contiguous, in bf16 or fp16; offsets [E + 1] int32, on the
+    device; out [max_rows, N] in their type (the default) or fp32."""
+    if stream is None and _fast is not None:
+        done = _fast.grouped_mm(a, offsets, b, dtype, out)
+        if done is not None:
+            return done
+    return _product("mok_grouped_mm", "a", a, offsets, b, True, out, dtype, stream)
+
+
+def grouped_mm_backward_rows(d_out, offsets, b, out=None, dtype=None, stream=None):
+    """Gradient of grouped_mm with respect to a: out[r] = d_out[r] @ b[e], out [max_rows, K]."""
+    if stream is None and _fast is not None:
+        done = _fast.grouped_mm_backward_rows(d_out, offsets, b, dtype, out)
+        if done is not None:
+            return done
+    return _product("mok_grouped_mm_bwd_rows", "d_out", d_out, offsets, b, False, out, dtype, stream)
+
+
+def grouped_mm_backward_weights(d_out, a, offsets, a_scales=None, out=None, dtype=torch.float32,
+                                accumulate=False, stream=None):
+    """Gradient of grouped_mm with respect to b: out[e] = sum over the rows r of expert e of
+    outer(d_out[r], a[r]), out [E, N, K], contiguous, in fp32 (the default) or d_out's type; 0 for
+    an expert without rows.  With `accumulate` the sums are added to what out (fp32) holds.
+
+    d_out [max_rows, N] bf16 or fp16; a [max_rows, K] in its type, or held in 8 bits: uint8 codes
+    with a_scales [max_rows, K / 32] (quantize_mx8)."""
+    if stream is None and _fast is not None:
+        done = _fast.grouped_mm_backward_weights(d_out, a, offsets, a_scales, dtype, out, accumulate)
+        if done is not None:
+            return done
+    pd, ld_d, de = _matrix("d_out", d_out)
+    if d_out.dtype not in _HALVES:
+        raise ValueError("d_out: bfloat16 or float16 is wanted")
+    n, N = d_out.shape
+    pa, ld_a, ae = _matrix("a", a, n, -1, d_out.dtype if a_scales is None else torch.uint8)
+    K = a.shape[1]
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 1 < len(offsets) <= _MAX:
+        raise ValueError("offsets: a contiguous int32 tensor of experts + 1 elements is wanted")
+    E = len(offsets) - 1
+    pf, fe = _flat("offsets", offsets, (E + 1,), torch.int32)
+    ps, ld_s, se = None, 0, 0
+    if a_scales is not None:
+        if K % 32:
+            raise ValueError("a: a multiple of 32 columns is wanted")
+        ps, ld_s, se = _matrix("a_scales", a_scales, n, K // 32, torch.uint8)
+    if out is None and (accumulate or dtype not in (d_out.dtype, torch.float32)):
+        raise ValueError(f"dtype: {d_out.dtype} or float32 is wanted, and an out to accumulate into")
+    dev = d_out.device
+    _same_device(dev, a, offsets, *(() if a_scales is None else (a_scales,)))
+    given = out
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(E, N, K, dtype=dtype, device=dev)
+        if not isinstance(out, torch.Tensor) or out.dtype not in (d_out.dtype, torch.float32):
+            raise ValueError(f"out: {d_out.dtype} or float32 is wanted")
+        if accumulate and out.dtype is not torch.float32:
+            raise ValueError("out: float32 is wanted to accumulate into")
+        po, oe = _flat("out", out, (E, N, K), out.dtype)
+        _same_device(dev, out)
+        _apart("out", po, oe, (("d_out", pd, de), ("a", pa, ae), ("offsets", pf, fe),
+                               ("a_scales", ps or 0, se)))
+        _call("mok_grouped_mm_bwd_weights", _TYPES[d_out.dtype], pd, ld_d, pa, ld_a, ps, ld_s, n, pf,
+              E, N, K, _TYPES[out.dtype], po, int(bool(accumulate)), st)
+    _written(given)
+    return out
+
+
+def quantize_mx8(src, codes=None, scales=None, stream=None):
+    """MXFP8 codes [..., K] and scales [..., K / 32] (uint8) that hold src [..., K], in blocks of 32
+    along its last axis.  Returns (codes, scales)."""
+    if stream is None and _fast is not None:
+        done = _fast.quantize_mx8(src, codes, scales)
+        if done is not None:
+            return done
+    ty = _type("src", src)
+    K = src.shape[-1] if src.dim() else 0
+    if K == 0 or K % 32:
+        raise ValueError("src: a last axis that is a multiple of 32 is wanted")
+    ps, ld_s, se, n = _rows_of("src", src, K)
+    dev = src.device
+    _same_device(dev)
+    given = codes, scales
+    with _On(dev, stream) as st:
+        if codes is None:
+            codes = torch.empty(src.shape, dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(*src.shape[:-1], K // 32, dtype=torch.uint8, device=dev)
+        pc, ld_c, ce, _ = _rows_of("codes", codes, K, n, torch.uint8, True)
+        pq, ld_q, qe, _ = _rows_of("scales", scales, K // 32, n, torch.uint8, True)
+        _same_device(dev, codes, scales)
+        _apart("codes", pc, ce, (("src", ps, se),))
+        _apart("scales", pq, qe, (("src", ps, se), ("codes", pc, ce)))
+        _call("mok_quantize_mx8", ty, ps, ld_s, n, K, pc, ld_c, pq, ld_q, st)
+    _written(*given)
+    return codes, scales
+
+
+def dequantize_mx8(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that MXFP8 codes [..., K] and scales [..., K / 32] hold, [..., K] in `dtype` (or
+    in out's)."""
+    if stream is None and _fast is not None:
+        done = _fast.dequantize_mx8(codes, scales, dtype, out)
+        if done is not None:
+            return done
+    if not isinstance(codes, torch.Tensor) or codes.dim() < 1 or codes.shape[-1] % 32 or \
+            codes.shape[-1] == 0:
+        raise ValueError("codes: a tensor with a last axis that is a multiple of 32 is wanted")
+    K = codes.shape[-1]
+    pc, ld_c, ce, n = _rows_of("codes", codes, K, -1, torch.uint8)
+    pq, ld_q, qe, _ = _rows_of("scales", scales, K // 32, n, torch.uint8)
+    if out is None and dtype not in _TYPES:
+        raise ValueError("dtype: bfloat16, float16 or float32 is wanted")
+    dev = codes.device
+    _same_device(dev, scales)
+    given = out
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty(codes.shape, dtype=dtype, device=dev)
+        ty = _type("out", out)
+        po, ld_o, oe, _ = _rows_of("out", out, K, n, None, True)
+        _same_device(dev, out)
+        _apart("out", po, oe, (("codes", pc, ce), ("scales", pq, qe)))
+        _call("mok_dequantize_mx8", pc, ld_c, pq, ld_q, n, K, ty, po, ld_o, st)
+    _written(given)
+    return out
+
+
+def _covered(offsets, dev) -> tuple:
+    """The schedule's offsets, whose last says how many rows there are: (address or None, end,
+    experts)."""
+    if offsets is None:
+        return None, 0, 0
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or not 1 < len(offsets) <= _MAX:
+        raise ValueError("offsets: a contiguous int32 tensor of experts + 1 elements is wanted")
+    pf, fe = _flat("offsets", offsets, offsets.shape, torch.int32)
+    _same_device(dev, offsets)
+    return pf, fe, len(offsets) - 1
+
+
+def swiglu_mx8(ab, offsets=None, h=None, codes=None, scales=None, stream=None):
+    """h = silu(a) * b of ab [rows, 2 I] = a | b, with ab held in 8 bits for the backward pass.
+    Returns (h [rows, I], codes [rows, 2 I], scales [rows, 2 I / 32]).
+
+    bf16, fp16 or fp32, I a multiple of 32.  With offsets [E + 1] int32 (the schedule's) only the
+    rows below offsets[E] are read and written, their number being on the device."""
+    if stream is None and _fast is not None:
+        done = _fast.swiglu_mx8(ab, offsets, h, codes, scales)
+        if done is not None:
+            return done
+    ty = _type("ab", ab)
+    pa, ld_a, ae = _matrix("ab", ab)
+    n, cols = ab.shape
+    if cols == 0 or cols % 64:
+        raise ValueError("ab: a multiple of 64 columns is wanted")
+    I = cols // 2
+    dev = ab.device
+    pf, fe, E = _covered(offsets, dev)
+    _same_device(dev)
+    given = h, codes, scales
+    with _On(dev, stream) as st:
+        if h is None:
+            h = torch.empty(n, I, dtype=ab.dtype, device=dev)
+        if codes is None:
+            codes = torch.empty(n, cols, dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(n, cols // 32, dtype=torch.uint8, device=dev)
+        ph, ld_h, he = _matrix("h", h, n, I, ab.dtype, True)
+        pc, ld_c, ce = _matrix("codes", codes, n, cols, torch.uint8, True)
+        pq, ld_q, qe = _matrix("scales", scales, n, cols // 32, torch.uint8, True)
+        _same_device(dev, h, codes, scales)
+        inputs = (("ab", pa, ae), ("offsets", pf or 0, fe))
+        _apart("h", ph, he, inputs)
+        _apart("codes", pc, ce, inputs + (("h", ph, he),))
+        _apart("scales", pq, qe, inputs + (("h", ph, he), ("codes", pc, ce)))
+        _call("mok_swiglu_mx8", ty, pa, ld_a, n, I, pf, E, ph, ld_h, pc, ld_c, pq, ld_q, st)
+    _written(*given)
+    return h, codes, scales
+
+
+def swiglu_mx8_backward(dh, codes, scales, offsets=None, d_ab=None, h=None, with_h=True,
+                        stream=None):
+    """Gradient of swiglu_mx8 from what is held: with a | b the values of codes and scales,
+    d_ab = d silu(a) * b * dh | silu(a) * dh, and the activation again (for the next product's
+    weights' gradient), h = silu(a) * b.  Returns (d_ab [rows, 2 I], h [rows, I], or None without
+    `with_h`), both in dh's type.  offsets as for swiglu_mx8."""
+    if h is not None:
+        with_h = True
+    if stream is None and _fast is not None:
+        done = _fast.swiglu_mx8_backward(dh, codes, scales, offsets, d_ab, h, with_h)
+        if done is not None:
+            return done
+    ty = _type("dh", dh)
+    pd, ld_d, de = _matrix("dh", dh)
+    n, I = dh.shape
+    if I == 0 or I % 32:
+        raise ValueError("dh: a multiple of 32 columns is wanted")
+    pc, ld_c, ce = _matrix("codes", codes, n, 2 * I, torch.uint8)
+    pq, ld_q, qe = _matrix("scales", scales, n, I // 16, torch.uint8)
+    dev = dh.device
+    pf, fe, E = _covered(offsets, dev)
+    _same_device(dev, codes, scales)
+    given = d_ab, h
+    with _On(dev, stream) as st:
+        if d_ab is None:
+            d_ab = torch.empty(n, 2 * I, dtype=dh.dtype, device=dev)
+        if h is None and with_h:
+            h = torch.empty(n, I, dtype=dh.dtype, device=dev)
+        pa, ld_a, ae = _matrix("d_ab", d_ab, n, 2 * I, dh.dtype, True)
+        inputs = (("dh", pd, de), ("codes", pc, ce), ("scales", pq, qe), ("offsets", pf or 0, fe))
+        _apart("d_ab", pa, ae, inputs)
+        ph, ld_h = None, 0
+        if with_h:
+            ph, ld_h, he = _matrix("h", h, n, I, dh.dtype, True)
+            _same_device(dev, h)
+            _apart("h", ph, he, inputs + (("d_ab", pa, ae),))
+        _same_device(dev, d_ab)
+        _call("mok_swiglu_mx8_bwd", ty, pd, ld_d, pc, ld_c, pq, ld_q, n, I, pf, E, pa, ld_a, ph, ld_h,
+              st)
+    _written(*given)
+    return d_ab, h

@@ -1,5 +1,5 @@
-"""Plain float64 forms of the row operators and the MXFP4 operators, for the tests: explicit
-loops over tokens, slots and blocks, sharing nothing with the HIP library."""
+"""Plain float64 forms of the operators beside the layer, for the tests: explicit loops over tokens,
+slots, blocks and experts, sharing nothing with the HIP library."""
 from __future__ import annotations
 
 import numpy as np
@@ -130,3 +130,88 @@ def grouped(a, offsets, b, out, scales8=None):
                 tol[lo:hi] += 8 * 2.0**-13 * (top(a[lo:hi], scales8[0][lo:hi], 2.0**-6) @
                                               top(b[e], scales8[1][e], 1.0).T)
     return out, tol
+
+
+def _ranges(offsets, max_rows):
+    """(expert, first row, end) of every expert that has rows."""
+    for e in range(len(offsets) - 1):
+        lo, hi = max(int(offsets[e]), 0), min(int(offsets[e + 1]), max_rows)
+        if hi > lo:
+            yield e, lo, hi
+
+
+def grouped_mm(a, offsets, b, out):
+    """out (float64, changed in place): b[e] @ a[r] for the rows r of every expert; and the sums of
+    the products' magnitudes, 0 in the other rows."""
+    mag = np.zeros_like(out)
+    for e, lo, hi in _ranges(offsets, a.shape[0]):
+        out[lo:hi] = a[lo:hi] @ b[e].T
+        mag[lo:hi] = np.abs(a[lo:hi]) @ np.abs(b[e]).T
+    return out, mag
+
+
+def grouped_mm_backward_rows(d_out, offsets, b, d_a):
+    mag = np.zeros_like(d_a)
+    for e, lo, hi in _ranges(offsets, d_out.shape[0]):
+        d_a[lo:hi] = d_out[lo:hi] @ b[e]
+        mag[lo:hi] = np.abs(d_out[lo:hi]) @ np.abs(b[e])
+    return d_a, mag
+
+
+def grouped_mm_backward_weights(d_out, a, offsets):
+    d_b = np.zeros((len(offsets) - 1, d_out.shape[1], a.shape[1]))
+    mag = np.zeros_like(d_b)
+    for e, lo, hi in _ranges(offsets, a.shape[0]):
+        d_b[e] = d_out[lo:hi].T @ a[lo:hi]
+        mag[e] = np.abs(d_out[lo:hi]).T @ np.abs(a[lo:hi])
+    return d_b, mag
+
+
+# magnitudes of the 127 finite e4m3 codes without sign
+E4M3 = np.array([(c % 8) / 8 * 2.0**-6 if c < 8 else (1 + (c % 8) / 8) * 2.0**((c >> 3) - 7)
+                 for c in range(127)])
+
+
+def quantize_mx8(x):
+    """(codes [R, K], scales [R, K / 32]) of float64 x: the smallest n in [-127, 127] with
+    amax <= 448 * 2^n, codes by nearest distance, a tie to the even code; the NaN scale and zero
+    codes for a block that is not finite."""
+    R, K = x.shape
+    codes = np.zeros((R, K), np.uint8)
+    scales = np.zeros((R, K // 32), np.uint8)
+    for r in range(R):
+        for b in range(K // 32):
+            v = x[r, 32 * b:32 * b + 32].astype(np.float64)
+            if not np.isfinite(v).all():
+                scales[r, b] = 255
+                continue
+            amax = np.abs(v).max()
+            n = -127
+            if amax > 0:
+                n = max(-127, int(np.floor(np.log2(amax))) - 10)
+                while amax > 448 * 2.0**n:
+                    n += 1
+            u = np.abs(v) * 2.0**-n
+            hi = np.minimum(np.searchsorted(E4M3, u), 126)  # the first code that is not below
+            lo = np.maximum(hi - 1, 0)
+            up, down = E4M3[hi] - u, u - E4M3[lo]
+            pick = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+            codes[r, 32 * b:32 * b + 32] = pick.astype(np.uint8) | (np.signbit(v) * 128).astype(np.uint8)
+            scales[r, b] = n + 127
+    return codes, scales
+
+
+def swiglu(ab):
+    """h = silu(a) * b of ab = a | b."""
+    a, b = np.split(ab, 2, axis=1)
+    return a / (1 + np.exp(-a)) * b
+
+
+def swiglu_backward(ab, dh):
+    """d_ab, and the size of the terms that each element adds up (s * b * dh and a s (1 - s) * b * dh
+    for the gate's)."""
+    a, b = np.split(ab, 2, axis=1)
+    s = 1 / (1 + np.exp(-a))
+    d = np.concatenate([dh * b * s * (1 + a * (1 - s)), dh * a * s], axis=1)
+    terms = np.concatenate([np.abs(dh * b * s) * (1 + np.abs(a * (1 - s))), np.abs(dh * a * s)], axis=1)
+    return d, terms
