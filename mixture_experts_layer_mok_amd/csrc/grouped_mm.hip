@@ -115,6 +115,10 @@ __global__ __launch_bounds__(256) void k_grouped_mm(MmArgs p) {
 }  // namespace
 
 mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st) {
+  if (!a.scales)
+    return kind == kMmOut    ? launch_mm_tiles_out(a, st)
+           : kind == kMmRows ? launch_mm_tiles_rows(a, st)
+                             : launch_mm_tiles_weights(a, st);
   const int N = kind == kMmOut ? a.n : a.k;
   // every expert may end inside a tile
   const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kTile - 1)) / kTile);
