@@ -9,46 +9,53 @@
 //
 // Fragments of 16 x 16 x 32: lane l holds row l % 16 of its operand, elements 8 (l / 16) .. +8 of
 // the slice's 32.
-//   kAlong: LDS rows of 128 bytes, 8 chunks of 16 bytes, chunk c of row r at place
-//     c ^ (r & 7) ^ ((r >> 3) & 1): the 16 rows that one pass of a 16-byte read takes at one chunk
-//     then cover all 64 banks.
+//   kAlong: LDS rows of 128 bytes, 8 chunks of 16 bytes, chunk c of row r at place c ^ (r & 7).  A
+//     read of 16 rows at 4 chunks each takes the LDS 4.1 clocks so, 8.0 with another term
+//     (r >> 3) & 1 in the place (which suits reads of 32 rows at 2 chunks), 16 as the rows come.
 //   kAcross: LDS rows of one summed element, 16 columns (32 bytes) a block; the fragment comes
 //     from two transposing reads (ds_read_b64_tr_b16: lane i of 16 receives element i % 4 of the
 //     8 bytes that lanes i / 4, 4 + i / 4, 8 + i / 4 and 12 + i / 4 address), summed elements
-//     8 g .. +4 and 8 g + 4 .. +4 for lane group g.  Block c of element k lies at place
-//     c ^ (k & 3) ^ 4 ((k >> 3) & 1): the eight elements of a pass lie in eight places of the 256
-//     bytes that cover the banks.
+//     8 g .. +4 and 8 g + 4 .. +4 for lane group g.  A pass reads a block of eight elements, 0..3
+//     and 8..11 for one; they lie in eight places of the 256 bytes that cover the banks: within a
+//     load (two rows of 512 bytes, or four of 256) block c of its row x lies at c ^ x, and the loads
+//     lie further apart than their 1 KB.  So a lane needs two (or four) read addresses for all
+//     blocks, the rest being the reads' own offset.
 //
 // Rows past an operand's last are read as its last one and never stored (kAlong); chunks and
 // columns past the end, and summed elements past the last, as zeros (an out-of-range offset reads
 // no memory).
 #pragma once
-#include "gemm_bf16.h"
 #include "ops_launch.h"
+#include "gemm_mx4.h"
 
 namespace mok {
 namespace g16 {
 
 constexpr int kThr = 256;
 constexpr int kDeep = 64;                    // summed elements a step
-constexpr uint32_t kStage = 32768;           // bytes of one operand's stage
+constexpr uint32_t kStage = 35840;           // bytes of one operand's stage
 constexpr uint32_t kPast = 0x80000000u;      // added to an offset: out of every resource's range
-constexpr int64_t kFar = int64_t(kPast);
 
 static __shared__ __align__(1024) v4u s_a[2 * kStage / 16];
 static __shared__ __align__(1024) v4u s_b[2 * kStage / 16];
 static __shared__ __align__(1024) v4u s_out[4 * 4096 / 16];  // results on their way out, 4 KB a wave
 
-typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t v2u_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v4u lds_w16;
 typedef __attribute__((address_space(3))) v2u_t lds_w8;
 
+// c += a * b.  All MFMAs of a tile are inline asm with their sums in accumulation registers: 64 blocks
+// take all 256 of those, and with the builtin the compiler moved blocks between the register files
+// inside the loop as soon as some of them were named by asm (lds_load16_mfma4).  What the compiler
+// then does not see to: before the first MFMA come waits and reads (the sums' zeros are long
+// written), a block is used again only after all others, and run() ends with wait states before the
+// sums are read otherwise.
 template <int TYPE>
-__device__ __forceinline__ f32x4_t mfma(v4u a, v4u b, f32x4_t c) {
-  if (TYPE == MOK_TYPE_BF16) return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
-                                                0, 0, 0);
+__device__ __forceinline__ void mfma(v4u a, v4u b, f32x4_t& c) {
+  if (TYPE == MOK_TYPE_BF16)
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+  else
+    asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 // (Two bf16 conversions, not one of a pair: that instruction makes the compiler move accumulators
 // between its register files inside the loop that sums them.)
@@ -71,49 +78,47 @@ __device__ __forceinline__ int scalar(int v) {
 
 enum Kind { kAlong = 0, kAcross = 1 };
 
-// One operand of a tile.  NB: blocks of 16 rows a wave; the tile has 32 NB rows, and NB loads a
-// wave and step.
+// One operand of a tile.  NB: blocks of 16 rows a wave (8 or 4, along also 2); the tile has 32 NB
+// rows, and a wave NB loads a step.
 template <int KIND, int NB>
 struct Operand {
   static constexpr int kLanes = KIND == kAlong ? 8 : 4 * NB;  // lanes of a load that one LDS row takes
+  static constexpr int kRows = 64 / kLanes;                   // LDS rows a load
+  static_assert(KIND == kAlong || NB >= 4);
   i32x4_t r;
   uint32_t off[NB];
   int left;       // what is left of the summed axis at the next step to be loaded: chunks of 8
                   // elements (kAlong), elements (kAcross)
-  int at;         // this lane's chunk, or its element within load 0, of a step
   uint32_t step;  // bytes from step to step
 
+  // This lane's chunk, or its element of load q, of a step.
+  static __device__ __forceinline__ int at(int q) {
+    const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    return KIND == kAlong ? (l & 7) ^ (l >> 3) : (q * 4 + w) * kRows + l / kLanes;
+  }
   // base: element 0 of the operand's first row (kAlong) or of its first summed element (kAcross);
   // rows: rows, or columns, that there are; ld: elements from line to line.
   __device__ __forceinline__ void init(const void* base, int64_t ld, int rows, int summed) {
     const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint64_t x = reinterpret_cast<uint64_t>(base);
     r = i32x4_t{scalar(int(uint32_t(x))), scalar(int(uint32_t(x >> 32) & 0xFFFFu)), int(kPast), 0x00020000};
-    if (KIND == kAlong) {
-      at = (l & 7) ^ (l >> 3) ^ (w & 1);
-      left = summed / 8;
-      step = 128;
+    left = KIND == kAlong ? summed / 8 : summed;
+    step = KIND == kAlong ? kDeep * 2 : uint32_t(kDeep * ld * 2);
 #pragma unroll
-      for (int q = 0; q < NB; ++q)
-        off[q] = uint32_t(min((q * 4 + w) * 8 + (l >> 3), rows - 1)) * uint32_t(ld * 2) + at * 16;
-    } else {
-      constexpr int kRows = 64 / kLanes;  // summed elements a load
-      at = w * kRows + l / kLanes;
-      left = summed;
-      step = uint32_t(kDeep * ld * 2);
-#pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        const int k = (q * 4 + w) * kRows + l / kLanes, p = l % kLanes;
-        const int chunk = 2 * ((p >> 1) ^ (k & 3) ^ (4 * ((k >> 3) & 1))) + (p & 1);
-        off[q] = (uint32_t(k) * uint32_t(ld * 2) + chunk * 16) | (8 * chunk < rows ? 0u : kPast);
+    for (int q = 0; q < NB; ++q) {
+      if (KIND == kAlong) {
+        off[q] = uint32_t(min((q * 4 + w) * 8 + (l >> 3), rows - 1)) * uint32_t(ld * 2) + at(q) * 16;
+      } else {
+        const int p = l % kLanes, chunk = 2 * ((p >> 1) ^ (l / kLanes)) + (p & 1);
+        off[q] = (uint32_t(at(q)) * uint32_t(ld * 2) + chunk * 16) | (8 * chunk < rows ? 0u : kPast);
       }
     }
+    cut();
   }
-  // Load q of the next step into the stage at LDS address `to`.
-  __device__ __forceinline__ void load(int q, uint32_t to) const {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int mine = KIND == kAlong ? at : at + q * 4 * (64 / kLanes);
-    dma16_at<false>(r, off[q] | (mine < left ? 0u : kPast), 0u, to + (q * 4 + w) * 1024);
+  // Chunks or elements that the next step no longer has: out of range from here on.
+  __device__ __forceinline__ void cut() {
+#pragma unroll
+    for (int q = 0; q < NB; ++q) off[q] |= at(q) < left ? 0u : kPast;
   }
   __device__ __forceinline__ void next() {
     left -= KIND == kAlong ? kDeep / 8 : kDeep;
@@ -121,6 +126,16 @@ struct Operand {
     r.x = scalar(int(uint32_t(base)));
     r.y = scalar(int(uint32_t(base >> 32)));
   }
+  __device__ __forceinline__ bool whole() const { return left >= (KIND == kAlong ? kDeep / 8 : kDeep); }
+  // LDS byte of load j = 4 q + w in its stage.
+  static constexpr uint32_t place_of(int j) {
+    return KIND == kAlong ? j * 1024 : NB == 8 ? j * 1088 + (j >> 2) * 128 : j * 1024 + (j >> 1) * 128;
+  }
+  static __device__ __forceinline__ uint32_t place(int q, uint32_t to) {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    return to + place_of(4 * q) + place_of(w);
+  }
+  __device__ __forceinline__ void load(int q, uint32_t to) const { dma16_at<false>(r, off[q], 0u, place(q, to)); }
   __device__ __forceinline__ void uniform() {
     r.x = scalar(r.x);
     r.y = scalar(r.y);
@@ -131,34 +146,47 @@ struct Operand {
   }
 };
 
-// LDS byte addresses of this lane's fragment reads in stage 0.
+// LDS byte addresses of this lane's fragment reads.
 template <int KIND, int NB>
 struct FragAt {
-  static constexpr int kAddr = KIND == kAlong ? 2 : NB;
-  static constexpr uint32_t kRow = 64 * NB;  // kAcross: bytes of a summed element
+  typedef Operand<KIND, NB> Op;
+  static constexpr int kAddr = KIND == kAlong ? 2 : Op::kRows;
+  static_assert(Op::place_of(31) + 1024 <= kStage);
   uint32_t p[kAddr];
 
   // half: which half of the tile's rows the wave has
   __device__ __forceinline__ void init(uint32_t base, int half) {
     const int l = threadIdx.x & 63, r = l & 15, g = l >> 4;
-    if (KIND == kAlong) {
-      const int sw = (r & 7) ^ ((r >> 3) & 1);
 #pragma unroll
-      for (int s = 0; s < kAddr; ++s) p[s] = base + uint32_t(half * 16 * NB + r) * 128 + (((4 * s + g) ^ sw) * 16);
-    } else {
-      const int k = 8 * g + (r >> 2), f = (k & 3) ^ (4 * ((k >> 3) & 1));
-#pragma unroll
-      for (int i = 0; i < kAddr; ++i)
-        p[i] = base + uint32_t(k) * kRow + uint32_t((half * NB + i) ^ f) * 32 + (r & 3) * 8;
+    for (int x = 0; x < kAddr; ++x) {
+      if (KIND == kAlong) {
+        p[x] = base + uint32_t(half * 16 * NB + r) * 128 + (((4 * x + g) ^ (r & 7)) * 16);
+      } else {
+        const int k = 8 * g + (r >> 2), y = k % Op::kRows;
+        p[x] = base + Op::place_of(k / Op::kRows) + y * (64 * NB) + half * (32 * NB) + (x ^ y) * 32 + (r & 3) * 8;
+      }
     }
   }
-  // Fragment i of slice s of the stage at byte `stage`; part: 0 or 1 of kAcross' two reads.
-  __device__ __forceinline__ v4u along(int s, int i, uint32_t stage) const {
-    return *reinterpret_cast<lds_cv4u*>(uintptr_t(p[KIND == kAlong ? s : 0] + stage + uint32_t(i) * 2048));
+  // The same in the stage at byte `stage`, opaque, so that what differs by block and slice becomes
+  // the reads' own offset and no address is computed between the MFMAs.
+  __device__ __forceinline__ FragAt in(uint32_t stage) const {
+    FragAt f;
+#pragma unroll
+    for (int x = 0; x < kAddr; ++x) {
+      f.p[x] = p[x] + stage;
+      asm volatile("" : "+v"(f.p[x]));
+    }
+    return f;
   }
-  __device__ __forceinline__ v2u_t across(int s, int i, int part, uint32_t stage) const {
-    const v4s_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_v4s*>(
-        uintptr_t(p[KIND == kAcross ? i : 0] + stage + (32 * s + 4 * part) * kRow)));
+  // Fragment i of slice s; part: 0 or 1 of kAcross' two reads.
+  __device__ __forceinline__ v4u along(int s, int i) const {
+    return *reinterpret_cast<lds_cv4u*>(uintptr_t(p[KIND == kAlong ? s : 0] + uint32_t(i) * 2048));
+  }
+  __device__ __forceinline__ v2u_t across(int s, int i, int part) const {
+    // (32 elements on, and 4 on, the places of the loads are the same distance apart for every lane)
+    const uint32_t o = Op::place_of(32 / Op::kRows) * s + Op::place_of(4 / Op::kRows) * part;
+    const v4s_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        reinterpret_cast<lds_v4s*>(uintptr_t(p[i % kAddr] + o + i / kAddr * (32 * kAddr))));
     return __builtin_bit_cast(v2u_t, v);
   }
 };
@@ -193,48 +221,96 @@ struct Tile {
   };
 
   // Read r of a slice's kReads.
-  __device__ __forceinline__ void read(Frag& f, int s, int r, uint32_t stage) const {
+  static __device__ __forceinline__ void read(Frag& f, const FragAt<AK, IB>& fa, const FragAt<BK, JB>& fb, int s, int r) {
     constexpr int kB = BK == kAlong ? JB : 2 * JB;
     if (r < kB) {
       if (BK == kAlong) {
-        f.b[r % JB] = fb.along(s, r, stage);
+        f.b[r % JB] = fb.along(s, r);
       } else {
-        const v2u_t v = fb.across(s, r >> 1, r & 1, stage);
+        const v2u_t v = fb.across(s, r >> 1, r & 1);
         f.b[(r >> 1) % JB][2 * (r & 1)] = v.x;
         f.b[(r >> 1) % JB][2 * (r & 1) + 1] = v.y;
       }
     } else {
       const int x = r - kB;
       if (AK == kAlong) {
-        f.a[x % IB] = fa.along(s, x, stage);
+        f.a[x % IB] = fa.along(s, x);
       } else {
-        const v2u_t v = fa.across(s, x >> 1, x & 1, stage);
+        const v2u_t v = fa.across(s, x >> 1, x & 1);
         f.a[(x >> 1) % IB][2 * (x & 1)] = v.x;
         f.a[(x >> 1) % IB][2 * (x & 1) + 1] = v.y;
       }
     }
   }
 
-  // The MFMAs of a slice on f; between them the reads of slice RS (of the stage at rd) into fr,
-  // and, with LOAD, the next step's loads into the stage at wr.
-  template <int RS, bool LOAD>
-  __device__ __forceinline__ void slice(const A& a, const B& b, const Frag& f, Frag& fr, uint32_t rd, uint32_t wr) {
-    constexpr int kM = IB * JB;
+  // A step's MFMAs, 2 kM of them, slice 0's on f0 and then slice 1's on f1, and what happens
+  // between them, by the MFMA it follows:
+  //   0 .. kRead0        slice 1's fragments are read into f1;
+  //   kFree              every wave has read the last of this step's stage;
+  //   from kFree on      the loads of the step after the next into it, spread over the rest of the
+  //                      step: in a burst they hold up the MFMAs behind them;
+  //   kM + kLanded       the next step has landed (mine by the wait, everyone's by the barrier);
+  //   from there on      its slice 0 is read into f0.
+  // One wave a SIMD issues everything, an MFMA every 16 clocks and three other instructions beside
+  // it, so nothing stands between MFMAs that waits for the instruction before it: read addresses are
+  // ready before the step (FragAt::in; computed at each read they cost 7% of the product), and the
+  // loads' wait states are MFMAs (11%).
+  static constexpr int kM = IB * JB;
+  static constexpr int kRead0 = kM * 5 / 16, kFree = kM / 2 - 1, kLanded = kM / 4 - 1, kRead1 = kM / 2;
+  // Whole tiles take a load with four MFMAs (lds_load16_mfma4), never the step's last eight.
+  static constexpr bool kWith4 = kM == 64;
+  static constexpr int load_slot(int q) {
+    return kWith4 ? (kFree + 1) + q * 22 / 16 * 4 : kFree + 1 + q * (2 * kM - kFree - 2) / kLoads;
+  }
+  static constexpr int loads_before(int slot) {
+    int n = 0;
+    while (n < kLoads && load_slot(n) < slot) ++n;
+    return n;
+  }
+  static constexpr int reads_before(int x, int span) {
+    return x <= 0 ? 0 : x >= span ? kReads : (x * kReads + span - 1) / span;
+  }
+  template <int H, int M>
+  __device__ __forceinline__ void slot(const A& a, const B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
+                                       const FragAt<BK, JB>& rb, uint32_t wr) {
+    constexpr int i = M / JB, j = M % JB;
+    constexpr int q0 = loads_before(H * kM + M), q1 = loads_before(H * kM + M + 1);
+    static_assert(!kWith4 || load_slot(kLoads - 1) < 2 * kM - 8);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (kWith4 && q1 > q0) {
+      mx4::lds_load16_mfma4<TYPE == MOK_TYPE_FP16>(
+          q0 < IB ? a.r : b.r, q0 < IB ? a.off[q0 % IB] : b.off[(q0 + JB - IB) % JB],
+          q0 < IB ? A::place(q0, lds_addr(s_a) + wr) : B::place(q0 - IB, lds_addr(s_b) + wr), f.a[i], f.b[j],
+          f.b[j + 1], f.b[j + 2], f.b[j + 3], acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+    } else if constexpr (!kWith4 || loads_before(H * kM + M + 1) == loads_before((H * kM + M) / 4 * 4)) {
+      mfma<TYPE>(f.b[j], f.a[i], acc[i][j]);
+    }  // (else it was one of the four of a load)
+    if constexpr (H == 0 && M == kFree) {
+      wait_lds();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+    if constexpr (H == 1 && M == kLanded) {
+      wait_vmcnt<loads_before(kM + kLanded)>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+    constexpr int kFirst = H == 0 ? 0 : kLanded + 1, kSpan = H == 0 ? kRead0 : kRead1;
+    constexpr int r0 = reads_before(M - kFirst, kSpan), r1 = reads_before(M - kFirst + 1, kSpan);
 #pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      const int i = m / JB, j = m % JB;
-      __builtin_amdgcn_sched_barrier(0);
-      acc[i][j] = mfma<TYPE>(f.b[j], f.a[i], acc[i][j]);
+    for (int r = r0; r < r1; ++r) read(fr, ra, rb, H == 0 ? 1 : 0, r);
+    if constexpr (!kWith4) {
 #pragma unroll
-      for (int r = m * kReads / kM; r < (m + 1) * kReads / kM; ++r) read(fr, RS, r, rd);
-      if (LOAD) {
-#pragma unroll
-        for (int q = m * kLoads / kM; q < (m + 1) * kLoads / kM; ++q) {
-          if (q < IB) a.load(q, lds_addr(s_a) + wr);
-          else b.load(q - IB, lds_addr(s_b) + wr);
-        }
+      for (int q = q0; q < q1; ++q) {
+        if (q < IB) a.load(q, lds_addr(s_a) + wr);
+        else b.load(q - IB, lds_addr(s_b) + wr);
       }
     }
+  }
+  template <int H, int... M>
+  __device__ __forceinline__ void half(const A& a, const B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
+                                       const FragAt<BK, JB>& rb, uint32_t wr, std::integer_sequence<int, M...>) {
+    (slot<H, M>(a, b, f, fr, ra, rb, wr), ...);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -248,7 +324,9 @@ struct Tile {
 #pragma unroll
       for (int q = 0; q < JB; ++q) b.load(q, lds_addr(s_b) + ks * kStage);
       a.next();
+      a.cut();
       b.next();
+      b.cut();
     }
     asm volatile("" ::: "memory");
   }
@@ -265,32 +343,39 @@ struct Tile {
     for (int i = 0; i < IB; ++i)
 #pragma unroll
       for (int j = 0; j < JB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    wait_all_but(kLoads + stores);  // step 0
+    wait_all_but(stores);  // steps 0 and 1
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     Frag f0, f1;
 #pragma unroll
-    for (int r = 0; r < kReads; ++r) read(f0, 0, r, 0);
+    for (int r = 0; r < kReads; ++r) read(f0, fa, fb, 0, r);
     uint32_t cur = 0;
+    FragAt<AK, IB> na = fa.in(0);
+    FragAt<BK, JB> nb = fb.in(0);
     for (int ks = 0; ks < steps; ++ks) {
-      slice<1, false>(a, b, f0, f1, cur, cur);
-      // step ks + 1 has landed (mine by the wait, everyone's by the barrier), and every wave has
-      // read the last of this step's stage
-      if (ks == 0) wait_all_but(stores);
-      else wait_vmcnt<0>();
-      wait_lds();
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      const uint32_t nxt = cur ^ kStage;
-      slice<0, true>(a, b, f1, f0, nxt, cur);
+      const uint32_t nxt = kStage - cur;
+      half<0>(a, b, f0, f1, na, nb, cur, std::make_integer_sequence<int, kM>());
+      na = fa.in(nxt);
+      nb = fb.in(nxt);
+      half<1>(a, b, f1, f0, na, nb, cur, std::make_integer_sequence<int, kM>());
       a.next();
       b.next();
+      if (!a.whole()) {
+        asm volatile("");  // a branch: as selects the cut would stand in every step
+        a.cut();
+      }
+      if (!b.whole()) {
+        asm volatile("");
+        b.cut();
+      }
       cur = nxt;
     }
-    // every load has landed and every wave has read its last fragments: the stages are free
+    // every load has landed and every wave has read its last fragments: the stages are free; and the
+    // last sums are there (seven wait states after an MFMA of four passes)
     wait_loads_and_lds();
     __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    asm volatile("s_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // Memory operations that store() issues for results in 16 and in 32 bits.
@@ -319,7 +404,8 @@ struct Tile {
       for (int j0 = 0; j0 < JB; j0 += kJ) {
 #pragma unroll
         for (int j = j0; j < j0 + kJ; ++j) {
-          const f32x4_t c = acc[i][j];
+          f32x4_t c = acc[i][j];
+          asm volatile("" : "+a"(c));  // read out here, not for all blocks before the kinds of store part
           if (OUT32)
             *reinterpret_cast<lds_w16*>(uintptr_t(area + r * 256 + (((4 * (j - j0) + g) ^ r) * 16))) =
                 __builtin_bit_cast(v4u, c);
@@ -344,6 +430,7 @@ struct Tile {
           buf_st16<kCpolStream>(ro, at, v);
         }
         asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);  // (else the compiler holds so many at once that it spills)
       }
   }
 };

@@ -110,6 +110,32 @@ __device__ __forceinline__ void lds_load16(const i32x4_t& rsrc, uint32_t voff, u
                : "memory", "m0");
 }
 
+// The same load with four MFMAs of 16 x 16 x 32 (c[j] += b[j] * a) in the place of its wait states:
+// the matrix cores work through them, where s_nop would leave them idle for an MFMA's length.  (Bound
+// by the wave's issue slots, the K loop of the 16-bit product lost a tenth of its time to them.)
+// The compiler does not know that c holds MFMA results: it may use them otherwise only after at
+// least four more MFMAs.
+template <bool F16>
+__device__ __forceinline__ void lds_load16_mfma4(const i32x4_t& rsrc, uint32_t voff, uint32_t lds_wave_addr,
+                                                 v4u a, v4u b0, v4u b1, v4u b2, v4u b3, f32x4_t& c0, f32x4_t& c1,
+                                                 f32x4_t& c2, f32x4_t& c3) {
+  const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_wave_addr);
+  if (F16)
+    asm volatile("s_mov_b32 m0, %11\n\tv_mfma_f32_16x16x32_f16 %0, %5, %4, %0\n\t"
+                 "v_mfma_f32_16x16x32_f16 %1, %6, %4, %1\n\tv_mfma_f32_16x16x32_f16 %2, %7, %4, %2\n\t"
+                 "v_mfma_f32_16x16x32_f16 %3, %8, %4, %3\n\tbuffer_load_dwordx4 %9, %10, 0 offen lds"
+                 : "+a"(c0), "+a"(c1), "+a"(c2), "+a"(c3)
+                 : "v"(a), "v"(b0), "v"(b1), "v"(b2), "v"(b3), "v"(voff), "s"(rsrc), "s"(m0)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %11\n\tv_mfma_f32_16x16x32_bf16 %0, %5, %4, %0\n\t"
+                 "v_mfma_f32_16x16x32_bf16 %1, %6, %4, %1\n\tv_mfma_f32_16x16x32_bf16 %2, %7, %4, %2\n\t"
+                 "v_mfma_f32_16x16x32_bf16 %3, %8, %4, %3\n\tbuffer_load_dwordx4 %9, %10, 0 offen lds"
+                 : "+a"(c0), "+a"(c1), "+a"(c2), "+a"(c3)
+                 : "v"(a), "v"(b0), "v"(b1), "v"(b2), "v"(b3), "v"(voff), "s"(rsrc), "s"(m0)
+                 : "memory", "m0");
+}
+
 // SHIFT: some row's scales do not start at a 16-byte address or are not whole 16-byte pieces.
 //
 // Where a tile's operands come from, and its direct-to-LDS loads.
