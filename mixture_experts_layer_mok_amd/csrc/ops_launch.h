@@ -102,6 +102,7 @@ struct MmArgs {
   int64_t ld_out;
 };
 mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st);
+mok_status_t launch_mm_few(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_tiles_out(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_tiles_rows(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_tiles_weights(const MmArgs& a, hipStream_t st);
