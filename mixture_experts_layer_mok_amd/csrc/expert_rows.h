@@ -12,40 +12,58 @@ __device__ __forceinline__ void expert_rows(const MmArgs& p, int e, int* lo, int
   *hi = int(min(int64_t(p.offsets[e + 1]), p.max_rows));
 }
 
-// The m-tiles of all experts (each expert's rows cut from its first row on into tiles of TM),
-// numbered in expert order.  Every wave scans the experts, 64 at a time; with at most 64 of them
-// they are read once.
-template <int TM>
-struct RowTiles {
-  int lo, hi, incl;  // this lane's expert of the current 64: rows, m-tiles up to it
-  int tiles;         // this lane's expert's
-  int total;         // m-tiles of all experts
+// Sums of x over the lanes up to this one (gfx9 DPP: within rows of 16 lanes, then across them).
+__device__ __forceinline__ int scan64(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false);  // row_shr:1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return x;
+}
+__device__ __forceinline__ int sum64(int x) { return __builtin_amdgcn_readlane(scan64(x), 63); }
 
-  __device__ __forceinline__ void scan(const MmArgs& p, int e0) {
+// The m-tiles of all experts (each expert's rows cut from its first row on into tiles of `tall`),
+// numbered in expert order; an expert without rows has `least` of them (0 or 1).  Every wave scans
+// the experts, 64 at a time, all lanes active; with at most 64 of them they are read once.
+struct RowTiles {
+  int tall, least;
+  int lo, hi;   // this lane's expert of the current 64: rows
+  bool mine;    // there is such an expert
+  int tiles, incl;  // its m-tiles, and those up to it
+  int total;    // m-tiles of all experts
+
+  __device__ __forceinline__ void read(const MmArgs& p, int e0) {
     const int lane = threadIdx.x & 63;
     lo = hi = 0;
-    if (e0 + lane < p.groups) expert_rows(p, e0 + lane, &lo, &hi);
-    tiles = hi > lo ? (hi - lo + TM - 1) / TM : 0;
-    incl = tiles;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int u = __shfl_up(incl, d);
-      if (lane >= d) incl += u;
-    }
+    mine = e0 + lane < p.groups;
+    if (mine) expert_rows(p, e0 + lane, &lo, &hi);
   }
-  __device__ __forceinline__ void init(const MmArgs& p) {
+  __device__ __forceinline__ int tiles_of(int h) const { return hi > lo ? (hi - lo + h - 1) / h : 0; }
+  __device__ __forceinline__ void scan() {
+    tiles = hi > lo ? tiles_of(tall) : mine ? least : 0;
+    incl = scan64(tiles);
+  }
+  // have: the experts, at most 64, are read already.
+  __device__ __forceinline__ void init(const MmArgs& p, int tall_, int least_ = 0, bool have = false) {
+    tall = tall_;
+    least = least_;
     total = 0;
     for (int e0 = 0; e0 < p.groups; e0 += 64) {
-      scan(p, e0);
+      if (!have) read(p, e0);
+      scan();
       total += __builtin_amdgcn_readlane(incl, 63);
     }
   }
-  // m-tile m < total: its expert, first row and rows
-  __device__ __forceinline__ void find(const MmArgs& p, int m, int* e, int* r0, int* rows) {
+  // m-tile m < total: its expert, first row and rows, its number among the expert's m-tiles and
+  // how many those are.
+  __device__ __forceinline__ void find(const MmArgs& p, int m, int* e, int* r0, int* rows, int* part, int* parts) {
     int e0 = 0;
     if (p.groups > 64) {
       for (;; e0 += 64) {
-        scan(p, e0);
+        read(p, e0);
+        scan();
         const int n = __builtin_amdgcn_readlane(incl, 63);
         if (m < n) break;
         m -= n;
@@ -53,9 +71,15 @@ struct RowTiles {
     }
     const int s = __ffsll((unsigned long long)__ballot(incl > m)) - 1;
     *e = e0 + s;
-    const int first = __builtin_amdgcn_readlane(lo, s) + (m - __builtin_amdgcn_readlane(incl - tiles, s)) * TM;
+    *parts = __builtin_amdgcn_readlane(tiles, s);
+    *part = m - (__builtin_amdgcn_readlane(incl, s) - *parts);
+    const int first = __builtin_amdgcn_readlane(lo, s) + *part * tall;
     *r0 = first;
-    *rows = min(__builtin_amdgcn_readlane(hi, s) - first, TM);
+    *rows = max(min(__builtin_amdgcn_readlane(hi, s) - first, tall), 0);
+  }
+  __device__ __forceinline__ void find(const MmArgs& p, int m, int* e, int* r0, int* rows) {
+    int part, parts;
+    find(p, m, e, r0, rows, &part, &parts);
   }
 };
 

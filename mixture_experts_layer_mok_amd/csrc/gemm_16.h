@@ -33,12 +33,26 @@ namespace g16 {
 
 constexpr int kThr = 256;
 constexpr int kDeep = 64;                    // summed elements a step
-constexpr uint32_t kStage = 35840;           // bytes of one operand's stage
 constexpr uint32_t kPast = 0x80000000u;      // added to an offset: out of every resource's range
 
-static __shared__ __align__(1024) v4u s_a[2 * kStage / 16];
-static __shared__ __align__(1024) v4u s_b[2 * kStage / 16];
-static __shared__ __align__(1024) v4u s_out[4 * 4096 / 16];  // results on their way out, 4 KB a wave
+// Bytes of one operand's stage, NB blocks of 16 rows a wave.
+template <int KIND, int NB>
+constexpr uint32_t stage_bytes() { return KIND == 0 ? 4096 * NB : NB == 8 ? 35840 : 17408; }
+
+// The LDS of a kernel: two stages of each operand, then the results on their way out, 512 JB bytes a
+// wave.
+template <uint32_t STAGE_A, uint32_t STAGE_B, int JB>
+struct Lds {
+  static constexpr uint32_t kA = STAGE_A, kB = STAGE_B;
+  static constexpr uint32_t kBytes = 2 * STAGE_A + 2 * STAGE_B + 4 * 512 * JB;
+  static __device__ __forceinline__ v4u* mem() {
+    static __shared__ __align__(1024) v4u s_mem[kBytes / 16];
+    return s_mem;
+  }
+  static __device__ __forceinline__ uint32_t a() { return lds_addr(mem()); }
+  static __device__ __forceinline__ uint32_t b() { return a() + 2 * STAGE_A; }
+  static __device__ __forceinline__ uint32_t out() { return a() + 2 * STAGE_A + 2 * STAGE_B; }
+};
 
 typedef uint32_t v2u_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) v4u lds_w16;
@@ -151,7 +165,7 @@ template <int KIND, int NB>
 struct FragAt {
   typedef Operand<KIND, NB> Op;
   static constexpr int kAddr = KIND == kAlong ? 2 : Op::kRows;
-  static_assert(Op::place_of(31) + 1024 <= kStage);
+  static_assert(Op::place_of(4 * NB - 1) + 1024 <= stage_bytes<KIND, NB>());
   uint32_t p[kAddr];
 
   // half: which half of the tile's rows the wave has
@@ -205,10 +219,13 @@ __device__ __forceinline__ void wait_all_but(int n) {
 }
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14)); }
 
-template <int TYPE, int AK, int BK, int IB, int JB>
+// IB, JB: blocks of 16 rows of A and of B a wave.  A may be opened for a taller tile (AB blocks), of
+// which this one's rows are the first.
+template <int TYPE, int AK, int BK, int IB, int JB, typename LDS, int AB = IB>
 struct Tile {
-  typedef Operand<AK, IB> A;
+  typedef Operand<AK, AB> A;
   typedef Operand<BK, JB> B;
+  static_assert(AB == IB || AK == kAlong);
   static constexpr int kLoads = IB + JB;  // a wave and step
   static constexpr int kReads = (AK == kAlong ? IB : 2 * IB) + (BK == kAlong ? JB : 2 * JB);
 
@@ -272,7 +289,7 @@ struct Tile {
   }
   template <int H, int M>
   __device__ __forceinline__ void slot(const A& a, const B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
-                                       const FragAt<BK, JB>& rb, uint32_t wr) {
+                                       const FragAt<BK, JB>& rb, uint32_t wa, uint32_t wb) {
     constexpr int i = M / JB, j = M % JB;
     constexpr int q0 = loads_before(H * kM + M), q1 = loads_before(H * kM + M + 1);
     static_assert(!kWith4 || load_slot(kLoads - 1) < 2 * kM - 8);
@@ -280,7 +297,7 @@ struct Tile {
     if constexpr (kWith4 && q1 > q0) {
       mx4::lds_load16_mfma4<TYPE == MOK_TYPE_FP16>(
           q0 < IB ? a.r : b.r, q0 < IB ? a.off[q0 % IB] : b.off[(q0 + JB - IB) % JB],
-          q0 < IB ? A::place(q0, lds_addr(s_a) + wr) : B::place(q0 - IB, lds_addr(s_b) + wr), f.a[i], f.b[j],
+          q0 < IB ? A::place(q0, LDS::a() + wa) : B::place(q0 - IB, LDS::b() + wb), f.a[i], f.b[j],
           f.b[j + 1], f.b[j + 2], f.b[j + 3], acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
     } else if constexpr (!kWith4 || loads_before(H * kM + M + 1) == loads_before((H * kM + M) / 4 * 4)) {
       mfma<TYPE>(f.b[j], f.a[i], acc[i][j]);
@@ -302,15 +319,15 @@ struct Tile {
     if constexpr (!kWith4) {
 #pragma unroll
       for (int q = q0; q < q1; ++q) {
-        if (q < IB) a.load(q, lds_addr(s_a) + wr);
-        else b.load(q - IB, lds_addr(s_b) + wr);
+        if (q < IB) a.load(q, LDS::a() + wa);
+        else b.load(q - IB, LDS::b() + wb);
       }
     }
   }
   template <int H, int... M>
   __device__ __forceinline__ void half(const A& a, const B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
-                                       const FragAt<BK, JB>& rb, uint32_t wr, std::integer_sequence<int, M...>) {
-    (slot<H, M>(a, b, f, fr, ra, rb, wr), ...);
+                                       const FragAt<BK, JB>& rb, uint32_t wa, uint32_t wb, std::integer_sequence<int, M...>) {
+    (slot<H, M>(a, b, f, fr, ra, rb, wa, wb), ...);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -320,9 +337,9 @@ struct Tile {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
-      for (int q = 0; q < IB; ++q) a.load(q, lds_addr(s_a) + ks * kStage);
+      for (int q = 0; q < IB; ++q) a.load(q, LDS::a() + ks * LDS::kA);
 #pragma unroll
-      for (int q = 0; q < JB; ++q) b.load(q, lds_addr(s_b) + ks * kStage);
+      for (int q = 0; q < JB; ++q) b.load(q, LDS::b() + ks * LDS::kB);
       a.next();
       a.cut();
       b.next();
@@ -337,8 +354,8 @@ struct Tile {
     a.uniform();
     b.uniform();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    fa.init(lds_addr(s_a), w >> 1);
-    fb.init(lds_addr(s_b), w & 1);
+    fa.init(LDS::a(), w >> 1);
+    fb.init(LDS::b(), w & 1);
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
@@ -349,15 +366,14 @@ struct Tile {
     Frag f0, f1;
 #pragma unroll
     for (int r = 0; r < kReads; ++r) read(f0, fa, fb, 0, r);
-    uint32_t cur = 0;
+    uint32_t ca = 0, cb = 0;  // this step's stages
     FragAt<AK, IB> na = fa.in(0);
     FragAt<BK, JB> nb = fb.in(0);
     for (int ks = 0; ks < steps; ++ks) {
-      const uint32_t nxt = kStage - cur;
-      half<0>(a, b, f0, f1, na, nb, cur, std::make_integer_sequence<int, kM>());
-      na = fa.in(nxt);
-      nb = fb.in(nxt);
-      half<1>(a, b, f1, f0, na, nb, cur, std::make_integer_sequence<int, kM>());
+      half<0>(a, b, f0, f1, na, nb, ca, cb, std::make_integer_sequence<int, kM>());
+      na = fa.in(LDS::kA - ca);
+      nb = fb.in(LDS::kB - cb);
+      half<1>(a, b, f1, f0, na, nb, ca, cb, std::make_integer_sequence<int, kM>());
       a.next();
       b.next();
       if (!a.whole()) {
@@ -368,7 +384,8 @@ struct Tile {
         asm volatile("");
         b.cut();
       }
-      cur = nxt;
+      ca = LDS::kA - ca;
+      cb = LDS::kB - cb;
     }
     // every load has landed and every wave has read its last fragments: the stages are free; and the
     // last sums are there (seven wait states after an MFMA of four passes)
@@ -382,8 +399,8 @@ struct Tile {
   static constexpr int kStores16 = IB * JB / 2, kStores32 = IB * JB;
 
   // Block (i, j): lane l holds, of row l % 16, the columns 4 (l / 16) .. +4.  16 rows of 256 bytes
-  // at a time go through the wave's 4 KB of LDS and leave as whole 128-byte lines (16 chunks of 16
-  // bytes a row, chunk c of row r at c ^ r); with JB = 4 and 16-bit results the row has 128 bytes.
+  // (JB = 4: 128) at a time go through the wave's own LDS and leave as whole 128-byte lines (16 or 8
+  // chunks of 16 bytes a row, chunk c of row r at c ^ r).
   // The resource's range drops what lies outside `rows` and `cols`, so that every wave makes the
   // same number of stores.
   template <bool OUT32, bool ADD>
@@ -393,11 +410,11 @@ struct Tile {
     const int l = t & 63, w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = w >> 1, wn = w & 1, r = l & 15, g = l >> 4;
     constexpr int kSize = OUT32 ? 4 : 2;
-    constexpr int kChunks = JB == 8 || OUT32 ? 16 : 8;  // 16-byte chunks a row that go out together
+    constexpr int kChunks = JB == 8 ? 16 : 8;  // 16-byte chunks a row that go out together
     constexpr int kJ = kChunks / kSize;                 // column blocks that make them
     constexpr int kRows = 64 / kChunks;                 // rows that an instruction stores
     const rsrc_t ro = row_rsrc(out, kPast);
-    const uint32_t area = lds_addr(s_out) + uint32_t(w) * 4096;
+    const uint32_t area = LDS::out() + uint32_t(w) * (512 * JB);
 #pragma unroll
     for (int i = 0; i < IB; ++i)
 #pragma unroll
@@ -407,7 +424,7 @@ struct Tile {
           f32x4_t c = acc[i][j];
           asm volatile("" : "+a"(c));  // read out here, not for all blocks before the kinds of store part
           if (OUT32)
-            *reinterpret_cast<lds_w16*>(uintptr_t(area + r * 256 + (((4 * (j - j0) + g) ^ r) * 16))) =
+            *reinterpret_cast<lds_w16*>(uintptr_t(area + r * (16 * kChunks) + (((4 * (j - j0) + g) ^ (r & (kChunks - 1))) * 16))) =
                 __builtin_bit_cast(v4u, c);
           else
             *reinterpret_cast<lds_w8*>(uintptr_t(area + r * (16 * kChunks) +

@@ -116,9 +116,9 @@ __global__ __launch_bounds__(256) void k_grouped_mm(MmArgs p) {
 
 mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st) {
   if (!a.scales)
-    return kind == kMmOut    ? (a.max_rows <= 512 ? launch_mm_few(a, st) : launch_mm_tiles_out(a, st))
-           : kind == kMmRows ? launch_mm_tiles_rows(a, st)
-                             : launch_mm_tiles_weights(a, st);
+    return kind == kMmOut    ? launch_mm_out(a, st)
+           : kind == kMmRows ? launch_mm_rows(a, st)
+                             : launch_mm_weights(a, st);
   const int N = kind == kMmOut ? a.n : a.k;
   // every expert may end inside a tile
   const int64_t mt = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kTile - 1)) / kTile);

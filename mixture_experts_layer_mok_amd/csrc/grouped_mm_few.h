@@ -1,19 +1,14 @@
 // Grouped product of few 16-bit rows an expert (decoding): bound by reading the weights once.
-#include <algorithm>
-#include <type_traits>
-
-#include "device.h"
+#pragma once
 #include "expert_rows.h"
-#include "ops_launch.h"
 
 namespace mok {
 namespace g16 {
 
-namespace {
-
-constexpr int kPassRows = 32;   // rows a pass
+constexpr int kPassRows = 32;            // rows a pass
 constexpr int kWaves = 4;
-constexpr int kUnits = 16;      // 16-byte units of a row that a chunk holds: 128 elements
+constexpr uint32_t kFewLds = kWaves * 2 * 4 * 64 * 16;  // bytes of s_part
+constexpr int kUnits = 16;               // 16-byte units of a row that a chunk holds: 128 elements
 constexpr uint32_t kNone = 0x80000000u;  // added to an offset: out of every resource's range
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -111,40 +106,28 @@ __device__ __forceinline__ void pass(const MmArgs& p, f32x4_t* s_part, int e, in
   }
 }
 
-// Item t: passes of all experts times blocks of 16 NB columns, columns first, so that the passes
-// that read the same weights run on the same XCD, at about the same time.
+// Passes of all experts times blocks of 16 NB columns, columns first, so that the passes that read
+// the same weights run on the same XCD, at about the same time.
 template <int TYPE, int NB>
-__device__ __forceinline__ void item(const MmArgs& p, RowTiles<kPassRows>& til, f32x4_t* s_part, int t) {
-  const int blocks = (p.n + 16 * NB - 1) / (16 * NB);
-  const int m = t / blocks, n0 = (t - m * blocks) * 16 * NB;
-  if (m >= til.total) return;
-  int e, r0, rows;
-  til.find(p, m, &e, &r0, &rows);
-  if (rows <= 16) pass<TYPE, NB, 1>(p, s_part, e, r0, rows, n0);
-  else pass<TYPE, NB, 2>(p, s_part, e, r0, rows, n0);
+__device__ __forceinline__ void few_items(const MmArgs& p, RowTiles& til, f32x4_t* s_part) {
+  const int blocks = (p.n + 16 * NB - 1) / (16 * NB), total = til.total * blocks;
+  for (int t = blockIdx.x; t < total; t += int(gridDim.x)) {
+    const int m = t / blocks, n0 = (t - m * blocks) * 16 * NB;
+    int e, r0, rows;
+    til.find(p, m, &e, &r0, &rows);
+    if (rows <= 16) pass<TYPE, NB, 1>(p, s_part, e, r0, rows, n0);
+    else pass<TYPE, NB, 2>(p, s_part, e, r0, rows, n0);
+    __syncthreads();  // s_part is read before the next item writes it
+  }
 }
 
 // Columns a workgroup: the most that leave an item a CU (every item reads its rows again).
 template <int TYPE>
-__global__ __launch_bounds__(kWaves * 64) void k_mm_few(MmArgs p) {
-  __shared__ f32x4_t s_part[kWaves * 2 * 4 * 64];
-  RowTiles<kPassRows> til;
-  til.init(p);
-  if ((p.n + 63) / 64 * til.total >= 256) item<TYPE, 4>(p, til, s_part, blockIdx.x);
-  else if ((p.n + 31) / 32 * til.total >= 256) item<TYPE, 2>(p, til, s_part, blockIdx.x);
-  else item<TYPE, 1>(p, til, s_part, blockIdx.x);
+__device__ __forceinline__ void walk_few(const MmArgs& p, RowTiles& til, f32x4_t* s_part) {
+  if ((p.n + 63) / 64 * til.total >= 256) few_items<TYPE, 4>(p, til, s_part);
+  else if ((p.n + 31) / 32 * til.total >= 256) few_items<TYPE, 2>(p, til, s_part);
+  else few_items<TYPE, 1>(p, til, s_part);
 }
-
-}  // namespace
 
 }  // namespace g16
-
-mok_status_t launch_mm_few(const MmArgs& a, hipStream_t st) {
-  using namespace g16;
-  const int64_t passes = std::min<int64_t>(a.max_rows, (a.max_rows + int64_t(a.groups) * (kPassRows - 1)) / kPassRows);
-  const dim3 grid(unsigned((a.n + 15) / 16 * passes));
-  return a.type == MOK_TYPE_BF16 ? launch(k_mm_few<MOK_TYPE_BF16>, grid, dim3(64 * kWaves), st, a)
-                                 : launch(k_mm_few<MOK_TYPE_FP16>, grid, dim3(64 * kWaves), st, a);
-}
-
 }  // namespace mok

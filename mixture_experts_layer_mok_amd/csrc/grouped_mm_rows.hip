@@ -3,6 +3,6 @@
 
 namespace mok {
 
-mok_status_t launch_mm_tiles_rows(const MmArgs& a, hipStream_t st) { return g16::launch_tiles<kMmRows>(a, st); }
+mok_status_t launch_mm_rows(const MmArgs& a, hipStream_t st) { return g16::launch_tiles<kMmRows>(a, st); }
 
 }  // namespace mok

@@ -3,6 +3,6 @@
 
 namespace mok {
 
-mok_status_t launch_mm_tiles_weights(const MmArgs& a, hipStream_t st) { return g16::launch_tiles<kMmWeights>(a, st); }
+mok_status_t launch_mm_weights(const MmArgs& a, hipStream_t st) { return g16::launch_tiles<kMmWeights>(a, st); }
 
 }  // namespace mok

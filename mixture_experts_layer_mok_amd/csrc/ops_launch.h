@@ -102,10 +102,9 @@ struct MmArgs {
   int64_t ld_out;
 };
 mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st);
-mok_status_t launch_mm_few(const MmArgs& a, hipStream_t st);
-mok_status_t launch_mm_tiles_out(const MmArgs& a, hipStream_t st);
-mok_status_t launch_mm_tiles_rows(const MmArgs& a, hipStream_t st);
-mok_status_t launch_mm_tiles_weights(const MmArgs& a, hipStream_t st);
+mok_status_t launch_mm_out(const MmArgs& a, hipStream_t st);
+mok_status_t launch_mm_rows(const MmArgs& a, hipStream_t st);
+mok_status_t launch_mm_weights(const MmArgs& a, hipStream_t st);
 
 // Activations in 8 bits (mx8.hip).  ld_val: elements from row to row of src or dst.
 struct Mx8Args {
