@@ -21,6 +21,11 @@
 //     lie further apart than their 1 KB.  So a lane needs two (or four) read addresses for all
 //     blocks, the rest being the reads' own offset.
 //
+// An operand across the sum may be held in 8 bits (kHeld): e4m3 codes and a scale for 32 columns of an
+// element.  Its codes come through registers, a step ahead of their conversion (a scaled
+// instruction for two codes) into the same LDS layout, which falls between the MFMAs of the step
+// before their own.
+//
 // Rows past an operand's last are read as its last one and never stored (kAlong); chunks and
 // columns past the end, and summed elements past the last, as zeros (an out-of-range offset reads
 // no memory).
@@ -35,9 +40,11 @@ constexpr int kThr = 256;
 constexpr int kDeep = 64;                    // summed elements a step
 constexpr uint32_t kPast = 0x80000000u;      // added to an offset: out of every resource's range
 
+enum Kind { kAlong = 0, kAcross = 1, kHeld = 2 };
+
 // Bytes of one operand's stage, NB blocks of 16 rows a wave.
 template <int KIND, int NB>
-constexpr uint32_t stage_bytes() { return KIND == 0 ? 4096 * NB : NB == 8 ? 35840 : 17408; }
+constexpr uint32_t stage_bytes() { return KIND == kAlong ? 4096 * NB : NB == 8 ? 35840 : 17408; }
 
 // The LDS of a kernel: two stages of each operand, then the results on their way out, 512 JB bytes a
 // wave.
@@ -89,8 +96,6 @@ __device__ __forceinline__ int scalar(int v) {
   asm volatile("s_nop 0\n\tv_readfirstlane_b32 %0, %1\n\ts_nop 4" : "=s"(s) : "v"(v));
   return s;
 }
-
-enum Kind { kAlong = 0, kAcross = 1 };
 
 // One operand of a tile.  NB: blocks of 16 rows a wave (8 or 4, along also 2); the tile has 32 NB
 // rows, and a wave NB loads a step.
@@ -160,10 +165,96 @@ struct Operand {
   }
 };
 
+// Two e4m3 codes (the low or the high half of c) times 2^(scale byte - 127) in the product's type.
+// The instruction reads the exponent of `scale` alone: 0 stands for 2^-127, 255 for NaN.
+template <int TYPE, bool HIGH>
+__device__ __forceinline__ uint32_t held2(uint32_t c, uint32_t scale) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  const float f = __uint_as_float(scale << 23);
+  if (TYPE == MOK_TYPE_BF16)
+    return __builtin_bit_cast(uint32_t, bf16x2_t(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, f, HIGH)));
+  return __builtin_bit_cast(uint32_t, f16x2_t(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, f, HIGH)));
+}
+
+// An operand across the sum held in 8 bits, of 32 NB columns.  A lane takes 16 codes at a time, a
+// block of 16 columns of one element.
+template <int TYPE, int NB>
+struct Held {
+  typedef Operand<kAcross, NB> Op;
+  static constexpr int kUnits = NB / 2;                // of 16 codes a lane and step
+  static constexpr int kLanes = 2 * NB;                // lanes that one element takes
+  static constexpr int kOps = 6 * kUnits;              // pieces that a step's conversion is cut into
+  rsrc_t rc, rs;
+  uint64_t codes, scales;  // of the step to be loaded
+  int64_t ld, lds;
+  uint32_t off[kUnits], offs[kUnits];
+  int left;
+  v4u q[kUnits];
+  uint32_t s[kUnits];
+  v4u half;  // eight converted elements
+
+  static __device__ __forceinline__ int at(int u) {
+    const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    return (u * 4 + w) * (64 / kLanes) + l / kLanes;
+  }
+  // c, sc: code and scales' first byte of the operand's first element; col: its first column.
+  __device__ __forceinline__ void init(const uint8_t* c, int64_t ld_, const uint8_t* sc, int64_t lds_, int col,
+                                       int cols, int summed) {
+    codes = reinterpret_cast<uint64_t>(c) + uint32_t(col);
+    scales = reinterpret_cast<uint64_t>(sc) + uint32_t(col / 32);
+    ld = ld_;
+    lds = lds_;
+    left = summed;
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int b = int(threadIdx.x & 63) % kLanes;
+      const uint32_t past = 16 * b < cols ? 0u : kPast;
+      off[u] = (uint32_t(at(u)) * uint32_t(ld) + b * 16) | past;
+      offs[u] = (uint32_t(at(u)) * uint32_t(lds) + b / 2) | past;
+    }
+  }
+  __device__ __forceinline__ void next() {
+    left -= kDeep;
+    codes += uint64_t(kDeep * ld);
+    scales += uint64_t(kDeep * lds);
+  }
+  // Load 0 .. 2 kUnits - 1 of a step: a unit's codes, its scale.
+  __device__ __forceinline__ void load(int x) {
+    const int u = x >> 1;
+    const uint32_t past = at(u) < left ? 0u : kPast;
+    if (x == 0) {
+      rc = row_rsrc(reinterpret_cast<const void*>(codes), kPast);
+      rs = row_rsrc(reinterpret_cast<const void*>(scales), kPast);
+    }
+    if (x & 1) s[u] = uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(rs, offs[u] | past, 0, 0)));
+    else q[u] = buf_ld16<kCpolPlain>(rc, off[u] | past);
+  }
+  // Piece o of the conversion into the stage at LDS address `to`.
+  template <int O>
+  __device__ __forceinline__ void convert(uint32_t to) {
+    constexpr int u = O / 6, x = O % 6, w = x < 3 ? x : x - 1;
+    if constexpr (x == 2 || x == 5) {
+      const int l = threadIdx.x & 63, k = at(u), b = l % kLanes, y = k % Op::kRows;
+      // (element k's place: units and waves are whole loads of the 16-bit operand apart)
+      const uint32_t place = to + Op::place_of(4 * (64 / kLanes) / Op::kRows) * u + lane_place() + uint32_t(b ^ y) * 32;
+      *reinterpret_cast<lds_w16*>(uintptr_t(place + (x == 5 ? 16 : 0))) = half;
+    } else {
+      const uint32_t c = w == 0 ? q[u].x : w == 1 ? q[u].y : w == 2 ? q[u].z : q[u].w;
+      half[2 * (w & 1)] = held2<TYPE, false>(c, s[u]);
+      half[2 * (w & 1) + 1] = held2<TYPE, true>(c, s[u]);
+    }
+  }
+  // LDS byte, in its stage, of the element that this lane has of unit 0.
+  static __device__ __forceinline__ uint32_t lane_place() {
+    const int k = at(0), j = k / Op::kRows;
+    return (NB == 8 ? j * 1088 + (j >> 2) * 128 : j * 1024 + (j >> 1) * 128) + (k % Op::kRows) * (64 * NB);
+  }
+};
+
 // LDS byte addresses of this lane's fragment reads.
 template <int KIND, int NB>
 struct FragAt {
-  typedef Operand<KIND, NB> Op;
+  typedef Operand<KIND == kHeld ? kAcross : KIND, NB> Op;
   static constexpr int kAddr = KIND == kAlong ? 2 : Op::kRows;
   static_assert(Op::place_of(4 * NB - 1) + 1024 <= stage_bytes<KIND, NB>());
   uint32_t p[kAddr];
@@ -224,9 +315,10 @@ __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(15 | (7 
 template <int TYPE, int AK, int BK, int IB, int JB, typename LDS, int AB = IB>
 struct Tile {
   typedef Operand<AK, AB> A;
-  typedef Operand<BK, JB> B;
+  static constexpr bool kHolds = BK == kHeld;
+  typedef std::conditional_t<kHolds, Held<TYPE, JB>, Operand<kHolds ? kAcross : BK, JB>> B;
   static_assert(AB == IB || AK == kAlong);
-  static constexpr int kLoads = IB + JB;  // a wave and step
+  static constexpr int kLoads = kHolds ? IB : IB + JB;  // direct to LDS, a wave and step
   static constexpr int kReads = (AK == kAlong ? IB : 2 * IB) + (BK == kAlong ? JB : 2 * JB);
 
   FragAt<AK, IB> fa;
@@ -276,8 +368,16 @@ struct Tile {
   static constexpr int kRead0 = kM * 5 / 16, kFree = kM / 2 - 1, kLanded = kM / 4 - 1, kRead1 = kM / 2;
   // Whole tiles take a load with four MFMAs (lds_load16_mfma4), never the step's last eight.
   static constexpr bool kWith4 = kM == 64;
+  // (with B in 8 bits, before its own loads, which come first in slice 1: those are waited for first)
   static constexpr int load_slot(int q) {
-    return kWith4 ? (kFree + 1) + q * 22 / 16 * 4 : kFree + 1 + q * (2 * kM - kFree - 2) / kLoads;
+    return kHolds ? kFree + 1 + q * (kM - kFree - 1) / kLoads
+           : kWith4 ? kFree + 1 + q * 22 / 16 * 4 : kFree + 1 + q * (2 * kM - kFree - 2) / kLoads;
+  }
+  static constexpr int kHeldLoads = kHolds ? JB : 0;
+  static constexpr int held_before(int slot) { return slot <= kM ? 0 : 2 * (slot - kM) < kHeldLoads ? 2 * (slot - kM) : kHeldLoads; }
+  // (its conversion, from a quarter of slice 0 to the end)
+  static constexpr int convert_before(int m) {
+    return !kHolds || m <= kM / 4 ? 0 : (m - kM / 4) * (3 * JB) / (kM - kM / 4);
   }
   static constexpr int loads_before(int slot) {
     int n = 0;
@@ -288,17 +388,22 @@ struct Tile {
     return x <= 0 ? 0 : x >= span ? kReads : (x * kReads + span - 1) / span;
   }
   template <int H, int M>
-  __device__ __forceinline__ void slot(const A& a, const B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
+  __device__ __forceinline__ void slot(const A& a, B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
                                        const FragAt<BK, JB>& rb, uint32_t wa, uint32_t wb) {
     constexpr int i = M / JB, j = M % JB;
     constexpr int q0 = loads_before(H * kM + M), q1 = loads_before(H * kM + M + 1);
     static_assert(!kWith4 || load_slot(kLoads - 1) < 2 * kM - 8);
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (kWith4 && q1 > q0) {
-      mx4::lds_load16_mfma4<TYPE == MOK_TYPE_FP16>(
-          q0 < IB ? a.r : b.r, q0 < IB ? a.off[q0 % IB] : b.off[(q0 + JB - IB) % JB],
-          q0 < IB ? A::place(q0, LDS::a() + wa) : B::place(q0 - IB, LDS::b() + wb), f.a[i], f.b[j],
-          f.b[j + 1], f.b[j + 2], f.b[j + 3], acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+      i32x4_t r = a.r;
+      uint32_t off = a.off[q0 % IB], to = A::place(q0, LDS::a() + wa);
+      if constexpr (q0 >= IB) {
+        r = b.r;
+        off = b.off[q0 - IB];
+        to = B::place(q0 - IB, LDS::b() + wb);
+      }
+      mx4::lds_load16_mfma4<TYPE == MOK_TYPE_FP16>(r, off, to, f.a[i], f.b[j], f.b[j + 1], f.b[j + 2], f.b[j + 3],
+                                                   acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
     } else if constexpr (!kWith4 || loads_before(H * kM + M + 1) == loads_before((H * kM + M) / 4 * 4)) {
       mfma<TYPE>(f.b[j], f.a[i], acc[i][j]);
     }  // (else it was one of the four of a load)
@@ -308,7 +413,8 @@ struct Tile {
       asm volatile("" ::: "memory");
     }
     if constexpr (H == 1 && M == kLanded) {
-      wait_vmcnt<loads_before(kM + kLanded)>();
+      wait_vmcnt<loads_before(kM + kLanded) + held_before(kM + kLanded)>();
+      if (kHolds) wait_lds();  // what was converted is written
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     }
@@ -318,33 +424,58 @@ struct Tile {
     for (int r = r0; r < r1; ++r) read(fr, ra, rb, H == 0 ? 1 : 0, r);
     if constexpr (!kWith4) {
 #pragma unroll
-      for (int q = q0; q < q1; ++q) {
-        if (q < IB) a.load(q, LDS::a() + wa);
-        else b.load(q - IB, LDS::b() + wb);
+      for (int q = q0; q < q1; ++q) load(a, b, q, wa, wb);
+    }
+    if constexpr (kHolds) {
+      if constexpr (H == 0) {  // the next step's elements, into its stage
+        convert<convert_before(M)>(b, LDS::b() + (LDS::kB - wb),
+                                   std::make_integer_sequence<int, convert_before(M + 1) - convert_before(M)>());
+      } else {  // the codes of the step after
+#pragma unroll
+        for (int x = held_before(kM + M); x < held_before(kM + M + 1); ++x) b.load(x);
       }
     }
   }
+  static __device__ __forceinline__ void load(const A& a, const B& b, int q, uint32_t wa, uint32_t wb) {
+    if constexpr (kHolds) {
+      a.load(q, LDS::a() + wa);
+    } else {
+      if (q < IB) a.load(q, LDS::a() + wa);
+      else b.load(q - IB, LDS::b() + wb);
+    }
+  }
+  template <int O, int... X>
+  static __device__ __forceinline__ void convert(B& b, uint32_t to, std::integer_sequence<int, X...>) {
+    (b.template convert<O + X>(to), ...);
+  }
   template <int H, int... M>
-  __device__ __forceinline__ void half(const A& a, const B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
+  __device__ __forceinline__ void half(const A& a, B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
                                        const FragAt<BK, JB>& rb, uint32_t wa, uint32_t wb, std::integer_sequence<int, M...>) {
     (slot<H, M>(a, b, f, fr, ra, rb, wa, wb), ...);
     __builtin_amdgcn_sched_barrier(0);
   }
 
-  // The loads of two steps.
+  // The loads of two steps (of one, of what is held in 8 bits).
   static __device__ __forceinline__ void begin(A& a, B& b) {
     asm volatile("" ::: "memory");
+    if constexpr (kHolds) {
+#pragma unroll
+      for (int x = 0; x < kHeldLoads; ++x) b.load(x);
+    }
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
 #pragma unroll
       for (int q = 0; q < IB; ++q) a.load(q, LDS::a() + ks * LDS::kA);
-#pragma unroll
-      for (int q = 0; q < JB; ++q) b.load(q, LDS::b() + ks * LDS::kB);
       a.next();
       a.cut();
-      b.next();
-      b.cut();
+      if constexpr (!kHolds) {
+#pragma unroll
+        for (int q = 0; q < JB; ++q) b.load(q, LDS::b() + ks * LDS::kB);
+        b.next();
+        b.cut();
+      }
     }
+    if constexpr (kHolds) b.next();
     asm volatile("" ::: "memory");
   }
 
@@ -352,7 +483,7 @@ struct Tile {
   // memory operations.
   __device__ __forceinline__ void run(A a, B b, int steps, int stores) {
     a.uniform();
-    b.uniform();
+    if constexpr (!kHolds) b.uniform();
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     fa.init(LDS::a(), w >> 1);
     fb.init(LDS::b(), w & 1);
@@ -361,6 +492,13 @@ struct Tile {
 #pragma unroll
       for (int j = 0; j < JB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     wait_all_but(stores);  // steps 0 and 1
+    if constexpr (kHolds) {
+      convert<0>(b, LDS::b(), std::make_integer_sequence<int, 3 * JB>());
+#pragma unroll
+      for (int x = 0; x < kHeldLoads; ++x) b.load(x);
+      b.next();
+      wait_lds();
+    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     Frag f0, f1;
@@ -380,9 +518,11 @@ struct Tile {
         asm volatile("");  // a branch: as selects the cut would stand in every step
         a.cut();
       }
-      if (!b.whole()) {
-        asm volatile("");
-        b.cut();
+      if constexpr (!kHolds) {
+        if (!b.whole()) {
+          asm volatile("");
+          b.cut();
+        }
       }
       ca = LDS::kA - ca;
       cb = LDS::kB - cb;

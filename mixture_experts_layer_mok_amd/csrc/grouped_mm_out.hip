@@ -3,6 +3,6 @@
 
 namespace mok {
 
-mok_status_t launch_mm_out(const MmArgs& a, hipStream_t st) { return g16::launch_tiles<kMmOut>(a, st); }
+mok_status_t launch_mm_out(const MmArgs& a, hipStream_t st) { return g16::launch_tiles<kMmOut, g16::kAlong>(a, st); }
 
 }  // namespace mok

@@ -91,7 +91,7 @@ __device__ __forceinline__ void walk_rows(const MmArgs& p, RowTiles& til) {
 
 // d_b: the experts in the order of their rows, the most first, so that the tiles of a round take
 // about as long as each other.
-template <int TYPE, int IB, int JB>
+template <int TYPE, int BK, int IB, int JB>
 __device__ __forceinline__ void walk_weights(const MmArgs& p) {
   const int mt = (p.n + 32 * IB - 1) / (32 * IB), nt = (p.k + 32 * JB - 1) / (32 * JB);
   const int per = mt * nt, total = per * p.groups, lane = threadIdx.x & 63;
@@ -106,11 +106,11 @@ __device__ __forceinline__ void walk_weights(const MmArgs& p) {
     }
   }
   typedef Lds<stage_bytes<kAcross, IB>(), stage_bytes<kAcross, JB>(), JB> LDS;
-  typedef Tile<TYPE, kAcross, kAcross, IB, JB, LDS> T;
+  typedef Tile<TYPE, kAcross, BK, IB, JB, LDS> T;
   int i = 0, t = tile_at(0, total);
   if (t < 0) return;
-  Operand<kAcross, IB> a;
-  Operand<kAcross, JB> b;
+  typename T::A a;
+  typename T::B b;
   int m, n, e, rows;
   auto open = [&]() __attribute__((always_inline)) {
     e = t / per;
@@ -122,8 +122,12 @@ __device__ __forceinline__ void walk_weights(const MmArgs& p) {
     lo = __builtin_amdgcn_readfirstlane(lo);
     a.init(static_cast<const uint16_t*>(p.left) + int64_t(lo) * p.ld_left + m * 32 * IB, p.ld_left, p.n - m * 32 * IB,
            rows);
-    b.init(static_cast<const uint16_t*>(p.right) + int64_t(lo) * p.ld_right + n * 32 * JB, p.ld_right,
-           p.k - n * 32 * JB, rows);
+    const int left = p.k - n * 32 * JB;
+    if constexpr (BK == kHeld)
+      b.init(static_cast<const uint8_t*>(p.right) + int64_t(lo) * p.ld_right, p.ld_right,
+             p.scales + int64_t(lo) * p.ld_scales, p.ld_scales, n * 32 * JB, left, rows);
+    else
+      b.init(static_cast<const uint16_t*>(p.right) + int64_t(lo) * p.ld_right + n * 32 * JB, p.ld_right, left, rows);
     T::begin(a, b);
   };
   open();
@@ -186,10 +190,10 @@ __device__ __forceinline__ Form form_of(const MmArgs& p, RowTiles& t) {
 }
 
 // Whole tiles, a workgroup a CU; `both`: k_mm_small is launched too and the routed rows decide.
-template <int KIND, int TYPE>
+template <int KIND, int TYPE, int BK>
 __global__ __launch_bounds__(kThr) void k_mm_tiles(MmArgs p, bool both) {
   if constexpr (KIND == kMmWeights) {
-    walk_weights<TYPE, 8, 8>(p);
+    walk_weights<TYPE, BK, 8, 8>(p);
   } else {
     RowTiles til;
     if (both && form_of<KIND>(p, til) != kWhole) return;
@@ -198,10 +202,10 @@ __global__ __launch_bounds__(kThr) void k_mm_tiles(MmArgs p, bool both) {
   }
 }
 // Tiles of half the rows and columns, two workgroups a CU, and the kernel of few rows.
-template <int KIND, int TYPE>
+template <int KIND, int TYPE, int BK>
 __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
   if constexpr (KIND == kMmWeights) {
-    walk_weights<TYPE, 4, 4>(p);
+    walk_weights<TYPE, BK, 4, 4>(p);
   } else {
     RowTiles til;
     const bool look = both || KIND == kMmOut;
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
 // about as many rows as are routed), small ones (and few rows) alone where these make a round at most,
 // otherwise both, one of which returns at once (2 us).  A product of weights has its tiles whatever
 // the rows.
-template <int KIND>
+template <int KIND, int BK>
 mok_status_t launch_tiles(const MmArgs& a, hipStream_t st) {
   const int64_t cols = KIND == kMmOut ? a.n : a.k;
   auto tiles = [&](int64_t tall) {
@@ -244,9 +248,9 @@ mok_status_t launch_tiles(const MmArgs& a, hipStream_t st) {
   mok_status_t s = MOK_OK;
   auto go = [&](auto kern, int grid) { return launch(kern, dim3(grid), dim3(kThr), st, a, both); };
   if (!whole)
-    s = a.type == MOK_TYPE_BF16 ? go(k_mm_small<KIND, MOK_TYPE_BF16>, 512) : go(k_mm_small<KIND, MOK_TYPE_FP16>, 512);
+    s = a.type == MOK_TYPE_BF16 ? go(k_mm_small<KIND, MOK_TYPE_BF16, BK>, 512) : go(k_mm_small<KIND, MOK_TYPE_FP16, BK>, 512);
   if (!small && s == MOK_OK)
-    s = a.type == MOK_TYPE_BF16 ? go(k_mm_tiles<KIND, MOK_TYPE_BF16>, 256) : go(k_mm_tiles<KIND, MOK_TYPE_FP16>, 256);
+    s = a.type == MOK_TYPE_BF16 ? go(k_mm_tiles<KIND, MOK_TYPE_BF16, BK>, 256) : go(k_mm_tiles<KIND, MOK_TYPE_FP16, BK>, 256);
   return s;
 }
 

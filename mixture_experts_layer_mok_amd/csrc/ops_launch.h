@@ -105,6 +105,7 @@ mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_out(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_rows(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_weights(const MmArgs& a, hipStream_t st);
+mok_status_t launch_mm_weights_held(const MmArgs& a, hipStream_t st);
 
 // Activations in 8 bits (mx8.hip).  ld_val: elements from row to row of src or dst.
 struct Mx8Args {
