@@ -233,6 +233,12 @@ struct Held {
   template <int O>
   __device__ __forceinline__ void convert(uint32_t to) {
     constexpr int u = O / 6, x = O % 6, w = x < 3 ? x : x - 1;
+    if constexpr (O == 0) {
+      // All of them are waited for here: a later wait would be for the loads to LDS too, which the
+      // compiler does not count and which have been issued since.
+#pragma unroll
+      for (int v = 0; v < kUnits; ++v) asm volatile("" : "+v"(q[v]), "+v"(s[v]));
+    }
     if constexpr (x == 2 || x == 5) {
       const int l = threadIdx.x & 63, k = at(u), b = l % kLanes, y = k % Op::kRows;
       // (element k's place: units and waves are whole loads of the 16-bit operand apart)
