@@ -36,6 +36,7 @@ MOK_TYPE_FP32 = 2
 MOK_MX_E4M3 = 0
 MOK_MX_E2M1 = 1
 MOK_MX_MAX_LD = 1 << 22
+MOK_MM_WORKSPACE_BYTES = 32 << 20
 MOK_DEV_BAD_ID = 0x1
 MOK_DEV_TIMEOUT = 0x2
 
@@ -46,7 +47,7 @@ EXPORTS = (
     "mok_device_cus", "mok_trace_layout", "mok_moe_fwd_noalloc", "mok_quantize_mx_t",
     "mok_moe_bwd_mx", "mok_schedule_layout", "mok_permute", "mok_permute_bwd", "mok_unpermute",
     "mok_unpermute_bwd", "mok_quantize_mx4", "mok_dequantize_mx4", "mok_grouped_mx4",
-    "mok_grouped_mm", "mok_grouped_mm_bwd_rows", "mok_grouped_mm_bwd_weights", "mok_quantize_mx8",
+    "mok_grouped_mm_workspace", "mok_grouped_mm", "mok_grouped_mm_bwd_rows", "mok_grouped_mm_bwd_weights", "mok_quantize_mx8",
     "mok_dequantize_mx8", "mok_swiglu_mx8", "mok_swiglu_mx8_bwd",
 )
 
@@ -121,12 +122,14 @@ def load() -> ctypes.CDLL:
         "mok_dequantize_mx4": (ctypes.c_int, [u8p, i64, u8p, i64, i64, i32, i32, vp, i64, vp]),
         "mok_grouped_mx4": (ctypes.c_int, [i32, u8p, i64, u8p, i64, i64, i32p, i32, u8p, u8p, i32,
                                            i32, i32, vp, i64, vp]),
+        "mok_grouped_mm_workspace": (ctypes.c_int, [i32, i64, i32, i32, i32,
+                                                    ctypes.POINTER(ctypes.c_size_t)]),
         "mok_grouped_mm": (ctypes.c_int, [i32, vp, i64, i64, i32p, i32, vp, i32, i32, i32, vp, i64,
-                                          vp]),
+                                          vp, sz, vp]),
         "mok_grouped_mm_bwd_rows": (ctypes.c_int, [i32, vp, i64, i64, i32p, i32, vp, i32, i32, i32,
-                                                   vp, i64, vp]),
+                                                   vp, i64, vp, sz, vp]),
         "mok_grouped_mm_bwd_weights": (ctypes.c_int, [i32, vp, i64, vp, i64, u8p, i64, i64, i32p,
-                                                      i32, i32, i32, i32, vp, i32, vp]),
+                                                      i32, i32, i32, i32, vp, i32, vp, sz, vp]),
         "mok_quantize_mx8": (ctypes.c_int, [i32, vp, i64, i64, i32, u8p, i64, u8p, i64, vp]),
         "mok_dequantize_mx8": (ctypes.c_int, [u8p, i64, u8p, i64, i64, i32, i32, vp, i64, vp]),
         "mok_swiglu_mx8": (ctypes.c_int, [i32, vp, i64, i64, i32, i32p, i32, vp, i64, u8p, i64, u8p,
@@ -316,26 +319,35 @@ def mok_grouped_mx4(a_format, a_codes, ld_a, a_scales, ld_a_scales, max_rows, of
         _stream(stream)))
 
 
+def mok_grouped_mm_workspace(which, max_rows, groups, n, k) -> int:
+    """Bytes of the workspace that a grouped product may use (0: none)."""
+    out = ctypes.c_size_t(0)
+    _check("mok_grouped_mm_workspace", load().mok_grouped_mm_workspace(which, max_rows, groups, n, k,
+                                                                       ctypes.byref(out)))
+    return out.value
+
+
 def mok_grouped_mm(type, a, ld_a, max_rows, offsets, groups, b, n, k, out_type, out, ld_out,
-                   stream=None) -> None:
+                   ws=None, ws_bytes=0, stream=None) -> None:
     _check("mok_grouped_mm", load().mok_grouped_mm(
         type, _ptr(a), ld_a, max_rows, _ptr(offsets), groups, _ptr(b), n, k, out_type, _ptr(out),
-        ld_out, _stream(stream)))
+        ld_out, _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def mok_grouped_mm_bwd_rows(type, d_out, ld_d_out, max_rows, offsets, groups, b, n, k, out_type,
-                            d_a, ld_d_a, stream=None) -> None:
+                            d_a, ld_d_a, ws=None, ws_bytes=0, stream=None) -> None:
     _check("mok_grouped_mm_bwd_rows", load().mok_grouped_mm_bwd_rows(
         type, _ptr(d_out), ld_d_out, max_rows, _ptr(offsets), groups, _ptr(b), n, k, out_type,
-        _ptr(d_a), ld_d_a, _stream(stream)))
+        _ptr(d_a), ld_d_a, _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def mok_grouped_mm_bwd_weights(type, d_out, ld_d_out, a, ld_a, a_scales, ld_a_scales, max_rows,
-                               offsets, groups, n, k, out_type, d_b, accumulate=0,
-                               stream=None) -> None:
+                               offsets, groups, n, k, out_type, d_b, accumulate=0, ws=None,
+                               ws_bytes=0, stream=None) -> None:
     _check("mok_grouped_mm_bwd_weights", load().mok_grouped_mm_bwd_weights(
         type, _ptr(d_out), ld_d_out, _ptr(a), ld_a, _ptr(a_scales), ld_a_scales, max_rows,
-        _ptr(offsets), groups, n, k, out_type, _ptr(d_b), int(accumulate), _stream(stream)))
+        _ptr(offsets), groups, n, k, out_type, _ptr(d_b), int(accumulate), _ptr(ws), ws_bytes,
+        _stream(stream)))
 
 
 def mok_quantize_mx8(type, src, ld_src, rows, cols, codes, ld_codes, scales, ld_scales,

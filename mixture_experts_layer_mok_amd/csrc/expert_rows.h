@@ -24,6 +24,17 @@ __device__ __forceinline__ int scan64(int x) {
 }
 __device__ __forceinline__ int sum64(int x) { return __builtin_amdgcn_readlane(scan64(x), 63); }
 
+// The largest of the lanes' x, which are not negative.
+__device__ __forceinline__ int max64(int x) {
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(x, 63);
+}
+
 // The m-tiles of all experts (each expert's rows cut from its first row on into tiles of `tall`),
 // numbered in expert order; an expert without rows has `least` of them (0 or 1).  Every wave scans
 // the experts, 64 at a time, all lanes active; with at most 64 of them they are read once.
@@ -33,6 +44,7 @@ struct RowTiles {
   bool mine;    // there is such an expert
   int tiles, incl;  // its m-tiles, and those up to it
   int total;    // m-tiles of all experts
+  int most;     // of one expert
 
   __device__ __forceinline__ void read(const MmArgs& p, int e0) {
     const int lane = threadIdx.x & 63;
@@ -49,11 +61,12 @@ struct RowTiles {
   __device__ __forceinline__ void init(const MmArgs& p, int tall_, int least_ = 0, bool have = false) {
     tall = tall_;
     least = least_;
-    total = 0;
+    total = most = 0;
     for (int e0 = 0; e0 < p.groups; e0 += 64) {
       if (!have) read(p, e0);
       scan();
       total += __builtin_amdgcn_readlane(incl, 63);
+      most = max(most, max64(tiles));
     }
   }
   // m-tile m < total: its expert, first row and rows, its number among the expert's m-tiles and

@@ -36,6 +36,7 @@ struct MoreEntries {
   decltype(&mok_dequantize_mx8) dequantize_mx8;
   decltype(&mok_swiglu_mx8) swiglu_mx8;
   decltype(&mok_swiglu_mx8_bwd) swiglu_mx8_bwd;
+  decltype(&mok_grouped_mm_workspace) grouped_mm_workspace;
 } g_more;  // null until bind_more
 PyObject* g_device = nullptr;  // torch: the current device's index
 PyObject* g_stream = nullptr;  // torch: the current raw stream of a device index
@@ -350,6 +351,17 @@ bool flag(Call& c, PyObject* o) {
 }
 bool half_type(at::ScalarType t) { return t == at::kBFloat16 || t == at::kHalf; }
 
+// A product's workspace, undefined where it needs none.
+struct Workspace {
+  at::Tensor t;
+  size_t bytes = 0;
+  Workspace(int32_t which, int64_t rows, int64_t E, int64_t N, int64_t K, const at::Tensor& like) {
+    if (g_more.grouped_mm_workspace(which, rows, int32_t(E), int32_t(N), int32_t(K), &bytes) != MOK_OK) bytes = 0;
+    if (bytes) t = at::empty({int64_t(bytes)}, like.options().dtype(at::kByte).requires_grad(false));
+  }
+  void* p() const { return bytes ? t.data_ptr() : nullptr; }
+};
+
 // rows (a or d_out), offsets, b, dtype (of an output made here; None: b's), out
 template <bool FORWARD>
 PyObject* do_product(PyObject* const* v) {
@@ -372,8 +384,9 @@ PyObject* do_product(PyObject* const* v) {
   if (!matrix(c, out.t, &mo, true) || (out.t->scalar_type() != held && out.t->scalar_type() != at::kFloat) ||
       mo.rows != mr.rows || mo.cols != cols || !apart(mo.s, {mr.s, so, sb}))
     return none();
+  const Workspace ws(FORWARD ? 0 : 1, mr.rows, E, N, K, *r);
   const auto s = fn(type_of(*r), mr.p, mr.ld, mr.rows, at_ptr<int32_t>(so), int32_t(E), at_ptr<void>(sb), int32_t(N),
-                    int32_t(K), type_of(*out.t), mo.p, mo.ld, st);
+                    int32_t(K), type_of(*out.t), mo.p, mo.ld, ws.p(), ws.bytes, st);
   return s == MOK_OK ? out.result() : refused(FORWARD ? "mok_grouped_mm" : "mok_grouped_mm_bwd_rows", s);
 }
 
@@ -402,9 +415,11 @@ PyObject* do_product_weights(PyObject* const* v) {
   if ((made != at::kFloat && (add || made != held)) || !flat(c, out.t, {E, N, K}, made, &sb) ||
       !apart(sb, {md.s, ma.s, so, ms.s}))
     return none();
+  if (N > INT32_MAX || K > INT32_MAX) return none();
+  const Workspace ws(2, md.rows, E, N, K, *d);
   const auto s = g_more.grouped_mm_bwd_weights(
       type_of(*d), md.p, md.ld, ma.p, ma.ld, static_cast<uint8_t*>(ms.p), ms.ld, md.rows, at_ptr<int32_t>(so),
-      int32_t(E), int32_t(N), int32_t(K), type_of(*out.t), at_ptr<void>(sb), add, st);
+      int32_t(E), int32_t(N), int32_t(K), type_of(*out.t), at_ptr<void>(sb), add, ws.p(), ws.bytes, st);
   return s == MOK_OK ? out.result() : refused("mok_grouped_mm_bwd_weights", s);
 }
 
@@ -535,12 +550,12 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // bind_more(addresses of the entry points in the order of MoreEntries)
 PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind_more: seven addresses are wanted");
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "bind_more: eight addresses are wanted");
     return nullptr;
   }
-  void* p[7];
-  for (int i = 0; i < 7; ++i)
+  void* p[8];
+  for (int i = 0; i < 8; ++i)
     if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_more: a null address");
       return nullptr;
@@ -551,7 +566,8 @@ PyObject* bind_more(PyObject*, PyObject* const* a, Py_ssize_t n) {
             reinterpret_cast<decltype(g_more.quantize_mx8)>(p[3]),
             reinterpret_cast<decltype(g_more.dequantize_mx8)>(p[4]),
             reinterpret_cast<decltype(g_more.swiglu_mx8)>(p[5]),
-            reinterpret_cast<decltype(g_more.swiglu_mx8_bwd)>(p[6])};
+            reinterpret_cast<decltype(g_more.swiglu_mx8_bwd)>(p[6]),
+            reinterpret_cast<decltype(g_more.grouped_mm_workspace)>(p[7])};
   return none();
 }
 

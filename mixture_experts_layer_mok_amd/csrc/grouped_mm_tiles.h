@@ -33,114 +33,61 @@ __device__ __forceinline__ int tile_at(int i, int total) {
   return j < per && x * per + j < n ? first + x * per + j : -1;
 }
 
-// Results of a tile, to `out` at its first.
+// Where a tile's results go.
+struct Result {
+  void* out;  // its first
+  int64_t ld;
+  bool out32, add;
+};
+__device__ __forceinline__ Result result(const MmArgs& p, int64_t first) {
+  return {static_cast<uint8_t*>(p.out) + first * (p.out32 ? 4 : 2), p.ld_out, p.out32, p.add};
+}
+__device__ __forceinline__ Result partial(const MmArgs& p, int item) {
+  return {p.ws + int64_t(item) * (128 * 128), 128, true, false};
+}
 template <typename T>
-__device__ __forceinline__ int store_tile(const T& tile, const MmArgs& p, int64_t first, int rows, int cols) {
-  if (!p.out32) {
-    tile.template store<false, false>(static_cast<uint16_t*>(p.out) + first, p.ld_out, rows, cols);
+__device__ __forceinline__ int store_tile(const T& tile, const Result& r, int rows, int cols) {
+  if (!r.out32) {
+    tile.template store<false, false>(r.out, r.ld, rows, cols);
     return T::kStores16;
   }
-  if (p.add) tile.template store<true, true>(static_cast<float*>(p.out) + first, p.ld_out, rows, cols);
-  else tile.template store<true, false>(static_cast<float*>(p.out) + first, p.ld_out, rows, cols);
+  if (r.add) tile.template store<true, true>(r.out, r.ld, rows, cols);
+  else tile.template store<true, false>(r.out, r.ld, rows, cols);
   return T::kStores32;
 }
 
 template <int KIND, int IB, int JB>
 using RowsLds = Lds<stage_bytes<kAlong, IB>(), stage_bytes<KIND == kMmOut ? kAlong : kAcross, JB>(), JB>;
 
-// out and d_a: rows of an expert times its weights.  Tiles of few rows (the end of an expert's, or
-// all of them) run with fewer row blocks.
-template <int KIND, int TYPE, int IB, int JB>
-__device__ __forceinline__ void walk_rows(const MmArgs& p, RowTiles& til) {
-  constexpr int BK = KIND == kMmOut ? kAlong : kAcross;
-  typedef RowsLds<KIND, IB, JB> LDS;
-  const int cols = KIND == kMmOut ? p.n : p.k, deep = KIND == kMmOut ? p.k : p.n;
-  const int nt = (cols + 32 * JB - 1) / (32 * JB), total = til.total * nt;
-  const int steps = (deep + kDeep - 1) / kDeep;
-  int i = 0, t = tile_at(0, total);
-  if (t < 0) return;
-  Operand<kAlong, IB> a;
-  Operand<BK, JB> b;
-  int m, n, e, r0, rows;
-  auto with = [&](auto f) __attribute__((always_inline)) {  // f with the tile of as many rows as there are
-    if (IB > 2 && rows > 64 * (IB / 4)) f(Tile<TYPE, kAlong, BK, IB, JB, LDS, IB>());
-    else if (IB == 8 && rows > 64) f(Tile<TYPE, kAlong, BK, 4, JB, LDS, IB>());
-    else f(Tile<TYPE, kAlong, BK, 2, JB, LDS, IB>());
-  };
-  auto open = [&]() __attribute__((always_inline)) {
-    tile_of(t, til.total, nt, &m, &n);
-    til.find(p, m, &e, &r0, &rows);
-    const uint16_t* w = static_cast<const uint16_t*>(p.right) + int64_t(e) * p.n * p.k;
-    a.init(static_cast<const uint16_t*>(p.left) + int64_t(r0) * p.ld_left, p.ld_left, rows, deep);
-    b.init(KIND == kMmOut ? w + int64_t(n) * 32 * JB * p.k : w + n * 32 * JB, p.k, cols - n * 32 * JB, deep);
-    with([&](auto tile) __attribute__((always_inline)) { tile.begin(a, b); });
-  };
-  open();
-  int stores = 0;
-  while (t >= 0) {
-    with([&](auto tile) __attribute__((always_inline)) {
-      tile.run(a, b, steps, stores);
-      const int64_t first = int64_t(r0) * p.ld_out + n * 32 * JB;
-      const int have = rows, left = cols - n * 32 * JB;
-      t = tile_at(++i, total);
-      if (t >= 0) open();
-      stores = store_tile(tile, p, first, have, left);
-    });
-  }
+// Sums split over workgroups: every tile is summed in `splits` items of `per` steps each, the partial
+// results go to the workspace, 64 KB an item, and k_mm_join adds them up in order.  As many items as
+// take the least by estimate, in microseconds: 0.72 a step where a CU has one item at most, 0.95 with
+// two, and, where sums are split, 5 for the second launch and 0.033 an item to write it and read it
+// again.  Measured on MI355X, without and with splitting: 2000 rows of one expert, n 8192, k 64, rows'
+// gradient 81 -> 22 us; 256 rows, n 4096, k 7168, forward 85 -> 36; weights' gradient of 16,384 rows,
+// n 1024, k 1024 170 -> 55, n 64, k 64 129 -> 25; and, always split, where that does not pay: 4096
+// rows, n 1024, k 1024, forward 14 -> 29.
+struct Split {
+  int splits, per;
+};
+constexpr int kItems = int(MOK_MM_WORKSPACE_BYTES / (128 * 128 * 4));  // 512: two workgroups a CU
+constexpr int kLeastSteps = 8;  // of an item
+__device__ __forceinline__ float split_us(int steps, int items, bool split) {
+  return float(steps) * (items <= 256 ? 0.72f : 0.95f) + (split ? 5.f + 0.033f * float(items) : 0.f);
 }
-
-// d_b: the experts in the order of their rows, the most first, so that the tiles of a round take
-// about as long as each other.
-template <int TYPE, int BK, int IB, int JB>
-__device__ __forceinline__ void walk_weights(const MmArgs& p) {
-  const int mt = (p.n + 32 * IB - 1) / (32 * IB), nt = (p.k + 32 * JB - 1) / (32 * JB);
-  const int per = mt * nt, total = per * p.groups, lane = threadIdx.x & 63;
-  int rank = 0;
-  if (p.groups <= 64) {
-    int lo = 0, hi = 0;
-    if (lane < p.groups) expert_rows(p, lane, &lo, &hi);
-    const int have = lane < p.groups ? max(hi - lo, 0) : -1;
-    for (int o = 0; o < p.groups; ++o) {
-      const int other = __builtin_amdgcn_readlane(have, o);
-      rank += other > have || (other == have && o < lane) ? 1 : 0;
+__device__ __forceinline__ Split split_of(const MmArgs& p, int tiles, int steps) {
+  Split best = {1, steps};
+  if (!p.ws || tiles <= 0) return best;
+  float us = split_us(steps, tiles, false);
+  for (int s = 2; s * tiles <= kItems && s * kLeastSteps <= steps; s *= 2) {
+    const int per = (steps + s - 1) / s;
+    const float t = split_us(per, s * tiles, true);
+    if (t < us) {
+      us = t;
+      best = {(steps + per - 1) / per, per};
     }
   }
-  typedef Lds<stage_bytes<kAcross, IB>(), stage_bytes<kAcross, JB>(), JB> LDS;
-  typedef Tile<TYPE, kAcross, BK, IB, JB, LDS> T;
-  int i = 0, t = tile_at(0, total);
-  if (t < 0) return;
-  typename T::A a;
-  typename T::B b;
-  int m, n, e, rows;
-  auto open = [&]() __attribute__((always_inline)) {
-    e = t / per;
-    tile_of(t - e * per, mt, nt, &m, &n);
-    if (p.groups <= 64) e = __ffsll((unsigned long long)__ballot(rank == e && lane < p.groups)) - 1;
-    int lo, hi;
-    expert_rows(p, e, &lo, &hi);
-    rows = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
-    lo = __builtin_amdgcn_readfirstlane(lo);
-    a.init(static_cast<const uint16_t*>(p.left) + int64_t(lo) * p.ld_left + m * 32 * IB, p.ld_left, p.n - m * 32 * IB,
-           rows);
-    const int left = p.k - n * 32 * JB;
-    if constexpr (BK == kHeld)
-      b.init(static_cast<const uint8_t*>(p.right) + int64_t(lo) * p.ld_right, p.ld_right,
-             p.scales + int64_t(lo) * p.ld_scales, p.ld_scales, n * 32 * JB, left, rows);
-    else
-      b.init(static_cast<const uint16_t*>(p.right) + int64_t(lo) * p.ld_right + n * 32 * JB, p.ld_right, left, rows);
-    T::begin(a, b);
-  };
-  open();
-  int stores = 0;
-  while (t >= 0) {
-    T tile;
-    tile.run(a, b, (rows + kDeep - 1) / kDeep, stores);
-    const int64_t first = (int64_t(e) * p.n + m * 32 * IB) * p.k + n * 32 * JB;
-    const int have = p.n - m * 32 * IB, left = p.k - n * 32 * JB;
-    t = tile_at(++i, total);
-    if (t >= 0) open();
-    stores = store_tile(tile, p, first, have, left);
-  }
+  return best;
 }
 
 // Which kernel has a product of rows, from estimates in microseconds: rounds of tiles times steps at
@@ -176,17 +123,245 @@ __device__ __forceinline__ Form form_of(const MmArgs& p, RowTiles& t) {
   const float steps = float((deep + kDeep - 1) / kDeep), weights = float(p.n) * float(p.k) * (2.f / 5.2e6f);
   const int whole = n256 * ((cols + 255) / 256), small = n128 * ((cols + 127) / 128);
   const float least = 1.05f * weights * float(live);
-  const float us_small = 4.f + fmaxf(least, steps * (small <= 256 ? 0.72f : float((small + 511) / 512) *
-                                                                               (KIND == kMmOut ? 0.95f : 1.1f)));
+  const Split sp = split_of(p, small, int(steps));
+  const int items = small * sp.splits;
+  const float us_small =
+      4.f + (sp.splits > 1 ? 5.f : 0.f) +
+      fmaxf(least, float(sp.per) * (items <= 256 ? 0.72f : float((items + 511) / 512) *
+                                                               (KIND == kMmOut ? 0.95f : 1.1f)));
   const float us_whole = 4.f + fmaxf(least, float((whole + 255) / 256) * (1.4f * steps + 6.f));
   if (KIND == kMmOut) {
-    const float items = float(n32) * float((p.n + 63) / 64);
+    const float passes = float(n32) * float((p.n + 63) / 64);
     // (a wave's pair of chunks takes 1.5 at least, and four waves share the sum)
     const float us_few = 3.f + fmaxf((0.7f * float(n32) + 0.3f * float(n16)) * weights,
-                                     ceilf(items / 512.f) * ceilf(float(p.k) / 1024.f) * 1.5f);
+                                     ceilf(passes / 512.f) * ceilf(float(p.k) / 1024.f) * 1.5f);
     if (us_few < fminf(us_small, us_whole)) return kFew;
   }
   return us_small < us_whole ? kSmall : kWhole;
+}
+
+// out and d_a: rows of an expert times its weights.  Tiles of few rows (the end of an expert's, or
+// all of them) run with fewer row blocks.
+template <int KIND, int TYPE, int IB, int JB>
+__device__ __forceinline__ void walk_rows(const MmArgs& p, RowTiles& til) {
+  constexpr int BK = KIND == kMmOut ? kAlong : kAcross;
+  constexpr bool kSplit = IB == 4;
+  typedef RowsLds<KIND, IB, JB> LDS;
+  const int cols = KIND == kMmOut ? p.n : p.k, deep = KIND == kMmOut ? p.k : p.n;
+  const int nt = (cols + 32 * JB - 1) / (32 * JB), tiles = til.total * nt;
+  const int steps = (deep + kDeep - 1) / kDeep;
+  const Split sp = kSplit ? split_of(p, tiles, steps) : Split{1, steps};
+  const int total = tiles * sp.splits;
+  int i = 0, t = tile_at(0, total);
+  if (t < 0) return;
+  Operand<kAlong, IB> a;
+  Operand<BK, JB> b;
+  int m, n, e, r0, rows, item, now;  // now: steps
+  auto with = [&](auto f) __attribute__((always_inline)) {  // f with the tile of as many rows as there are
+    if (IB > 2 && rows > 64 * (IB / 4)) f(Tile<TYPE, kAlong, BK, IB, JB, LDS, IB>());
+    else if (IB == 8 && rows > 64) f(Tile<TYPE, kAlong, BK, 4, JB, LDS, IB>());
+    else f(Tile<TYPE, kAlong, BK, 2, JB, LDS, IB>());
+  };
+  auto open = [&]() __attribute__((always_inline)) {
+    const int s = kSplit ? t / tiles : 0, k0 = s * sp.per * kDeep;
+    item = t;
+    now = min(sp.per, steps - s * sp.per);
+    tile_of(t - s * tiles, til.total, nt, &m, &n);
+    til.find(p, m, &e, &r0, &rows);
+    const int sum = min(deep - k0, sp.per * kDeep);
+    const uint16_t* w = static_cast<const uint16_t*>(p.right) + int64_t(e) * p.n * p.k;
+    a.init(static_cast<const uint16_t*>(p.left) + int64_t(r0) * p.ld_left + k0, p.ld_left, rows, sum);
+    b.init(KIND == kMmOut ? w + int64_t(n) * 32 * JB * p.k + k0 : w + int64_t(k0) * p.k + n * 32 * JB, p.k,
+           cols - n * 32 * JB, sum);
+    with([&](auto tile) __attribute__((always_inline)) { tile.begin(a, b); });
+  };
+  open();
+  int stores = 0;
+  while (t >= 0) {
+    with([&](auto tile) __attribute__((always_inline)) {
+      tile.run(a, b, now, stores);
+      const Result res = kSplit && sp.splits > 1 ? partial(p, item) : result(p, int64_t(r0) * p.ld_out + n * 32 * JB);
+      const int have = rows, left = cols - n * 32 * JB;
+      t = tile_at(++i, total);
+      if (t >= 0) open();
+      stores = store_tile(tile, res, have, left);
+    });
+  }
+}
+
+// Opens d_b's tile (m, n) over `rows` rows from r0 on.
+template <int BK, int IB, int JB, typename A, typename B>
+__device__ __forceinline__ void open_weights(const MmArgs& p, A& a, B& b, int r0, int rows, int m, int n) {
+  a.init(static_cast<const uint16_t*>(p.left) + int64_t(r0) * p.ld_left + m * 32 * IB, p.ld_left, p.n - m * 32 * IB,
+         rows);
+  const int left = p.k - n * 32 * JB;
+  if constexpr (BK == kHeld)
+    b.init(static_cast<const uint8_t*>(p.right) + int64_t(r0) * p.ld_right, p.ld_right,
+           p.scales + int64_t(r0) * p.ld_scales, p.ld_scales, n * 32 * JB, left, rows);
+  else
+    b.init(static_cast<const uint16_t*>(p.right) + int64_t(r0) * p.ld_right + n * 32 * JB, p.ld_right, left, rows);
+}
+
+// d_b in small tiles.  An expert's rows are cut into units of at most `per` steps, so that all units'
+// tiles make no more items than the workspace holds; an expert without rows has one, of zeros.  An
+// expert of several units has its partial results joined.
+__device__ __forceinline__ int unit_steps(const MmArgs& p, RowTiles& til, int per_unit) {
+  int best = 1 << 18;  // (steps of 64 rows: more than there can be)
+  if (!p.ws) return best;
+  til.init(p, kDeep);
+  const int most = til.most;
+  float us = split_us(most, min(per_unit * p.groups, kItems), false);
+  for (int items = 64; items <= kItems; items *= 2) {
+    const int units = items / per_unit - p.groups;  // units are at most steps / per + groups
+    if (units <= 0) continue;
+    const int per = max(kLeastSteps, (til.total + units - 1) / units);
+    const float t = split_us(per, items, true);
+    if (per < most && t < us) {
+      us = t;
+      best = per;
+    }
+  }
+  return best;
+}
+template <int TYPE, int BK, int IB, int JB>
+__device__ __forceinline__ void walk_units(const MmArgs& p) {
+  const int mt = (p.n + 32 * IB - 1) / (32 * IB), nt = (p.k + 32 * JB - 1) / (32 * JB), tiles = mt * nt;
+  RowTiles til;
+  til.init(p, kDeep * unit_steps(p, til, tiles), 1);
+  const int total = tiles * til.total;
+  typedef Lds<stage_bytes<kAcross, IB>(), stage_bytes<kAcross, JB>(), JB> LDS;
+  typedef Tile<TYPE, kAcross, BK, IB, JB, LDS> T;
+  int i = 0, t = tile_at(0, total);
+  if (t < 0) return;
+  typename T::A a;
+  typename T::B b;
+  int m, n, e, r0, rows, part, parts, item;
+  auto open = [&]() __attribute__((always_inline)) {
+    item = t;
+    til.find(p, t / tiles, &e, &r0, &rows, &part, &parts);
+    tile_of(t % tiles, mt, nt, &m, &n);
+    open_weights<BK, IB, JB>(p, a, b, r0, rows, m, n);
+    T::begin(a, b);
+  };
+  open();
+  int stores = 0;
+  while (t >= 0) {
+    T tile;
+    tile.run(a, b, (rows + kDeep - 1) / kDeep, stores);
+    const Result res = parts > 1 ? partial(p, item)
+                                 : result(p, (int64_t(e) * p.n + m * 32 * IB) * p.k + n * 32 * JB);
+    const int have = p.n - m * 32 * IB, left = p.k - n * 32 * JB;
+    t = tile_at(++i, total);
+    if (t >= 0) open();
+    stores = store_tile(tile, res, have, left);
+  }
+}
+
+// Partial results added up, in the order of their items.  A workgroup has 16 rows of a tile at a time,
+// a thread eight elements.
+template <int KIND, int TYPE>
+__global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
+  const int rows_of = KIND == kMmWeights ? p.n : 0, cols = KIND == kMmOut ? p.n : p.k;
+  const int mt = (rows_of + 127) / 128, nt = (cols + 127) / 128;
+  RowTiles til;
+  Split sp = {1, 0};
+  int tiles, units = 0;
+  if (KIND == kMmWeights) {
+    tiles = mt * nt;
+    til.init(p, kDeep * unit_steps(p, til, tiles), 1);
+    units = til.total;
+  } else {
+    if (KIND == kMmOut && form_of<KIND>(p, til) == kFew) return;
+    til.init(p, 128);
+    tiles = til.total * nt;
+    sp = split_of(p, tiles, ((KIND == kMmOut ? p.k : p.n) + kDeep - 1) / kDeep);
+    if (sp.splits == 1) return;
+    units = 1;
+  }
+  for (int t = blockIdx.x; t < units * tiles * 8; t += int(gridDim.x)) {
+    const int x = t >> 3, row = (t & 7) * 16 + int(threadIdx.x >> 4), col = int(threadIdx.x & 15) * 8;
+    int m, n, e, r0, rows, part, parts = sp.splits, first = x, stride = tiles;
+    int64_t at;
+    if (KIND == kMmWeights) {
+      til.find(p, x / tiles, &e, &r0, &rows, &part, &parts);
+      if (part != 0 || parts == 1) continue;
+      tile_of(x % tiles, mt, nt, &m, &n);
+      rows = p.n - m * 128;
+      at = (int64_t(e) * p.n + m * 128 + row) * p.k;
+    } else {
+      tile_of(x, til.total, nt, &m, &n);
+      til.find(p, m, &e, &r0, &rows);
+      at = int64_t(r0 + row) * p.ld_out;
+    }
+    if (row >= rows || n * 128 + col >= cols) continue;
+    at += n * 128 + col;
+    const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.ws) + int64_t(first) * 4096 + row * 32 + col / 4;
+    f32x4_t lo = from[0], hi = from[1];
+    for (int s = 1; s < parts; ++s) {
+      from += int64_t(stride) * 4096;
+      lo += from[0];
+      hi += from[1];
+    }
+    if (p.out32) {
+      f32x4_t* o = reinterpret_cast<f32x4_t*>(static_cast<float*>(p.out) + at);
+      if (p.add) {
+        lo += o[0];
+        hi += o[1];
+      }
+      o[0] = lo;
+      o[1] = hi;
+    } else {
+      *reinterpret_cast<v4u*>(static_cast<uint16_t*>(p.out) + at) =
+          v4u{pack2<TYPE>(lo.x, lo.y), pack2<TYPE>(lo.z, lo.w), pack2<TYPE>(hi.x, hi.y), pack2<TYPE>(hi.z, hi.w)};
+    }
+  }
+}
+
+// d_b in whole tiles: the experts in the order of their rows, the most first, so that the tiles of a round take
+// about as long as each other.
+template <int TYPE, int BK, int IB, int JB>
+__device__ __forceinline__ void walk_weights(const MmArgs& p) {
+  const int mt = (p.n + 32 * IB - 1) / (32 * IB), nt = (p.k + 32 * JB - 1) / (32 * JB);
+  const int per = mt * nt, total = per * p.groups, lane = threadIdx.x & 63;
+  int rank = 0;
+  if (p.groups <= 64) {
+    int lo = 0, hi = 0;
+    if (lane < p.groups) expert_rows(p, lane, &lo, &hi);
+    const int have = lane < p.groups ? max(hi - lo, 0) : -1;
+    for (int o = 0; o < p.groups; ++o) {
+      const int other = __builtin_amdgcn_readlane(have, o);
+      rank += other > have || (other == have && o < lane) ? 1 : 0;
+    }
+  }
+  typedef Lds<stage_bytes<kAcross, IB>(), stage_bytes<kAcross, JB>(), JB> LDS;
+  typedef Tile<TYPE, kAcross, BK, IB, JB, LDS> T;
+  int i = 0, t = tile_at(0, total);
+  if (t < 0) return;
+  typename T::A a;
+  typename T::B b;
+  int m, n, e, rows;
+  auto open = [&]() __attribute__((always_inline)) {
+    e = t / per;
+    tile_of(t - e * per, mt, nt, &m, &n);
+    if (p.groups <= 64) e = __ffsll((unsigned long long)__ballot(rank == e && lane < p.groups)) - 1;
+    int lo, hi;
+    expert_rows(p, e, &lo, &hi);
+    rows = __builtin_amdgcn_readfirstlane(max(hi - lo, 0));
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    open_weights<BK, IB, JB>(p, a, b, lo, rows, m, n);
+    T::begin(a, b);
+  };
+  open();
+  int stores = 0;
+  while (t >= 0) {
+    T tile;
+    tile.run(a, b, (rows + kDeep - 1) / kDeep, stores);
+    const Result res = result(p, (int64_t(e) * p.n + m * 32 * IB) * p.k + n * 32 * JB);
+    const int have = p.n - m * 32 * IB, left = p.k - n * 32 * JB;
+    t = tile_at(++i, total);
+    if (t >= 0) open();
+    stores = store_tile(tile, res, have, left);
+  }
 }
 
 // Whole tiles, a workgroup a CU; `both`: k_mm_small is launched too and the routed rows decide.
@@ -205,7 +380,7 @@ __global__ __launch_bounds__(kThr) void k_mm_tiles(MmArgs p, bool both) {
 template <int KIND, int TYPE, int BK>
 __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
   if constexpr (KIND == kMmWeights) {
-    walk_weights<TYPE, BK, 4, 4>(p);
+    walk_units<TYPE, BK, 4, 4>(p);
   } else {
     RowTiles til;
     const bool look = both || KIND == kMmOut;
@@ -226,6 +401,7 @@ __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
   }
 }
 
+// (a.ws is set only where sums may be split, which is where small tiles make a round at most.)
 // Which kernels are launched: whole tiles alone where there may be four rounds of them (buffers hold
 // about as many rows as are routed), small ones (and few rows) alone where these make a round at most,
 // otherwise both, one of which returns at once (2 us).  A product of weights has its tiles whatever
@@ -249,6 +425,11 @@ mok_status_t launch_tiles(const MmArgs& a, hipStream_t st) {
   auto go = [&](auto kern, int grid) { return launch(kern, dim3(grid), dim3(kThr), st, a, both); };
   if (!whole)
     s = a.type == MOK_TYPE_BF16 ? go(k_mm_small<KIND, MOK_TYPE_BF16, BK>, 512) : go(k_mm_small<KIND, MOK_TYPE_FP16, BK>, 512);
+  if (a.ws && s == MOK_OK) {
+    const dim3 grid(512), block(256);
+    s = a.type == MOK_TYPE_BF16 ? launch(k_mm_join<KIND, MOK_TYPE_BF16>, grid, block, st, a)
+                                : launch(k_mm_join<KIND, MOK_TYPE_FP16>, grid, block, st, a);
+  }
   if (!small && s == MOK_OK)
     s = a.type == MOK_TYPE_BF16 ? go(k_mm_tiles<KIND, MOK_TYPE_BF16, BK>, 256) : go(k_mm_tiles<KIND, MOK_TYPE_FP16, BK>, 256);
   return s;

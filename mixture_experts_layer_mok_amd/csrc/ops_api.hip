@@ -101,6 +101,14 @@ mok_status_t check_mm(int32_t type, int32_t out_type, int64_t max_rows, int32_t 
     return MOK_E_SHAPE;
   return MOK_OK;
 }
+// The workspace: too small or unaligned, or the pointer that the product gets (null where it would not
+// split its sums).
+mok_status_t check_ws(MmKind kind, void** ws, size_t bytes, int64_t max_rows, int32_t groups, int32_t n, int32_t k) {
+  if (*ws && bytes < MOK_MM_WORKSPACE_BYTES) return MOK_E_WORKSPACE;
+  if (!aligned(*ws, 16)) return MOK_E_SHAPE;
+  if (!mm_may_split(kind, max_rows, groups, n, k)) *ws = nullptr;
+  return MOK_OK;
+}
 // A row operand's stride in elements: rows of a tile stay within 31-bit byte offsets.
 bool mm_ld_ok(int64_t ld, int32_t cols, bool read) {
   return ld % 8 == 0 && ld <= kMaxLdOut && (ld >= cols || (read && ld == 0));
@@ -230,32 +238,46 @@ mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t l
                             static_cast<hipStream_t>(stream));
 }
 
+mok_status_t mok_grouped_mm_workspace(int32_t which, int64_t max_rows, int32_t groups, int32_t n,
+                                      int32_t k, size_t* bytes) {
+  if (!bytes) return MOK_E_NULL;
+  if (which < 0 || which > 2) return MOK_E_UNSUPPORTED;
+  const mok_status_t s = check_mm(MOK_TYPE_BF16, MOK_TYPE_BF16, max_rows, groups, n, k);
+  if (s != MOK_OK) return s;
+  *bytes = mm_may_split(MmKind(which), max_rows, groups, n, k) ? MOK_MM_WORKSPACE_BYTES : 0;
+  return MOK_OK;
+}
+
 mok_status_t mok_grouped_mm(int32_t type, const void* a, int64_t ld_a, int64_t max_rows,
                             const int32_t* offsets, int32_t groups, const void* b, int32_t n,
-                            int32_t k, int32_t out_type, void* out, int64_t ld_out, void* stream) {
+                            int32_t k, int32_t out_type, void* out, int64_t ld_out, void* ws,
+                            size_t ws_bytes, void* stream) {
   const mok_status_t s = check_mm(type, out_type, max_rows, groups, n, k);
   if (s != MOK_OK) return s;
   if (!mm_ld_ok(ld_a, k, true) || !mm_ld_ok(ld_out, n, false)) return MOK_E_SHAPE;
+  if (const mok_status_t w = check_ws(kMmOut, &ws, ws_bytes, max_rows, groups, n, k)) return w;
   if (max_rows == 0) return MOK_OK;
   if (!a || !offsets || !b || !out) return MOK_E_NULL;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16) || !aligned(offsets, 4)) return MOK_E_SHAPE;
   return launch_grouped_mm(kMmOut, {type, a, ld_a, b, 0, nullptr, 0, max_rows, offsets, groups, n, k,
-                                    out_type == MOK_TYPE_FP32, false, out, ld_out},
+                                    out_type == MOK_TYPE_FP32, false, out, ld_out, static_cast<float*>(ws)},
                            static_cast<hipStream_t>(stream));
 }
 
 mok_status_t mok_grouped_mm_bwd_rows(int32_t type, const void* d_out, int64_t ld_d_out,
                                      int64_t max_rows, const int32_t* offsets, int32_t groups,
                                      const void* b, int32_t n, int32_t k, int32_t out_type,
-                                     void* d_a, int64_t ld_d_a, void* stream) {
+                                     void* d_a, int64_t ld_d_a, void* ws, size_t ws_bytes,
+                                     void* stream) {
   const mok_status_t s = check_mm(type, out_type, max_rows, groups, n, k);
   if (s != MOK_OK) return s;
   if (!mm_ld_ok(ld_d_out, n, true) || !mm_ld_ok(ld_d_a, k, false)) return MOK_E_SHAPE;
+  if (const mok_status_t w = check_ws(kMmRows, &ws, ws_bytes, max_rows, groups, n, k)) return w;
   if (max_rows == 0) return MOK_OK;
   if (!d_out || !offsets || !b || !d_a) return MOK_E_NULL;
   if (!aligned(d_out, 16) || !aligned(b, 16) || !aligned(d_a, 16) || !aligned(offsets, 4)) return MOK_E_SHAPE;
   return launch_grouped_mm(kMmRows, {type, d_out, ld_d_out, b, 0, nullptr, 0, max_rows, offsets, groups, n, k,
-                                     out_type == MOK_TYPE_FP32, false, d_a, ld_d_a},
+                                     out_type == MOK_TYPE_FP32, false, d_a, ld_d_a, static_cast<float*>(ws)},
                            static_cast<hipStream_t>(stream));
 }
 
@@ -264,7 +286,7 @@ mok_status_t mok_grouped_mm_bwd_weights(int32_t type, const void* d_out, int64_t
                                         int64_t ld_a_scales, int64_t max_rows,
                                         const int32_t* offsets, int32_t groups, int32_t n,
                                         int32_t k, int32_t out_type, void* d_b,
-                                        int32_t accumulate, void* stream) {
+                                        int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
   const mok_status_t s = check_mm(type, out_type, max_rows, groups, n, k);
   if (s != MOK_OK) return s;
   if (accumulate && out_type != MOK_TYPE_FP32) return MOK_E_UNSUPPORTED;
@@ -276,10 +298,12 @@ mok_status_t mok_grouped_mm_bwd_weights(int32_t type, const void* d_out, int64_t
   } else if (!mm_ld_ok(ld_a, k, true)) {
     return MOK_E_SHAPE;
   }
+  if (const mok_status_t w = check_ws(kMmWeights, &ws, ws_bytes, max_rows, groups, n, k)) return w;
   if (!offsets || !d_b || (max_rows > 0 && (!a || !d_out))) return MOK_E_NULL;
   if (!aligned(a, 16) || !aligned(d_out, 16) || !aligned(d_b, 16) || !aligned(offsets, 4)) return MOK_E_SHAPE;
   return launch_grouped_mm(kMmWeights, {type, d_out, ld_d_out, a, ld_a, a_scales, ld_a_scales, max_rows, offsets,
-                                        groups, n, k, out_type == MOK_TYPE_FP32, accumulate != 0, d_b, k},
+                                        groups, n, k, out_type == MOK_TYPE_FP32, accumulate != 0, d_b, k,
+                                        static_cast<float*>(ws)},
                            static_cast<hipStream_t>(stream));
 }
 

@@ -100,7 +100,10 @@ struct MmArgs {
   bool out32, add;
   void* out;
   int64_t ld_out;
+  float* ws;  // MOK_MM_WORKSPACE_BYTES for partial sums, or null
 };
+// Whether a product's sums may be split over workgroups, given a workspace.
+bool mm_may_split(MmKind kind, int64_t max_rows, int32_t groups, int32_t n, int32_t k);
 mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_out(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_rows(const MmArgs& a, hipStream_t st);

@@ -180,7 +180,8 @@ def _bind(lib) -> None:
     module.bind(getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), _raw_stream,
                 *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names))
     more = ("mok_grouped_mm", "mok_grouped_mm_bwd_rows", "mok_grouped_mm_bwd_weights",
-            "mok_quantize_mx8", "mok_dequantize_mx8", "mok_swiglu_mx8", "mok_swiglu_mx8_bwd")
+            "mok_quantize_mx8", "mok_dequantize_mx8", "mok_swiglu_mx8", "mok_swiglu_mx8_bwd",
+            "mok_grouped_mm_workspace")
     module.bind_more(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in more))
     _fast = module
 
@@ -435,6 +436,15 @@ def _experts(b) -> tuple:
     return (*b.shape, *_flat("b", b, b.shape, b.dtype))
 
 
+def _workspace(which, rows, E, N, K, dev):
+    """(workspace or None, its bytes) of a product, on the stream that is current."""
+    try:
+        n = L.mok_grouped_mm_workspace(which, rows, E, N, K)
+    except L.MokError:  # the product's own refusal follows
+        n = 0
+    return (torch.empty(n, dtype=torch.uint8, device=dev), n) if n else (None, 0)
+
+
 def _product(fn, name, rows, offsets, b, forward, out, dtype, stream):
     E, N, K, pb, be = _experts(b)
     pf, fe = _flat("offsets", offsets, (E + 1,), torch.int32)
@@ -453,7 +463,8 @@ def _product(fn, name, rows, offsets, b, forward, out, dtype, stream):
             raise ValueError(f"out: {b.dtype} or float32 is wanted")
         _same_device(dev, out)
         _apart("out", po, oe, ((name, pr, re), ("offsets", pf, fe), ("b", pb, be)))
-        _call(fn, _TYPES[b.dtype], pr, ld_r, n, pf, E, pb, N, K, _TYPES[out.dtype], po, ld_o, st)
+        ws = _workspace(0 if forward else 1, n, E, N, K, dev)
+        _call(fn, _TYPES[b.dtype], pr, ld_r, n, pf, E, pb, N, K, _TYPES[out.dtype], po, ld_o, *ws, st)
     _written(given)
     return out
 
@@ -524,7 +535,7 @@ def grouped_mm_backward_weights(d_out, a, offsets, a_scales=None, out=None, dtyp
         _apart("out", po, oe, (("d_out", pd, de), ("a", pa, ae), ("offsets", pf, fe),
                                ("a_scales", ps or 0, se)))
         _call("mok_grouped_mm_bwd_weights", _TYPES[d_out.dtype], pd, ld_d, pa, ld_a, ps, ld_s, n, pf,
-              E, N, K, _TYPES[out.dtype], po, int(bool(accumulate)), st)
+              E, N, K, _TYPES[out.dtype], po, int(bool(accumulate)), *_workspace(2, n, E, N, K, dev), st)
     _written(given)
     return out
 

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from mixture_experts_layer_mok_amd import _lib as L
 from mixture_experts_layer_mok_amd import ops
 from oracle import operators as O
 
@@ -352,3 +353,55 @@ def test_the_two_directions_meet():
     size = sum((np.abs(c.g64[lo:hi]) @ np.abs(c.b64[e]) * np.abs(c.a64[lo:hi])).sum()
                for e, (lo, hi) in enumerate(zip(c.offsets, c.offsets[1:])))
     assert abs(s[0] - s[1]) <= 600 * 2.0**-23 * size and abs(s[0] - s[2]) <= 600 * 2.0**-23 * size
+
+
+def c_call(kind, c, out, ws):
+    """The C entry point with a workspace of the caller's, or none."""
+    E = len(c.offsets) - 1
+    ty = {BF: L.MOK_TYPE_BF16, FP: L.MOK_TYPE_FP16, F32: L.MOK_TYPE_FP32}
+    w = (ws, 0 if ws is None else ws.numel())
+    if kind == "out":
+        L.mok_grouped_mm(ty[c.dtype], c.a, c.k, c.rows, c.off, E, c.b, c.n, c.k, ty[out.dtype], out, c.n, *w)
+    elif kind == "rows":
+        L.mok_grouped_mm_bwd_rows(ty[c.dtype], c.g, c.n, c.rows, c.off, E, c.b, c.n, c.k, ty[out.dtype], out, c.k, *w)
+    else:
+        held = c.scales is not None
+        L.mok_grouped_mm_bwd_weights(ty[c.dtype], c.g, c.n, c.codes if held else c.a, c.k, c.scales,
+                                     c.k // 32 if held else 0, c.rows, c.off, E, c.n, c.k, ty[out.dtype], out,
+                                     kind == "weights+", *w)
+
+
+SPLITS = [  # rows an expert, n, k: long sums of few results
+    ("out", [300], 136, 4104), ("out", [1, 200, 0, 77], 72, 8200), ("out", [130], 264, 1544),
+    ("rows", [300], 4104, 136), ("rows", [1, 200, 0, 77], 8200, 72), ("rows", [130], 1544, 264),
+    ("weights", [5000], 136, 264), ("weights", [4000, 0, 1, 700], 72, 40), ("weights", [0, 2100], 264, 8),
+    ("weights", [513, 1830, 64, 63], 136, 136), ("weights", [30] * 70, 40, 24), ("weights+", [3000, 0, 70], 136, 72),
+    ("held", [5000], 136, 288), ("held", [4000, 0, 1, 700], 72, 32), ("held", [513, 1830, 64, 63], 264, 160),
+]
+
+
+@pytest.mark.parametrize("kind,counts,n,k", SPLITS, ids=lambda v: str(v)[:24].replace(" ", ""))
+@pytest.mark.parametrize("dtype", [BF, FP], ids=IDS)
+def test_sums_split_over_workgroups(kind, counts, n, k, dtype):
+    say(f"[mm] split {kind} {counts[:4]} n {n} k {k}")
+    held = kind == "held"
+    kind = "weights" if held else kind
+    which = dict(out=0, rows=1).get(kind, 2)
+    c = Case(counts, n, k, dtype, seed=21, whole=True, held=held)
+    assert L.mok_grouped_mm_workspace(which, c.rows, len(counts), n, k) == L.MOK_MM_WORKSPACE_BYTES
+    out_types = [F32] if kind == "weights+" else [dtype, F32]
+    for out_dtype in out_types:
+        o = check(c, kind, out_dtype, True)
+        check(Case(counts, n, k, dtype, seed=22, held=held), kind, out_dtype, False)
+        for ws in (None, torch.full((L.MOK_MM_WORKSPACE_BYTES,), 255, dtype=torch.uint8, device=DEV)):
+            again = torch.full_like(o, 7.0)
+            c_call(kind, c, again, ws)
+            assert torch.equal(again, o)
+
+
+def test_a_split_product_again_the_same_bits():
+    for kind, counts, n, k in (SPLITS[1], SPLITS[4], SPLITS[7]):
+        c = Case(counts, n, k, BF, seed=23)
+        first = check(c, kind, F32, False)
+        for _ in range(3):
+            assert torch.equal(check(c, kind, F32, False), first)

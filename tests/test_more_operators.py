@@ -87,13 +87,13 @@ def test_mx8_codes_by_hand():
 # refusals of the C ABI
 # ----------------------------------------------------------------------------------------
 def _mm_calls(type=0, ld_a=64, ld_o=32, n_rows=8, off=FAKE, groups=2, b=FAKE, n=32, k=64, ty=0, a=FAKE,
-              o=FAKE):
+              o=FAKE, ws=None, wsb=0):
     lib = L.load()
-    return dict(out=lib.mok_grouped_mm(type, a, ld_a, n_rows, off, groups, b, n, k, ty, o, ld_o, None),
+    return dict(out=lib.mok_grouped_mm(type, a, ld_a, n_rows, off, groups, b, n, k, ty, o, ld_o, ws, wsb, None),
                 rows=lib.mok_grouped_mm_bwd_rows(type, o, ld_o, n_rows, off, groups, b, n, k, ty, a, ld_a,
-                                                 None),
+                                                 ws, wsb, None),
                 weights=lib.mok_grouped_mm_bwd_weights(type, o, ld_o, a, ld_a, None, 0, n_rows, off, groups,
-                                                       n, k, ty, b, 0, None))
+                                                       n, k, ty, b, 0, ws, wsb, None))
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -109,6 +109,8 @@ def _mm_calls(type=0, ld_a=64, ld_o=32, n_rows=8, off=FAKE, groups=2, b=FAKE, n=
     (dict(ld_o=(1 << 21) + 8), L.MOK_E_SHAPE), (dict(a=None), L.MOK_E_NULL), (dict(o=None), L.MOK_E_NULL),
     (dict(b=None), L.MOK_E_NULL), (dict(off=None), L.MOK_E_NULL), (dict(a=FAKE + 8), L.MOK_E_SHAPE),
     (dict(o=FAKE + 2), L.MOK_E_SHAPE), (dict(b=FAKE + 8), L.MOK_E_SHAPE), (dict(off=FAKE + 2), L.MOK_E_SHAPE),
+    (dict(ws=FAKE), L.MOK_E_WORKSPACE), (dict(ws=FAKE, wsb=L.MOK_MM_WORKSPACE_BYTES - 1), L.MOK_E_WORKSPACE),
+    (dict(ws=FAKE + 8, wsb=L.MOK_MM_WORKSPACE_BYTES), L.MOK_E_SHAPE),
 ])
 def test_grouped_mm_refuses(kw, code):
     assert set(_mm_calls(**kw).values()) == {code}
@@ -120,7 +122,8 @@ def test_grouped_mm_refuses_written_strides_and_8_bits():
     fn = L.load().mok_grouped_mm_bwd_weights
 
     def call(type=0, a=FAKE, ld_a=64, s=FAKE, ld_s=2, k=64, ty=2, add=0):
-        return fn(type, FAKE, 32, a, ld_a, s, ld_s, 8, FAKE, 2, 32, k, ty, FAKE, add, None)
+        return fn(type, FAKE, 32, a, ld_a, s, ld_s, 8, FAKE, 2, 32, k, ty, FAKE, add, None, 0,
+                  None)
 
     for kw in (dict(k=40), dict(ld_a=72), dict(ld_a=48), dict(ld_a=(1 << 22) + 16), dict(ld_s=1),
                dict(ld_s=(1 << 21) + 1), dict(a=FAKE + 4)):
@@ -129,12 +132,27 @@ def test_grouped_mm_refuses_written_strides_and_8_bits():
     assert call(a=None) == L.MOK_E_NULL
 
 
+def test_workspace_of_products():
+    all_of = L.MOK_MM_WORKSPACE_BYTES
+    w = L.mok_grouped_mm_workspace
+    assert w(2, 16384, 1, 1024, 1024) == all_of  # 64 tiles of 256 steps
+    assert w(2, 16384, 8, 4096, 7168) == w(2, 512, 1, 1024, 1024) == 0
+    assert w(0, 2000, 1, 64, 8192) == w(1, 2000, 1, 8192, 64) == all_of
+    assert w(0, 2000, 1, 8192, 64) == w(1, 2000, 1, 64, 8192) == w(0, 16384, 8, 4096, 7168) == 0
+    for bad, code in (((3, 8, 1, 64, 64), L.MOK_E_UNSUPPORTED), ((0, -1, 1, 64, 64), L.MOK_E_SHAPE),
+                      ((0, 8, 0, 64, 64), L.MOK_E_SHAPE), ((2, 8, 1, 60, 64), L.MOK_E_SHAPE)):
+        with pytest.raises(L.MokError) as e:
+            w(*bad)
+        assert e.value.code == code
+    assert L.load().mok_grouped_mm_workspace(0, 8, 1, 64, 64, None) == L.MOK_E_NULL
+
+
 def test_empty_calls_do_nothing():
     lib = L.load()
     got = _mm_calls(n_rows=0, a=None, o=None)
     assert got["out"] == got["rows"] == L.MOK_OK
     assert lib.mok_grouped_mm_bwd_weights(0, None, 32, None, 64, None, 0, 0, None, 2, 32, 64, 0, FAKE, 0,
-                                          None) == L.MOK_E_NULL  # (its result is 0, not nothing)
+                                          None, 0, None) == L.MOK_E_NULL  # (its result is 0, not nothing)
     assert lib.mok_quantize_mx8(0, None, 64, 0, 64, None, 64, None, 2, None) == L.MOK_OK
     assert lib.mok_dequantize_mx8(None, 64, None, 2, 0, 64, 0, None, 64, None) == L.MOK_OK
     assert lib.mok_swiglu_mx8(0, None, 64, 0, 32, None, 0, None, 32, None, 64, None, 2, None) == L.MOK_OK
@@ -287,6 +305,6 @@ def test_the_extension_module_passes_on_what_is_not_in_order():
     with pytest.raises(TypeError):
         _fast.bind_more(1, 2)
     with pytest.raises(TypeError):
-        _fast.bind_more(*["a"] * 7)
+        _fast.bind_more(*["a"] * 8)
     with pytest.raises(ValueError):
-        _fast.bind_more(*[0] * 7)
+        _fast.bind_more(*[0] * 8)
