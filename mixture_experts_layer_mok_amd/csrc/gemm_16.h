@@ -497,6 +497,11 @@ struct Tile {
     for (int i = 0; i < IB; ++i)
 #pragma unroll
       for (int j = 0; j < JB; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    // (written here, well before the first MFMA, and not made again next to one)
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+      for (int j = 0; j < JB; ++j) asm volatile("" : "+a"(acc[i][j]));
     wait_all_but(stores);  // steps 0 and 1
     if constexpr (kHolds) {
       convert<0>(b, LDS::b(), std::make_integer_sequence<int, 3 * JB>());
