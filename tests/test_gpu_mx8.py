@@ -255,3 +255,24 @@ def test_far_rows(dtype):
     assert torch.equal(ops.dequantize_mx8(cs, ss, dtype=dtype), ops.dequantize_mx8(c, s, dtype=dtype))
     del cs, ss, ds
     torch.cuda.empty_cache()
+
+
+@TYPES
+def test_large_calls_give_what_their_slices_give(dtype):
+    """A call of hundreds of MiB reads its values another way; each element comes of its own block
+    (or pair) only, so a slice of rows, taken alone, has the same bits."""
+    rows, cols = (9001, 8256) if dtype is F32 else (17000, 8256)
+    torch.manual_seed(7)
+    x = torch.randn(rows, cols, device=DEV, dtype=dtype)
+    dh = torch.randn(rows, cols // 2, device=DEV, dtype=dtype)
+    codes, scales = ops.quantize_mx8(x)
+    h, held, held_scales = ops.swiglu_mx8(x)
+    d_ab, again = ops.swiglu_mx8_backward(dh, held, held_scales)
+    assert torch.equal(codes, held) and torch.equal(scales, held_scales)
+    for a, b in ((0, 1), (4000, 4313), (rows - 65, rows)):
+        part, part_scales = ops.quantize_mx8(x[a:b])
+        assert torch.equal(part, codes[a:b]) and torch.equal(part_scales, scales[a:b])
+        h_part, _, _ = ops.swiglu_mx8(x[a:b])
+        assert torch.equal(h_part, h[a:b])
+        d_part, again_part = ops.swiglu_mx8_backward(dh[a:b], held[a:b], held_scales[a:b])
+        assert torch.equal(d_part, d_ab[a:b]) and torch.equal(again_part, again[a:b])
