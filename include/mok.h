@@ -414,7 +414,8 @@ mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t l
  * ws: NULL, or a workspace of ws_bytes >= MOK_MM_WORKSPACE_BYTES, 16-byte aligned, of this
  * call alone until its work is done.  With it long sums of few results are split over
  * workgroups (one expert of 16384 rows, n 1024, k 1024: the weights' gradient takes 0.17 ms
- * without); mok_grouped_mm_workspace says where that may be.  Errors: MOK_E_NULL,
+ * without), and so is the last round of few tiles of long sums; mok_grouped_mm_workspace
+ * says where that may be.  Errors: MOK_E_NULL,
  * MOK_E_SHAPE, MOK_E_UNSUPPORTED (types), MOK_E_WORKSPACE, MOK_E_LAUNCH.  Asynchronous on
  * stream, kernel launches only; fixed-order sums, bitwise repeatable for the same arguments
  * (with and without a workspace the order may differ). */

@@ -38,6 +38,9 @@ __device__ __forceinline__ int max64(int x) {
 // The m-tiles of all experts (each expert's rows cut from its first row on into tiles of `tall`),
 // numbered in expert order; an expert without rows has `least` of them (0 or 1).  Every wave scans
 // the experts, 64 at a time, all lanes active; with at most 64 of them they are read once.
+//
+// init_sorted numbers those of more than half a tile first, in expert order, then the others, which take
+// less time: of more than a quarter, then of less.  So the last round of tiles is the shortest.
 struct RowTiles {
   int tall, least;
   int lo, hi;   // this lane's expert of the current 64: rows
@@ -45,6 +48,8 @@ struct RowTiles {
   int tiles, incl;  // its m-tiles, and those up to it
   int total;    // m-tiles of all experts
   int most;     // of one expert
+  bool sorted = false;
+  int wholes, rank;  // sorted: how many come in expert order; this lane's place among the others, or -1
 
   __device__ __forceinline__ void read(const MmArgs& p, int e0) {
     const int lane = threadIdx.x & 63;
@@ -59,6 +64,7 @@ struct RowTiles {
   }
   // have: the experts, at most 64, are read already.
   __device__ __forceinline__ void init(const MmArgs& p, int tall_, int least_ = 0, bool have = false) {
+    sorted = false;
     tall = tall_;
     least = least_;
     total = most = 0;
@@ -68,6 +74,21 @@ struct RowTiles {
       total += __builtin_amdgcn_readlane(incl, 63);
       most = max(most, max64(tiles));
     }
+  }
+  __device__ __forceinline__ void init_sorted(const MmArgs& p, int tall_, bool have = false) {
+    if (p.groups > 64) return init(p, tall_);
+    sorted = true;
+    tall = tall_;
+    if (!have) read(p, 0);
+    const int n = max(hi - lo, 0);
+    const int rest = n % tall;
+    tiles = n / tall + (rest > tall / 2 ? 1 : 0);
+    incl = scan64(tiles);
+    wholes = __builtin_amdgcn_readlane(incl, 63);
+    const bool more = rest > tall / 4 && rest <= tall / 2, less = rest > 0 && rest <= tall / 4;
+    const uint64_t m = __ballot(more), l = __ballot(less), before = (1ull << (threadIdx.x & 63)) - 1;
+    rank = more ? __popcll(m & before) : less ? __popcll(m) + __popcll(l & before) : -1;
+    total = wholes + __popcll(m) + __popcll(l);
   }
   // m-tile m < total: its expert, first row and rows, its number among the expert's m-tiles and
   // how many those are.
@@ -91,6 +112,15 @@ struct RowTiles {
     *rows = max(min(__builtin_amdgcn_readlane(hi, s) - first, tall), 0);
   }
   __device__ __forceinline__ void find(const MmArgs& p, int m, int* e, int* r0, int* rows) {
+    if (sorted) {
+      const bool whole = m < wholes;
+      const int s = __ffsll((unsigned long long)__ballot(whole ? incl > m : rank == m - wholes)) - 1;
+      const int have = __builtin_amdgcn_readlane(tiles, s), first = __builtin_amdgcn_readlane(lo, s);
+      *e = s;
+      *r0 = first + tall * (whole ? m - (__builtin_amdgcn_readlane(incl, s) - have) : have);
+      *rows = min(__builtin_amdgcn_readlane(hi, s) - *r0, tall);
+      return;
+    }
     int part, parts;
     find(p, m, e, r0, rows, &part, &parts);
   }

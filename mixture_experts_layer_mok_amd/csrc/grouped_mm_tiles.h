@@ -42,8 +42,8 @@ struct Result {
 __device__ __forceinline__ Result result(const MmArgs& p, int64_t first) {
   return {static_cast<uint8_t*>(p.out) + first * (p.out32 ? 4 : 2), p.ld_out, p.out32, p.add};
 }
-__device__ __forceinline__ Result partial(const MmArgs& p, int item) {
-  return {p.ws + int64_t(item) * (128 * 128), 128, true, false};
+__device__ __forceinline__ Result partial(const MmArgs& p, int item, int tall = 128, int wide = 128) {
+  return {p.ws + int64_t(item) * (tall * wide), wide, true, false};
 }
 template <typename T>
 __device__ __forceinline__ int store_tile(const T& tile, const Result& r, int rows, int cols) {
@@ -90,6 +90,40 @@ __device__ __forceinline__ Split split_of(const MmArgs& p, int tiles, int steps)
   return best;
 }
 
+// The last round of whole tiles, if it has at most half of the workgroups: its tiles are summed in
+// `splits` items of `per` steps each, as above; an item holds `tall` rows, as many as the round's
+// tallest tile needs.  A step takes 1.4 us in a whole tile, 1.1 with at most 128 rows and 0.95 with 64
+// (the loads' latency: two steps are in flight, whatever the tile).  Measured on MI355X, without and
+// with, us: 16,384 rows of 8 experts with about 2048 each, N 4096, K 7168 (1024 tiles and 64 of a few
+// rows) 790 / 739, rows' gradient 784 / 754; 8192 rows, N 2048, K 4096 162 / 132; 4000 rows, N 4096,
+// K 7168 311 / 220; 4400 rows of one expert 275 / 222; the launch that joins costs 3 to 5 where the
+// routed rows leave no such round (3777 rows, skewed, N 7168, K 4096: 216 / 222), so short sums (less
+// than 4096) are left alone.
+constexpr int kRound = 256;  // workgroups of whole tiles
+struct Tail {
+  int first, tiles, splits, per, tall;
+  float us;  // what the round takes
+};
+__device__ __forceinline__ Tail tail_of(const MmArgs& p, RowTiles& t, int nt, int steps) {
+  const int total = t.total * nt, first = total / kRound * kRound, r = total - first;
+  Tail best = {total, 0, 1, steps, 256, 0.f};
+  if (r == 0) return best;
+  best.us = 1.4f * float(steps) + 6.f;
+  if (!p.ws || !t.sorted || 2 * r > kRound) return best;
+  int e, r0, rows;
+  t.find(p, first / (kGroupM * nt) * kGroupM, &e, &r0, &rows);  // (none after it needs more)
+  const int tall = rows > 128 ? 256 : rows > 64 ? 128 : 64;
+  const float step = tall == 256 ? 1.4f : tall == 128 ? 1.1f : 0.95f;
+  best.us = step * float(steps) + 6.f;
+  for (int n = 2; n * r <= kRound && n * r * tall <= int(MOK_MM_WORKSPACE_BYTES / 1024) && n * kLeastSteps <= steps;
+       n *= 2) {
+    const int per = (steps + n - 1) / n;
+    const float us = step * float(per) + 11.f + 0.033f * float(n * r * (tall / 64));
+    if (us < best.us) best = {first, r, (steps + per - 1) / per, per, tall, us};
+  }
+  return best;
+}
+
 // Which kernel has a product of rows, from estimates in microseconds: rounds of tiles times steps at
 // what a step was measured to take, or the weights of the experts that have rows at 5.2 TB/s.
 //   few:   every pass reads its expert's weights, and takes a third longer with more than 16 rows;
@@ -107,7 +141,7 @@ __device__ __forceinline__ Split split_of(const MmArgs& p, int tiles, int steps)
 // 2000 rows 146 / 127, 4000 rows 148 / 164.
 enum Form { kFew, kSmall, kWhole };
 template <int KIND>
-__device__ __forceinline__ Form form_of(const MmArgs& p, RowTiles& t) {
+__device__ __forceinline__ Form form_of(const MmArgs& p, RowTiles& t, bool both) {
   int n256 = 0, n128 = 0, n32 = 0, n16 = 0, live = 0;
   for (int e0 = 0; e0 < p.groups; e0 += 64) {
     t.read(p, e0);
@@ -129,7 +163,15 @@ __device__ __forceinline__ Form form_of(const MmArgs& p, RowTiles& t) {
       4.f + (sp.splits > 1 ? 5.f : 0.f) +
       fmaxf(least, float(sp.per) * (items <= 256 ? 0.72f : float((items + 511) / 512) *
                                                                (KIND == kMmOut ? 0.95f : 1.1f)));
-  const float us_whole = 4.f + fmaxf(least, float((whole + 255) / 256) * (1.4f * steps + 6.f));
+  float us_whole = 1e30f;
+  if (both) {
+    us_whole = float((whole + 255) / 256) * (1.4f * steps + 6.f);
+    if (p.ws && p.groups <= 64 && whole % kRound != 0) {
+      t.init_sorted(p, 256, true);
+      us_whole = float(whole / 256) * (1.4f * steps + 6.f) + tail_of(p, t, (cols + 255) / 256, int(steps)).us;
+    }
+    us_whole = 4.f + fmaxf(least, us_whole);
+  }
   if (KIND == kMmOut) {
     const float passes = float(n32) * float((p.n + 63) / 64);
     // (a wave's pair of chunks takes 1.5 at least, and four waves share the sum)
@@ -151,7 +193,8 @@ __device__ __forceinline__ void walk_rows(const MmArgs& p, RowTiles& til) {
   const int nt = (cols + 32 * JB - 1) / (32 * JB), tiles = til.total * nt;
   const int steps = (deep + kDeep - 1) / kDeep;
   const Split sp = kSplit ? split_of(p, tiles, steps) : Split{1, steps};
-  const int total = tiles * sp.splits;
+  const Tail tail = kSplit ? Tail{0, tiles, sp.splits, sp.per, 128, 0.f} : tail_of(p, til, nt, steps);
+  const int total = tail.first + tail.tiles * tail.splits;
   int i = 0, t = tile_at(0, total);
   if (t < 0) return;
   Operand<kAlong, IB> a;
@@ -163,12 +206,13 @@ __device__ __forceinline__ void walk_rows(const MmArgs& p, RowTiles& til) {
     else f(Tile<TYPE, kAlong, BK, 2, JB, LDS, IB>());
   };
   auto open = [&]() __attribute__((always_inline)) {
-    const int s = kSplit ? t / tiles : 0, k0 = s * sp.per * kDeep;
+    const bool cut = t >= tail.first;
+    const int s = cut ? (t - tail.first) / tail.tiles : 0, per = cut ? tail.per : steps, k0 = s * per * kDeep;
     item = t;
-    now = min(sp.per, steps - s * sp.per);
-    tile_of(t - s * tiles, til.total, nt, &m, &n);
+    now = min(per, steps - s * per);
+    tile_of(t - s * tail.tiles, til.total, nt, &m, &n);
     til.find(p, m, &e, &r0, &rows);
-    const int sum = min(deep - k0, sp.per * kDeep);
+    const int sum = min(deep - k0, per * kDeep);
     const uint16_t* w = static_cast<const uint16_t*>(p.right) + int64_t(e) * p.n * p.k;
     a.init(static_cast<const uint16_t*>(p.left) + int64_t(r0) * p.ld_left + k0, p.ld_left, rows, sum);
     b.init(KIND == kMmOut ? w + int64_t(n) * 32 * JB * p.k + k0 : w + int64_t(k0) * p.k + n * 32 * JB, p.k,
@@ -180,7 +224,9 @@ __device__ __forceinline__ void walk_rows(const MmArgs& p, RowTiles& til) {
   while (t >= 0) {
     with([&](auto tile) __attribute__((always_inline)) {
       tile.run(a, b, now, stores);
-      const Result res = kSplit && sp.splits > 1 ? partial(p, item) : result(p, int64_t(r0) * p.ld_out + n * 32 * JB);
+      const Result res = tail.splits > 1 && item >= tail.first
+                             ? partial(p, item - tail.first, tail.tall, 32 * JB)
+                             : result(p, int64_t(r0) * p.ld_out + n * 32 * JB);
       const int have = rows, left = cols - n * 32 * JB;
       t = tile_at(++i, total);
       if (t >= 0) open();
@@ -257,30 +303,46 @@ __device__ __forceinline__ void walk_units(const MmArgs& p) {
   }
 }
 
-// Partial results added up, in the order of their items.  A workgroup has 16 rows of a tile at a time,
-// a thread eight elements.
+// Which kernels of a product are launched.
+enum Launched { kOnlySmall, kOnlyWhole, kBoth };
+
+// Partial results added up, in the order of their items.  A thread has eight elements.
 template <int KIND, int TYPE>
-__global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
+__global__ __launch_bounds__(256) void k_mm_join(MmArgs p, Launched what) {
   const int rows_of = KIND == kMmWeights ? p.n : 0, cols = KIND == kMmOut ? p.n : p.k;
-  const int mt = (rows_of + 127) / 128, nt = (cols + 127) / 128;
+  const int steps = ((KIND == kMmOut ? p.k : p.n) + kDeep - 1) / kDeep;
   RowTiles til;
-  Split sp = {1, 0};
-  int tiles, units = 0;
+  int splits = 1, units = 1, tiles, tall = 128, wide = 128, begin = 0;
   if (KIND == kMmWeights) {
-    tiles = mt * nt;
+    tiles = ((rows_of + 127) / 128) * ((cols + 127) / 128);
     til.init(p, kDeep * unit_steps(p, til, tiles), 1);
     units = til.total;
   } else {
-    if (KIND == kMmOut && form_of<KIND>(p, til) == kFew) return;
-    til.init(p, 128);
-    tiles = til.total * nt;
-    sp = split_of(p, tiles, ((KIND == kMmOut ? p.k : p.n) + kDeep - 1) / kDeep);
-    if (sp.splits == 1) return;
-    units = 1;
+    const Form form = what == kOnlyWhole                   ? kWhole
+                      : what == kBoth || KIND == kMmOut ? form_of<KIND>(p, til, what == kBoth)
+                                                           : kSmall;
+    if (form == kFew) return;
+    if (form == kWhole) {
+      til.init_sorted(p, 256);
+      wide = 256;
+      const Tail x = tail_of(p, til, (cols + 255) / 256, steps);
+      tiles = x.tiles;
+      splits = x.splits;
+      tall = x.tall;
+      begin = x.first;
+    } else {
+      til.init(p, 128);
+      tiles = til.total * ((cols + 127) / 128);
+      splits = split_of(p, tiles, steps).splits;
+    }
+    if (splits == 1) return;
   }
-  for (int t = blockIdx.x; t < units * tiles * 8; t += int(gridDim.x)) {
-    const int x = t >> 3, row = (t & 7) * 16 + int(threadIdx.x >> 4), col = int(threadIdx.x & 15) * 8;
-    int m, n, e, r0, rows, part, parts = sp.splits, first = x, stride = tiles;
+  const int mt = (rows_of + 127) / 128, nt = (cols + wide - 1) / wide;
+  const int across = wide / 8, parts_of = tall * across / 256;  // threads a row, workgroups a tile
+  for (int t = blockIdx.x; t < units * tiles * parts_of; t += int(gridDim.x)) {
+    const int x = t / parts_of;
+    const int row = (t - x * parts_of) * (256 / across) + int(threadIdx.x) / across, col = int(threadIdx.x) % across * 8;
+    int m, n, e, r0, rows, part, parts = splits;
     int64_t at;
     if (KIND == kMmWeights) {
       til.find(p, x / tiles, &e, &r0, &rows, &part, &parts);
@@ -289,16 +351,17 @@ __global__ __launch_bounds__(256) void k_mm_join(MmArgs p) {
       rows = p.n - m * 128;
       at = (int64_t(e) * p.n + m * 128 + row) * p.k;
     } else {
-      tile_of(x, til.total, nt, &m, &n);
+      tile_of(begin + x, til.total, nt, &m, &n);
       til.find(p, m, &e, &r0, &rows);
       at = int64_t(r0 + row) * p.ld_out;
     }
-    if (row >= rows || n * 128 + col >= cols) continue;
-    at += n * 128 + col;
-    const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.ws) + int64_t(first) * 4096 + row * 32 + col / 4;
+    if (row >= rows || n * wide + col >= cols) continue;
+    at += n * wide + col;
+    const f32x4_t* from = reinterpret_cast<const f32x4_t*>(p.ws) + (int64_t(x) * tall + row) * (wide / 4) + col / 4;
+    const int64_t stride = int64_t(tiles) * tall * (wide / 4);
     f32x4_t lo = from[0], hi = from[1];
     for (int s = 1; s < parts; ++s) {
-      from += int64_t(stride) * 4096;
+      from += stride;
       lo += from[0];
       hi += from[1];
     }
@@ -371,8 +434,8 @@ __global__ __launch_bounds__(kThr) void k_mm_tiles(MmArgs p, bool both) {
     walk_weights<TYPE, BK, 8, 8>(p);
   } else {
     RowTiles til;
-    if (both && form_of<KIND>(p, til) != kWhole) return;
-    til.init(p, 256, 0, both && p.groups <= 64);
+    if (both && form_of<KIND>(p, til, true) != kWhole) return;
+    til.init_sorted(p, 256, both && p.groups <= 64);
     walk_rows<KIND, TYPE, 8, 8>(p, til);
   }
 }
@@ -384,8 +447,8 @@ __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
   } else {
     RowTiles til;
     const bool look = both || KIND == kMmOut;
-    const Form form = look ? form_of<KIND>(p, til) : kSmall;
-    if (both && form == kWhole) return;
+    const Form form = look ? form_of<KIND>(p, til, both) : kSmall;
+    if (form == kWhole) return;
     const bool have = look && p.groups <= 64;
     if constexpr (KIND == kMmOut) {
       typedef RowsLds<KIND, 4, 4> LDS;
@@ -401,7 +464,7 @@ __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
   }
 }
 
-// (a.ws is set only where sums may be split, which is where small tiles make a round at most.)
+// (a.ws is set only where sums may be split.)
 // Which kernels are launched: whole tiles alone where there may be four rounds of them (buffers hold
 // about as many rows as are routed), small ones (and few rows) alone where these make a round at most,
 // otherwise both, one of which returns at once (2 us).  A product of weights has its tiles whatever
@@ -417,21 +480,22 @@ mok_status_t launch_tiles(const MmArgs& a, hipStream_t st) {
   };
   bool whole = tiles(256) >= 1024, small = tiles(128) <= 512;
   if (KIND == kMmWeights) {
-    whole = tiles(256) >= 256;
+    whole = tiles(256) >= 256 && tiles(128) > 256;  // (up to 256 small ones their sums may be split)
     small = !whole;
   }
   const bool both = !whole && !small;
+  const Launched what = whole ? kOnlyWhole : small ? kOnlySmall : kBoth;
   mok_status_t s = MOK_OK;
   auto go = [&](auto kern, int grid) { return launch(kern, dim3(grid), dim3(kThr), st, a, both); };
   if (!whole)
     s = a.type == MOK_TYPE_BF16 ? go(k_mm_small<KIND, MOK_TYPE_BF16, BK>, 512) : go(k_mm_small<KIND, MOK_TYPE_FP16, BK>, 512);
+  if (!small && s == MOK_OK)
+    s = a.type == MOK_TYPE_BF16 ? go(k_mm_tiles<KIND, MOK_TYPE_BF16, BK>, kRound) : go(k_mm_tiles<KIND, MOK_TYPE_FP16, BK>, kRound);
   if (a.ws && s == MOK_OK) {
     const dim3 grid(512), block(256);
-    s = a.type == MOK_TYPE_BF16 ? launch(k_mm_join<KIND, MOK_TYPE_BF16>, grid, block, st, a)
-                                : launch(k_mm_join<KIND, MOK_TYPE_FP16>, grid, block, st, a);
+    s = a.type == MOK_TYPE_BF16 ? launch(k_mm_join<KIND, MOK_TYPE_BF16>, grid, block, st, a, what)
+                                : launch(k_mm_join<KIND, MOK_TYPE_FP16>, grid, block, st, a, what);
   }
-  if (!small && s == MOK_OK)
-    s = a.type == MOK_TYPE_BF16 ? go(k_mm_tiles<KIND, MOK_TYPE_BF16, BK>, 256) : go(k_mm_tiles<KIND, MOK_TYPE_FP16, BK>, 256);
   return s;
 }
 

@@ -377,6 +377,11 @@ SPLITS = [  # rows an expert, n, k: long sums of few results
     ("weights", [5000], 136, 264), ("weights", [4000, 0, 1, 700], 72, 40), ("weights", [0, 2100], 264, 8),
     ("weights", [513, 1830, 64, 63], 136, 136), ("weights", [30] * 70, 40, 24), ("weights+", [3000, 0, 70], 136, 72),
     ("held", [5000], 136, 288), ("held", [4000, 0, 1, 700], 72, 32), ("held", [513, 1830, 64, 63], 264, 160),
+    ("weights", [6000] + [8] * 255, 128, 128),
+    # a last round of few whole tiles: short ones, of 108 and of 208 rows
+    ("out", [2053, 2030, 2048, 2061, 1999, 2001, 2077, 2040], 1024, 4104), ("out", [8300], 2040, 4096),
+    ("out", [8400], 2048, 4160), ("rows", [2053, 2030, 2048, 2061, 1999, 2001, 2077, 2040], 4104, 1024),
+    ("rows", [8300], 4096, 2040), ("rows", [0, 8400], 4160, 2048),
 ]
 
 

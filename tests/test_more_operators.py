@@ -138,7 +138,8 @@ def test_workspace_of_products():
     assert w(2, 16384, 1, 1024, 1024) == all_of  # 64 tiles of 256 steps
     assert w(2, 16384, 8, 4096, 7168) == w(2, 512, 1, 1024, 1024) == 0
     assert w(0, 2000, 1, 64, 8192) == w(1, 2000, 1, 8192, 64) == all_of
-    assert w(0, 2000, 1, 8192, 64) == w(1, 2000, 1, 64, 8192) == w(0, 16384, 8, 4096, 7168) == 0
+    assert w(0, 2000, 1, 8192, 64) == w(1, 2000, 1, 64, 8192) == w(0, 16384, 8, 7168, 2048) == 0
+    assert w(0, 16384, 8, 4096, 7168) == w(1, 16384, 8, 4096, 7168) == L.MOK_MM_WORKSPACE_BYTES  # a last round of few tiles
     for bad, code in (((3, 8, 1, 64, 64), L.MOK_E_UNSUPPORTED), ((0, -1, 1, 64, 64), L.MOK_E_SHAPE),
                       ((0, 8, 0, 64, 64), L.MOK_E_SHAPE), ((2, 8, 1, 60, 64), L.MOK_E_SHAPE)):
         with pytest.raises(L.MokError) as e:
