@@ -1,4 +1,8 @@
-// Grouped product of few 16-bit rows an expert (decoding): bound by reading the weights once.
+// Grouped product of few 16-bit rows an expert (decoding): bound by reading the weights once, or, where
+// there is little to read, by the launch and the latency of a wave's chunks, one pair after another.
+// MI355X, bf16: 64 rows of 8 experts, N 4096, K 7168 92 to 95 us (5.0 TB/s; 180 on tiles); one row of
+// one expert 18 us (58.7 MB: seven pairs of chunks a wave, 2.2 us each); 4 rows of 12, N 1000, K 520,
+// fp16 3.9 us, of which the launch is most.
 #pragma once
 #include "expert_rows.h"
 
