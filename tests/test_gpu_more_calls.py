@@ -348,6 +348,47 @@ def test_two_graphs_replayed_on_two_streams():
                 assert all(torch.equal(g, r) for g, r in zip(c.written(), w[n])), (turn, n)
 
 
+@pytest.mark.parametrize("forward", [True, False], ids=["out", "rows"])
+def test_a_captured_product_with_any_routing(forward):
+    """One capture at a share's buffer size, replayed with routings that ask for each form, for a last
+    round of few tiles split along the sum, and for nothing: as the eager call each time."""
+    rows, E, n, k = 16500, 8, *((1024, 4104) if forward else (4104, 1024))
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn(rows, k if forward else n, generator=gen, device=DEV).to(BF)
+    b = (torch.randn(E, n, k, generator=gen, device=DEV) * 0.05).to(BF)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    fn = ops.grouped_mm if forward else ops.grouped_mm_backward_rows
+    assert L.mok_grouped_mm_workspace(0 if forward else 1, rows, E, n, k) == L.MOK_MM_WORKSPACE_BYTES
+    out = torch.full((rows, n if forward else k), 7.0, dtype=BF, device=DEV)
+    fn(x, off, b, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fn(x, off, b, out=out)
+    for counts in ([2053, 2030, 2048, 2061, 1999, 2001, 2077, 2040], [1, 0, 3, 0, 0, 2, 1, 0], [0] * 8,
+                   [16500] + [0] * 7, [500, 530, 512, 498, 470, 513, 560, 500], [8300, 0, 0, 0, 0, 0, 0, 8200],
+                   [70, 40, 60, 33, 64, 90, 20, 1]):
+        say(f"[mm] captured {counts}")
+        at = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+        off.copy_(torch.from_numpy(at))
+        want = torch.full_like(out, 7.0)
+        fn(x, off, b, out=want)
+        for _ in range(2):
+            out.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want)
+        assert bool((want[int(at[-1]):] == 7.0).all())
+        # products of two bf16 values are exact in fp32; a sum of 4104 in any order is off by at most
+        # 4104 * 2^-24 (and 1/1000 of that) of the sum of magnitudes, here and in the plain form, and the
+        # result is then rounded by at most 2^-8 of itself
+        for e in range(E):
+            i, j = int(at[e]), int(at[e + 1])
+            v, w = x[i:j].float(), b[e].float().t() if forward else b[e].float()
+            plain, off_by = v @ w, 2 * 4104 * 1.001 * 2**-24 * (v.abs() @ w.abs())
+            assert bool(((want[i:j].float() - plain).abs() <= 2**-8 * (plain.abs() + off_by) + off_by).all())
+
+
 @pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
 def test_a_given_stream(raw):
     """Work goes to the stream that is given, a torch stream or its handle, behind what is on it."""
