@@ -192,6 +192,19 @@ def test_many_tiles():
     check(Case([1300, 0, 2100, 77, 640], 2088, 224, BF, seed=3, whole=True, held=True), "weights", F32, True)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=IDS)
+@pytest.mark.parametrize("held", [False, True], ids=["16", "held"])
+@pytest.mark.parametrize("counts,n,k", [([300], 4104, 4064), ([129, 0, 700], 2312, 2336), ([1] + [150] * 70, 520, 544)],
+                         ids=["1e", "3e", "71e"])
+def test_weights_gradient_in_whole_tiles(counts, n, k, held, dtype):
+    """More than 128 rows an expert and 256 tiles of 256 x 256."""
+    say(f"[mm] whole tiles {counts[:3]} n {n} k {k} held {held}")
+    assert sum(counts) > 128 * len(counts) and len(counts) * (-(-n // 256)) * (-(-k // 256)) >= 256
+    for kind, out_dtype in (("weights", dtype), ("weights+", F32)):
+        check(Case(counts, n, k, dtype, seed=31, whole=True, held=held), kind, out_dtype, True)
+    check(Case(counts, n, k, dtype, seed=32, held=held), "weights", F32, False)
+
+
 def test_more_than_64_experts_of_tiles():
     c = Case([130 + (7 * i) % 150 for i in range(100)], 136, 72, BF, seed=4, whole=True)
     for kind in ("out", "rows", "weights"):
