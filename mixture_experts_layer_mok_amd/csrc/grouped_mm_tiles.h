@@ -467,7 +467,7 @@ __global__ __launch_bounds__(kThr, 2) void k_mm_small(MmArgs p, bool both) {
 // (a.ws is set only where sums may be split.)
 // Which kernels are launched: whole tiles alone where there may be four rounds of them (buffers hold
 // about as many rows as are routed), small ones (and few rows) alone where these make a round at most,
-// otherwise both, one of which returns at once (2 us).  A product of weights has its tiles whatever
+// otherwise both, one of which returns at once (4 us).  A product of weights has its tiles whatever
 // the rows; with two steps an expert or fewer they are small ones, two of which a CU has in flight: what
 // counts is to write the results.  MI355X, us, into fp32, whole / small: 2 rows of 32 experts, N 3432,
 // K 128 17.6 / 13.1, 25 of 13, N 3048, K 400 20.3 / 17.6, 1000 of 8, N 2048, K 2048 32.6 / 28.9, N 4096,
