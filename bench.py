@@ -96,7 +96,7 @@ def log(msg):
 # What the layer's kernels are not compiled from: the operators beside it.
 OPERATOR_SOURCES = ("expert_rows.h", "gemm_16.h", "gemm_mx4.h", "grouped_mm.hip", "grouped_mm_few.h", "grouped_mm_held.hip",
                     "grouped_mm_out.hip", "grouped_mm_rows.hip",
-                    "grouped_mm_tiles.h", "grouped_mm_weights.hip", "grouped_mx4.hip", "mx4.hip", "mx8.hip",
+                    "grouped_mm_tiles.h", "grouped_mm_weights.hip", "grouped_mx4.hip", "mm_forms.h", "mx4.hip", "mx8.hip",
                     "ops_api.hip", "ops_launch.h", "rows.hip")
 
 

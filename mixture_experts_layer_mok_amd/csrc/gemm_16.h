@@ -50,7 +50,6 @@ namespace mok {
 namespace g16 {
 
 constexpr int kThr = 256;
-constexpr int kDeep = 64;                    // summed elements a step
 constexpr uint32_t kPast = 0x80000000u;      // added to an offset: out of every resource's range
 
 enum Kind { kAlong = 0, kAcross = 1, kHeld = 2 };

@@ -9,7 +9,6 @@
 namespace mok {
 namespace g16 {
 
-constexpr int kPassRows = 32;            // rows a pass
 constexpr int kWaves = 4;
 constexpr uint32_t kFewLds = kWaves * 2 * 4 * 64 * 16;  // bytes of s_part
 constexpr int kUnits = 16;               // 16-byte units of a row that a chunk holds: 128 elements

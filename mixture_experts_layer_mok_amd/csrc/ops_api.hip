@@ -106,7 +106,7 @@ mok_status_t check_mm(int32_t type, int32_t out_type, int64_t max_rows, int32_t 
 mok_status_t check_ws(MmKind kind, void** ws, size_t bytes, int64_t max_rows, int32_t groups, int32_t n, int32_t k) {
   if (*ws && bytes < MOK_MM_WORKSPACE_BYTES) return MOK_E_WORKSPACE;
   if (!aligned(*ws, 16)) return MOK_E_SHAPE;
-  if (!mm_may_split(kind, max_rows, groups, n, k)) *ws = nullptr;
+  if (!g16::may_split(kind, max_rows, groups, n, k)) *ws = nullptr;
   return MOK_OK;
 }
 // A row operand's stride in elements: rows of a tile stay within 31-bit byte offsets.
@@ -244,7 +244,7 @@ mok_status_t mok_grouped_mm_workspace(int32_t which, int64_t max_rows, int32_t g
   if (which < 0 || which > 2) return MOK_E_UNSUPPORTED;
   const mok_status_t s = check_mm(MOK_TYPE_BF16, MOK_TYPE_BF16, max_rows, groups, n, k);
   if (s != MOK_OK) return s;
-  *bytes = mm_may_split(MmKind(which), max_rows, groups, n, k) ? MOK_MM_WORKSPACE_BYTES : 0;
+  *bytes = g16::may_split(MmKind(which), max_rows, groups, n, k) ? MOK_MM_WORKSPACE_BYTES : 0;
   return MOK_OK;
 }
 

@@ -7,6 +7,7 @@
 #include <utility>
 
 #include "launch.h"
+#include "mm_forms.h"
 
 namespace mok {
 
@@ -81,11 +82,7 @@ struct GroupedArgs {
 };
 mok_status_t launch_grouped_mx4(const GroupedArgs& a, hipStream_t st);
 
-// Grouped product of 16-bit rows (grouped_mm.hip): C = A B summed over one axis.
-//   kMmOut      out[r, c]  = sum_i a[r, i] b[e][c, i]      left a, right b
-//   kMmRows     d_a[r, i]  = sum_c d_out[r, c] b[e][c, i]  left d_out, right b
-//   kMmWeights  d_b[e][c, i] = sum_r d_out[r, c] a[r, i]   left d_out, right a
-enum MmKind { kMmOut = 0, kMmRows = 1, kMmWeights = 2 };
+// Grouped product of 16-bit rows (grouped_mm.hip); kinds: mm_forms.h.
 struct MmArgs {
   int32_t type;
   const void* left;
@@ -102,8 +99,6 @@ struct MmArgs {
   int64_t ld_out;
   float* ws;  // MOK_MM_WORKSPACE_BYTES for partial sums, or null
 };
-// Whether a product's sums may be split over workgroups, given a workspace.
-bool mm_may_split(MmKind kind, int64_t max_rows, int32_t groups, int32_t n, int32_t k);
 mok_status_t launch_grouped_mm(MmKind kind, const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_out(const MmArgs& a, hipStream_t st);
 mok_status_t launch_mm_rows(const MmArgs& a, hipStream_t st);

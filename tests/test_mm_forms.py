@@ -1,0 +1,60 @@
+"""What the 16-bit grouped product answers to which form a call takes and how its sums are split.  The
+kernels that need an answer are compiled apart, so the answers may not depend on what a compiler makes of
+the arithmetic.  mm_forms_check.cpp computes them on the host."""
+import os
+import re
+import subprocess
+
+import pytest
+
+from mixture_experts_layer_mok_amd import build
+from tests.mm_forms import compiler, forms_of, program
+
+
+def test_answers_do_not_depend_on_contraction(tmp_path):
+    """The estimates, bit for bit, whether or not the compiler may fuse a multiplication and an addition
+    where no pragma forbids it (for device code hipcc may by itself)."""
+    said = []
+    for how in ("off", "fast-honor-pragmas"):
+        exe = program(tmp_path / how, "-mfma", f"-ffp-contract={how}")
+        said.append(subprocess.run([exe, "sweep"], check=True, capture_output=True, text=True).stdout.splitlines())
+    assert len(said[0]) > 100000
+    bad = [(a, b) for a, b in zip(*said) if a != b]
+    assert not bad and len(said[0]) == len(said[1]), bad[:4]
+
+
+def test_device_code_fuses_nothing(tmp_path):
+    """The kernels of one product as hipcc makes them: estimates are all that they compute on single
+    floats, and no instruction of theirs multiplies and adds at once."""
+    listing = str(tmp_path / "rows.s")
+    subprocess.run([build.hipcc(), *build.HIPCC_FLAGS, "--cuda-device-only", "-S",
+                    os.path.join(build.CSRC, "grouped_mm_rows.hip"), "-o", listing], check=True, capture_output=True)
+    text = open(listing).read()
+    assert len(re.findall(r"v_mul_f32", text)) > 20
+    assert not re.findall(r"\b[vs]_(?:pk_)?(?:fma|mad)\w*_f32", text)
+
+
+@pytest.mark.parametrize("kind,counts,n,k,want", [
+    # at most 11 m-tiles of 128 times 32: one round of small ones at most.  112 steps of 0.72 us and 4,
+    # less than 20.8 times the weights' 11.3
+    ("out", [64] * 8, 4096, 7168, "only_small small 1 128"),
+    ("out", [8] * 8, 4096, 7168, "only_small few 1 128"),
+    # 71 x 16 whole tiles at most; 64 x 16 of them are four full rounds, 68 x 16 those and 64, in four items each
+    ("out", [2048] * 8, 4096, 7168, "only_whole whole 1 256"),
+    ("out", [2053, 2030, 2048, 2061, 1999, 2001, 2077, 2040], 4096, 7168, "only_whole whole 4 64"),
+    # 2 x 56 small tiles, 64 steps: four items, 512 being the most
+    ("rows", [256], 4096, 7168, "only_small small 4 128"),
+    # 64 tiles of 256 steps: 512 items leave 7 units, of 37 steps
+    ("weights", [16384], 1024, 1024, "only_small small 7 128"),
+    ("weights", [2048] * 8, 4096, 7168, "only_whole whole 1 128"),
+])
+def test_known_answers(kind, counts, n, k, want):
+    assert forms_of([(kind, counts, sum(counts), n, k)]) == [want]
+
+
+def test_malformed_calls_are_refused():
+    exe = program(os.path.join(build.BUILD, "mm_forms_check"))
+    for line in ("", "0 1", "3 8 8 8 1 0 8", "0 8 8 8 1 0"):
+        assert subprocess.run([exe, "calls"], input=line + "\n", text=True, capture_output=True).returncode == 1
+    assert subprocess.run([exe], capture_output=True).returncode == 2
+    assert compiler()
