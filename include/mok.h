@@ -405,7 +405,8 @@ mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t l
  *
  * Common rules.  offsets [groups + 1] int32 stays on the device, as for mok_grouped_mx4:
  * expert e (of `groups`, 1..1024) has the rows [offsets[e], offsets[e+1]) cut to [0,
- * max_rows); ranges must not overlap; max_rows 0..2^24.  b [groups, n, k], contiguous.
+ * max_rows), none where that ends before it begins; ranges must not overlap; max_rows
+ * 0..2^24.  b [groups, n, k], contiguous.
  * n a multiple of 8, 8..2^20; k a multiple of 8, 8..65536; n * k below 2^31.  Row
  * operands have ld elements from row to row: a multiple of 8, at least the row's elements
  * and at most 2^21 (a read one may have ld 0: every row the same).  Bases 16-byte aligned,

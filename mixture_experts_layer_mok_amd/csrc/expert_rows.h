@@ -8,8 +8,7 @@ namespace g16 {
 
 // Rows of expert e, cut to [0, max_rows).
 __device__ __forceinline__ void expert_rows(const MmArgs& p, int e, int* lo, int* hi) {
-  *lo = max(p.offsets[e], 0);
-  *hi = int(min(int64_t(p.offsets[e + 1]), p.max_rows));
+  cut_rows(p.offsets[e], p.offsets[e + 1], p.max_rows, lo, hi);
 }
 
 // Sums of x over the lanes up to this one (gfx9 DPP: within rows of 16 lanes, then across them).

@@ -42,6 +42,13 @@ MOK_FORMS void tile_of(int t, int mt, int nt, int* m, int* n) {
   *m = g * kGroupM + r - *n * gm;
 }
 
+// The rows [from, to) of an expert, cut to [0, max_rows); none where hi <= lo.  Neither end is negative,
+// whatever the offsets are, so that hi - lo does not overflow.
+MOK_FORMS void cut_rows(int from, int to, int64_t max_rows, int* lo, int* hi) {
+  *lo = from > 0 ? from : 0;
+  *hi = to <= 0 ? 0 : to < max_rows ? to : int(max_rows);
+}
+
 // Sums split over workgroups: every tile is summed in `splits` items of `per` steps each, the partial
 // results go to the workspace, 64 KB an item, and k_mm_join adds them up in order.  As many items as
 // take the least by estimate, in microseconds: 0.72 a step where a CU has one item at most, 0.95 with

@@ -5,6 +5,7 @@
 //                          (tall 128: all of them; else those of the last round) are summed in, 1 if
 //                          they are not split.  The kernels count an expert's tiles with a wave; here they are
 //                          counted one after another.
+//   mm_forms_check rows    for every line "max_rows from to": the ends of an expert's rows
 #include <algorithm>
 #include <cstdio>
 #include <cstring>
@@ -70,8 +71,9 @@ static int one(const std::string& line) {
   const Launched what = launched(MmKind(kind), max_rows, groups, n, k);
   std::vector<int> rows;
   for (int e = 0; e < groups; ++e) {
-    const int64_t lo = std::max(off[e], 0), hi = std::max<int64_t>(std::min<int64_t>(off[e + 1], max_rows), 0);
-    rows.push_back(int(std::max<int64_t>(hi - lo, 0)));
+    int lo, hi;
+    cut_rows(off[e], off[e + 1], max_rows, &lo, &hi);
+    rows.push_back(std::max(hi - lo, 0));
   }
   auto tiles = [&](int tall) {
     int t = 0;
@@ -122,6 +124,14 @@ static int one(const std::string& line) {
 int main(int argc, char** argv) {
   if (argc == 2 && !std::strcmp(argv[1], "sweep")) {
     sweep();
+    return 0;
+  }
+  if (argc == 2 && !std::strcmp(argv[1], "rows")) {
+    int64_t max_rows;
+    for (int from, to, lo, hi; std::cin >> max_rows >> from >> to;) {
+      cut_rows(from, to, max_rows, &lo, &hi);
+      std::printf("%d %d\n", lo, hi);
+    }
     return 0;
   }
   if (argc != 2 || std::strcmp(argv[1], "calls")) return 2;

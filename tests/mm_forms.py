@@ -21,14 +21,37 @@ def program(exe, *flags):
     return exe
 
 
+def answers(what, lines):
+    exe = program(os.path.join(build.BUILD, "mm_forms_check"))
+    return subprocess.run([exe, what], input="\n".join(" ".join(map(str, v)) for v in lines) + "\n", check=True,
+                          capture_output=True, text=True).stdout.splitlines()
+
+
+def offsets_of(counts):
+    off = [0]
+    for c in counts:
+        off.append(off[-1] + c)
+    return off
+
+
 def forms_of(calls, ws=True):
     """calls: (kind, rows an expert, max_rows, n, k) each; "launched form parts tall" each."""
-    lines = []
-    for kind, counts, max_rows, n, k in calls:
-        off = [0]
-        for c in counts:
-            off.append(off[-1] + c)
-        lines.append(" ".join(map(str, [KINDS[kind], max_rows, n, k, int(ws), *off])))
-    exe = program(os.path.join(build.BUILD, "mm_forms_check"))
-    return subprocess.run([exe, "calls"], input="\n".join(lines) + "\n", check=True, capture_output=True,
-                          text=True).stdout.splitlines()
+    return answers("calls", [[KINDS[kind], max_rows, n, k, int(ws), *offsets_of(counts)]
+                             for kind, counts, max_rows, n, k in calls])
+
+
+# Offsets whose ranges end before they begin, as far apart as 32 bits allow: what the call has, the offsets
+# in the place of its own, n, k, and what computes it.
+LEAST, MOST = -2**31, 2**31 - 1
+FAR_OFFSETS = [
+    ("out", [MOST, LEAST, 0, 40, 60], 72, 136, "only_small few 1 128"),
+    ("out", [0, 2000, LEAST], 1032, 520, "only_small small 1 128"),
+    ("out", [0, 8400, LEAST], 2048, 4160, "both whole 8 256"),
+    ("rows", [MOST, LEAST, 0, 40, 60], 72, 136, "only_small small 1 128"),
+    ("rows", [0, 8400, LEAST], 4160, 2048, "both whole 8 256"),
+    ("weights", [MOST, LEAST, 0, 40, 60], 72, 136, "only_small small 1 128"),
+    ("weights", [0, 5000, LEAST], 136, 264, "only_small small 8 128"),
+    ("weights", [0, 400, LEAST], 4104, 4064, "only_whole whole 1 128"),
+    ("held", [MOST, LEAST, 0, 40, 60], 72, 160, "only_small small 1 128"),
+    ("held", [0, 400, LEAST], 4104, 4064, "only_whole whole 1 128"),
+]

@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 from mixture_experts_layer_mok_amd import build
-from tests.mm_forms import compiler, forms_of, program
+from tests.mm_forms import FAR_OFFSETS, KINDS, LEAST, MOST, answers, compiler, forms_of, program
 
 
 def test_answers_do_not_depend_on_contraction(tmp_path):
@@ -58,3 +58,20 @@ def test_malformed_calls_are_refused():
         assert subprocess.run([exe, "calls"], input=line + "\n", text=True, capture_output=True).returncode == 1
     assert subprocess.run([exe], capture_output=True).returncode == 2
     assert compiler()
+
+
+def test_rows_of_any_offsets():
+    """An expert's rows lie in the matrix, and their number in 32 bits, whatever the offsets are."""
+    ends = [LEAST, LEAST + 1, -1, 0, 1, 7, 2**24, 2**24 + 1, MOST - 1, MOST]
+    lines = [(top, a, b) for top in (0, 1, 7, 2**24) for a in ends for b in ends]
+    for (top, a, b), got in zip(lines, answers("rows", lines)):
+        lo, hi = map(int, got.split())
+        assert 0 <= lo <= MOST and 0 <= hi <= top
+        assert list(range(lo, min(hi, lo + 9))) == list(range(max(a, 0), min(b, top, max(a, 0) + 9))), (top, a, b)
+        assert max(hi - lo, 0) == max(min(b, top) - max(a, 0), 0)
+
+
+def test_calls_with_far_offsets_reach_every_form():
+    """(Run on a GPU by test_gpu_grouped_mm_forms.py; five rows belong to nobody.)"""
+    lines = [(KINDS[kind], max(o for o in off if o < MOST) + 5, n, k, 1, *off) for kind, off, n, k, _ in FAR_OFFSETS]
+    assert answers("calls", lines) == [c[-1] for c in FAR_OFFSETS]
