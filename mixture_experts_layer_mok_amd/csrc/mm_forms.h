@@ -216,7 +216,10 @@ inline bool may_split(MmKind kind, int64_t max_rows, int32_t groups, int32_t n, 
   const int64_t tiles = tiles_at_most(kind, max_rows, groups, n, k, 128);
   if (kind == kMmWeights) return tiles <= 256 && max_rows >= 2048;
   const int32_t deep = kind == kMmOut ? k : n;
-  return (tiles <= 256 && deep >= 1536) || (tiles > 512 && deep >= 4096);
+  if (tiles <= 256) return deep >= 1536;
+  // (with more experts than a wave has lanes the tiles of few rows do not come last, and no round of
+  // whole tiles is split)
+  return tiles > 512 && deep >= 4096 && (groups <= 64 || launched(kind, max_rows, groups, n, k) == kBoth);
 }
 
 }  // namespace g16

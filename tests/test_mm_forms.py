@@ -7,6 +7,7 @@ import subprocess
 
 import pytest
 
+from mixture_experts_layer_mok_amd import _lib as L
 from mixture_experts_layer_mok_amd import build
 from tests.mm_forms import FAR_OFFSETS, KINDS, LEAST, MOST, answers, compiler, forms_of, program
 
@@ -75,3 +76,15 @@ def test_calls_with_far_offsets_reach_every_form():
     """(Run on a GPU by test_gpu_grouped_mm_forms.py; five rows belong to nobody.)"""
     lines = [(KINDS[kind], max(o for o in off if o < MOST) + 5, n, k, 1, *off) for kind, off, n, k, _ in FAR_OFFSETS]
     assert answers("calls", lines) == [c[-1] for c in FAR_OFFSETS]
+
+
+@pytest.mark.parametrize("which,n,k", [(0, 2048, 4096), (1, 4096, 2048)])
+def test_workspace_of_many_experts(which, n, k):
+    """Whole tiles are split with at most 64 experts: with more, a call that launches nothing else has no
+    use for a workspace; where the small tiles may run they may be split."""
+    kind = ("out", "rows")[which]
+    for groups, rows, launch, ws in ((64, 256 * 128, "only_whole", True), (65, 256 * 128, "only_whole", False),
+                                     (1024, 256 * 128, "only_whole", False), (65, 4096, "both", True),
+                                     (65, 30, "only_small", False)):
+        assert forms_of([(kind, [1] * groups, rows, n, k)])[0].split()[0] == launch, (groups, rows)
+        assert L.mok_grouped_mm_workspace(which, rows, groups, n, k) == ws * L.MOK_MM_WORKSPACE_BYTES, (groups, rows)
