@@ -450,7 +450,9 @@ mok_status_t mok_grouped_mm_bwd_rows(int32_t type, const void* d_out, int64_t ld
  * [max_rows, k] of ld_a bytes from row to row (a multiple of 16) with scales
  * [max_rows, k / 32] of ld_a_scales bytes (at least k / 32, at most 2^21), as
  * mok_quantize_mx8 writes them, k a multiple of 32; a value enters the product in
- * `type` (rounded to nearest even where its range needs it; NaN for the blocks of scale 255). */
+ * `type` (rounded to nearest even where its range needs it; NaN for the blocks of scale 255).
+ * In fp16 a held 65,536 enters as 65,504, the largest there is (fp16 magnitudes of 63,488 and
+ * more are held so), and what is larger as infinity. */
 mok_status_t mok_grouped_mm_bwd_weights(int32_t type, const void* d_out, int64_t ld_d_out,
                                         const void* a, int64_t ld_a, const uint8_t* a_scales,
                                         int64_t ld_a_scales, int64_t max_rows,
@@ -477,7 +479,8 @@ mok_status_t mok_quantize_mx8(int32_t type, const void* src, int64_t ld_src, int
                               int64_t ld_scales, void* stream);
 
 /* The values back: dst = code * 2^(scale - 127) in `type` (rounded to nearest even where
- * its range needs it; NaN for the blocks of scale 255). */
+ * its range needs it; NaN for the blocks of scale 255).  What that rounds past the type's
+ * range is infinite: in fp16 the 65,536 that magnitudes of 63,488 and more are held as. */
 mok_status_t mok_dequantize_mx8(const uint8_t* codes, int64_t ld_codes, const uint8_t* scales,
                                 int64_t ld_scales, int64_t rows, int32_t cols, int32_t type,
                                 void* dst, int64_t ld_dst, void* stream);

@@ -177,15 +177,36 @@ struct Operand {
   }
 };
 
+// Finite fp16 rows are held as up to 65,536 (63,488 and more: code 256 at scale byte 135), which fp16 does
+// not have: it becomes 65,504, off by half a step.  So from that scale byte on (with END; without, it
+// becomes infinite) half the value is converted, y, which is exact where the whole is finite, and y and
+// the nearest to it of +-32,736 are added: twice y up to 61,440, 65,504 for y = 32,768, infinite above,
+// where y is at least 36,864.  At smaller scale bytes the whole is converted and 0 added.  (The bounds as
+// integers, whose order is that of the magnitudes of either sign: as floats an instruction more
+// quiets NaNs, which y keeps.)
+constexpr uint32_t kEndOfFp16 = 135;
+// What a unit's conversion takes of its scale byte: a float of which the instructions read the exponent
+// alone (0 stands for 2^-127, 255 for NaN), and with END below it the bits of 32,736 in fp16, or 0.
+template <bool END>
+__device__ __forceinline__ uint32_t held_scale(uint32_t scale) {
+  const bool half = END && scale >= kEndOfFp16 && scale != 255;
+  return ((scale - half) << 23) | (half ? 0x77FEu : 0u);
+}
 // Two e4m3 codes (the low or the high half of c) times 2^(scale byte - 127) in the product's type.
-// The instruction reads the exponent of `scale` alone: 0 stands for 2^-127, 255 for NaN.
-template <int TYPE, bool HIGH>
+template <int TYPE, bool HIGH, bool END>
 __device__ __forceinline__ uint32_t held2(uint32_t c, uint32_t scale) {
-  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
-  const float f = __uint_as_float(scale << 23);
+  const float f = __uint_as_float(scale);
   if (TYPE == MOK_TYPE_BF16)
     return __builtin_bit_cast(uint32_t, bf16x2_t(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, f, HIGH)));
-  return __builtin_bit_cast(uint32_t, f16x2_t(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, f, HIGH)));
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  typedef int16_t i16x2_t __attribute__((ext_vector_type(2)));
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  const f16x2_t y = f16x2_t(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, f, HIGH));
+  if (!END) return __builtin_bit_cast(uint32_t, y);
+  const uint16_t top = uint16_t(scale), bottom = uint16_t(scale | 0x8000u);
+  const i16x2_t at_most = __builtin_elementwise_min(__builtin_bit_cast(i16x2_t, y), i16x2_t{int16_t(top), int16_t(top)});
+  const u16x2_t near = __builtin_elementwise_min(__builtin_bit_cast(u16x2_t, at_most), u16x2_t{bottom, bottom});
+  return __builtin_bit_cast(uint32_t, f16x2_t(y + __builtin_bit_cast(f16x2_t, near)));
 }
 
 // An operand across the sum held in 8 bits, of 32 NB columns.  A lane takes 16 codes at a time, a
@@ -241,8 +262,15 @@ struct Held {
     if (x & 1) s[u] = uint32_t(uint8_t(__builtin_amdgcn_raw_buffer_load_b8(rs, offs[u] | past, 0, 0)));
     else q[u] = buf_ld16<kCpolPlain>(rc, off[u] | past);
   }
+  // Whether a lane of the wave holds scales at the end of fp16's range.
+  __device__ __forceinline__ bool at_the_end() const {
+    uint32_t m = s[0];
+#pragma unroll
+    for (int v = 1; v < kUnits; ++v) m = max(m, s[v]);
+    return __builtin_amdgcn_ballot_w64(m >= kEndOfFp16) != 0;
+  }
   // Piece o of the conversion into the stage at LDS address `to`.
-  template <int O>
+  template <int O, bool END>
   __device__ __forceinline__ void convert(uint32_t to) {
     constexpr int u = O / 6, x = O % 6, w = x < 3 ? x : x - 1;
     if constexpr (O == 0) {
@@ -257,9 +285,10 @@ struct Held {
       const uint32_t place = to + Op::place_of(4 * (64 / kLanes) / Op::kRows) * u + lane_place() + uint32_t(b ^ y) * 32;
       *reinterpret_cast<lds_w16*>(uintptr_t(place + (x == 5 ? 16 : 0))) = half;
     } else {
+      const uint32_t scale = held_scale<END>(s[u]);
       const uint32_t c = w == 0 ? q[u].x : w == 1 ? q[u].y : w == 2 ? q[u].z : q[u].w;
-      half[2 * (w & 1)] = held2<TYPE, false>(c, s[u]);
-      half[2 * (w & 1) + 1] = held2<TYPE, true>(c, s[u]);
+      half[2 * (w & 1)] = held2<TYPE, false, END>(c, scale);
+      half[2 * (w & 1) + 1] = held2<TYPE, true, END>(c, scale);
     }
   }
   // LDS byte, in its stage, of the element that this lane has of unit 0.
@@ -446,8 +475,8 @@ struct Tile {
     }
     if constexpr (kHolds) {
       if constexpr (H == 0) {  // the next step's elements, into its stage
-        convert<convert_before(M)>(b, LDS::b() + (LDS::kB - wb),
-                                   std::make_integer_sequence<int, convert_before(M + 1) - convert_before(M)>());
+        convert<convert_before(M), false>(b, LDS::b() + (LDS::kB - wb),
+                                          std::make_integer_sequence<int, convert_before(M + 1) - convert_before(M)>());
       } else {  // the codes of the step after
 #pragma unroll
         for (int x = held_before(kM + M); x < held_before(kM + M + 1); ++x) b.load(x);
@@ -462,9 +491,18 @@ struct Tile {
       else b.load(q - IB, LDS::b() + wb);
     }
   }
-  template <int O, int... X>
+  template <int O, bool END, int... X>
   static __device__ __forceinline__ void convert(B& b, uint32_t to, std::integer_sequence<int, X...>) {
-    (b.template convert<O + X>(to), ...);
+    (b.template convert<O + X, END>(to), ...);
+  }
+  // The conversion of a step again, where a lane has values at the end of fp16's range.  MI355X, 16,384 rows
+  // of 8 experts, N 4096, K 7168, us: 769 where no lane has them (760 without the question), 906 where
+  // all have; with END in the conversion between the MFMAs 836 for every step.  (A branch that holds
+  // MFMAs makes the compiler move the sums; this one leaves them where they are.)
+  static __device__ __forceinline__ void convert_end(B& b, uint32_t to) {
+    if constexpr (kHolds && TYPE == MOK_TYPE_FP16) {
+      if (b.at_the_end()) convert<0, true>(b, to, std::make_integer_sequence<int, 3 * JB>());
+    }
   }
   template <int H, int... M>
   __device__ __forceinline__ void half(const A& a, B& b, const Frag& f, Frag& fr, const FragAt<AK, IB>& ra,
@@ -516,7 +554,8 @@ struct Tile {
       for (int j = 0; j < JB; ++j) asm volatile("" : "+a"(acc[i][j]));
     wait_all_but(stores);  // steps 0 and 1
     if constexpr (kHolds) {
-      convert<0>(b, LDS::b(), std::make_integer_sequence<int, 3 * JB>());
+      convert<0, false>(b, LDS::b(), std::make_integer_sequence<int, 3 * JB>());
+      convert_end(b, LDS::b());
 #pragma unroll
       for (int x = 0; x < kHeldLoads; ++x) b.load(x);
       b.next();
@@ -532,6 +571,7 @@ struct Tile {
     FragAt<BK, JB> nb = fb.in(0);
     for (int ks = 0; ks < steps; ++ks) {
       half<0>(a, b, f0, f1, na, nb, ca, cb, std::make_integer_sequence<int, kM>());
+      convert_end(b, LDS::b() + (LDS::kB - cb));
       na = fa.in(LDS::kA - ca);
       nb = fb.in(LDS::kB - cb);
       half<1>(a, b, f1, f0, na, nb, ca, cb, std::make_integer_sequence<int, kM>());

@@ -55,3 +55,10 @@ FAR_OFFSETS = [
     ("held", [MOST, LEAST, 0, 40, 60], 72, 160, "only_small small 1 128"),
     ("held", [0, 400, LEAST], 4104, 4064, "only_whole whole 1 128"),
 ]
+
+# Rows of one expert, held in 8 bits, n, k, and what computes their weights' gradient.
+HELD_FP16 = [
+    (37, 72, 96, "only_small small 1 128"),
+    (2500, 72, 64, "only_small small 5 128"),
+    (300, 4104, 4064, "only_whole whole 1 128"),
+]

@@ -9,7 +9,7 @@ import pytest
 
 from mixture_experts_layer_mok_amd import _lib as L
 from mixture_experts_layer_mok_amd import build
-from tests.mm_forms import FAR_OFFSETS, KINDS, LEAST, MOST, answers, compiler, forms_of, program
+from tests.mm_forms import FAR_OFFSETS, HELD_FP16, KINDS, LEAST, MOST, answers, compiler, forms_of, program
 
 
 def test_answers_do_not_depend_on_contraction(tmp_path):
@@ -88,3 +88,8 @@ def test_workspace_of_many_experts(which, n, k):
                                      (65, 30, "only_small", False)):
         assert forms_of([(kind, [1] * groups, rows, n, k)])[0].split()[0] == launch, (groups, rows)
         assert L.mok_grouped_mm_workspace(which, rows, groups, n, k) == ws * L.MOK_MM_WORKSPACE_BYTES, (groups, rows)
+
+
+def test_held_fp16_cases_reach_every_form():
+    """(Run on a GPU by test_gpu_held_fp16.py.)"""
+    assert forms_of([("held", [rows], rows, n, k) for rows, n, k, _ in HELD_FP16]) == [c[-1] for c in HELD_FP16]
