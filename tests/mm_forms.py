@@ -5,7 +5,7 @@ import subprocess
 
 from mixture_experts_layer_mok_amd import build
 
-KINDS = {"out": 0, "rows": 1, "weights": 2, "weights+": 2, "held": 2}
+KINDS = {"out": 0, "rows": 1, "weights": 2, "weights+": 2, "held": 2, "held+": 2}
 
 
 def compiler():
@@ -62,3 +62,69 @@ HELD_FP16 = [
     (2500, 72, 64, "only_small small 5 128"),
     (300, 4104, 4064, "only_whole whole 1 128"),
 ]
+
+# Cases of the three products by the form that computes them: kind, rows an expert, n, k, form.  An expert
+# of many rows decides the form, the other has the count or the depth that is looked at.
+ROWS = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 192, 193, 255, 256, 257, 511, 513]
+DEPTHS = [8, 16, 24, 56, 64, 72, 120, 128, 136, 184, 192, 200, 256, 264, 504, 520, 1032, 4104]
+SHORT = [8, 56, 64, 72, 128, 136, 192, 200, 520]
+SIXTY = [257 + i * 37 % 200 - 100 * (i % 5 == 0) for i in range(60)]
+EIGHTY = [257 + i * 53 % 90 for i in range(78)] + [0, 3]
+
+
+def form_cases():
+    small, whole = "only_small small 1 128", "both whole 1 256"
+    alone = "only_whole whole 1 256"
+    c = []
+    for r in ROWS:
+        c.append(("out", [r, 2000], 1032, 520, small))
+        c.append(("out", [r, 4200], 2040, 1032, whole))
+        c.append(("rows", [4200, r], 1032, 2040, whole))
+    for d in DEPTHS:
+        c.append(("out", [90, 3000], 1032, d, small))
+    for d in SHORT:
+        c.append(("out", SIXTY, 2064, d, alone))
+        c.append(("rows", SIXTY, d, 2064, alone))
+        c.append(("out", EIGHTY, 2056, d, alone))
+        c.append(("rows", EIGHTY, d, 2056, alone))
+    # ends of the columns
+    for cols in (2056, 2112, 2176, 2240, 2296):
+        c.append(("out", SIXTY, cols, 72, alone))
+        c.append(("rows", SIXTY, 72, cols, alone))
+        c.append(("out", [100, 2900], cols // 2 - cols // 2 % 8, 200, small))
+    # sums that are split, with more than 64 experts and with fewer; parts of 64, 128 and 256 rows
+    c += [
+        ("out", [100 + i % 9 for i in range(70)], 128, 4104, "only_small small 4 128"),
+        ("rows", [100 + i % 9 for i in range(70)], 4104, 128, "only_small small 4 128"),
+        ("rows", [3 * (i % 7) for i in range(70)], 8200, 136, "only_small small 4 128"),
+        ("out", [600, 700], 264, 4104, "only_small small 4 128"),
+        ("rows", [1, 200, 0, 77], 8200, 72, "only_small small 15 128"),
+        ("out", [2053, 2030, 2048, 2061, 1999, 2001, 2077, 2040], 1024, 4104, "both whole 8 64"),
+        ("rows", [2053, 2030, 2048, 2061, 1999, 2001, 2077, 2040], 4104, 1024, "both whole 8 64"),
+        ("out", [8300], 2040, 4096, "both whole 8 128"),
+        ("rows", [8300], 4096, 2040, "both whole 8 128"),
+        ("out", [8400], 2048, 4160, "both whole 8 256"),
+        ("rows", [0, 8400], 4160, 2048, "both whole 8 256"),
+    ]
+    # gradients of the weights, added to what is there, from 16 and from 8 bits
+    for kind in ("weights+", "held+"):
+        c += [
+            (kind, [40, 0, 300], 136, 96, small),
+            (kind, [5000, 1, 70], 136, 160, "only_small small 10 128"),
+            (kind, [300, 1, 0], 2312, 2336, "only_small small 1 128"),
+            (kind, [129, 0, 700], 2312, 2336, "only_whole whole 1 128"),
+            (kind, [600, 20], 4104, 2080, "only_whole whole 1 128"),
+            (kind, [130 + i % 3 for i in range(70)], 520, 544, "only_whole whole 1 128"),
+        ]
+    return c
+
+# The same with rows 2^21 elements apart.
+FAR_ROWS = [
+    ("out", [300], 131080, 72, "only_whole whole 1 256"),
+    ("rows", [300, 500], 72, 65536, "only_whole whole 1 256"),
+    ("weights", [300], 4104, 4064, "only_whole whole 1 128"),
+]
+
+
+def short(v):
+    return str(v)[:32].replace(" ", "").replace(str(MOST), "most").replace(str(LEAST), "least")

@@ -9,7 +9,8 @@ import pytest
 
 from mixture_experts_layer_mok_amd import _lib as L
 from mixture_experts_layer_mok_amd import build
-from tests.mm_forms import FAR_OFFSETS, HELD_FP16, KINDS, LEAST, MOST, answers, compiler, forms_of, program
+from tests.mm_forms import (FAR_OFFSETS, FAR_ROWS, HELD_FP16, KINDS, LEAST, MOST, answers, compiler, form_cases,
+                            forms_of, program)
 
 
 def test_answers_do_not_depend_on_contraction(tmp_path):
@@ -93,3 +94,13 @@ def test_workspace_of_many_experts(which, n, k):
 def test_held_fp16_cases_reach_every_form():
     """(Run on a GPU by test_gpu_held_fp16.py.)"""
     assert forms_of([("held", [rows], rows, n, k) for rows, n, k, _ in HELD_FP16]) == [c[-1] for c in HELD_FP16]
+
+
+def test_cases_take_the_forms_they_are_named_for():
+    """(Run on a GPU by test_gpu_grouped_mm_forms.py, with five rows more than are routed.)"""
+    cases = form_cases()
+    got = forms_of([(kind, counts, sum(counts) + 5, n, k) for kind, counts, n, k, _ in cases])
+    assert not [(c, g) for c, g in zip(cases, got) if c[-1] != g]
+    assert len({(c[0], c[-1]) for c in cases}) >= 20
+    assert forms_of([(kind, counts, sum(counts) + 5, n, k) for kind, counts, n, k, _ in FAR_ROWS]) == \
+        [c[-1] for c in FAR_ROWS]
