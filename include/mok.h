@@ -416,7 +416,9 @@ mok_status_t mok_grouped_mx4(int32_t a_format, const uint8_t* a_codes, int64_t l
  * call alone until its work is done.  With it long sums of few results are split over
  * workgroups (one expert of 16384 rows, n 1024, k 1024: the weights' gradient takes 0.17 ms
  * without), and so is the last round of few tiles of long sums; mok_grouped_mm_workspace
- * says where that may be.  Errors: MOK_E_NULL,
+ * says where that may be.  The routed rows choose the form on the device, but max_rows
+ * which kernels are launched at all: a matrix much taller than the rows that are routed may
+ * cost a call of few rows up to two thirds more time.  Errors: MOK_E_NULL,
  * MOK_E_SHAPE, MOK_E_UNSUPPORTED (types), MOK_E_WORKSPACE, MOK_E_LAUNCH.  Asynchronous on
  * stream, kernel launches only; fixed-order sums, bitwise repeatable for the same arguments
  * (with and without a workspace the order may differ). */
@@ -489,7 +491,8 @@ mok_status_t mok_dequantize_mx8(const uint8_t* codes, int64_t ld_codes, const ui
  * values b (inter a multiple of 32, 32..32768).  h [rows, inter] = silu(a) * b, in fp32 and
  * rounded once; codes [rows, 2 * inter] and scales [rows, inter / 16] hold ab as
  * mok_quantize_mx8 does.  offsets [groups + 1] (groups 1..1024) as the schedule has them:
- * only rows below offsets[groups] are read and written; NULL: all rows. */
+ * only rows below offsets[groups] are read and written; NULL: all rows.  In the 16-bit types an
+ * e^-|a| below 2^-126 (|a| above 87.3) counts as 0, here and backward: silu(a) is 0 below -87.3. */
 mok_status_t mok_swiglu_mx8(int32_t type, const void* ab, int64_t ld_ab, int64_t rows,
                             int32_t inter, const int32_t* offsets, int32_t groups, void* h,
                             int64_t ld_h, uint8_t* codes, int64_t ld_codes, uint8_t* scales,

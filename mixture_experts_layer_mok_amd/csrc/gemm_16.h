@@ -35,13 +35,17 @@
 // of 128 x 128 leave each SIMD one wave, whose sums fill the 256 accumulation registers and whose
 // fragments of two slices fit beside its loads' offsets; half the tile has the same latency a step and
 // half the work.  Bound by the matrix cores and the clock that the card's power allows under them.
-// MI355X, bf16, 8 experts of 2048 rows, in a loop, us (and a library product of one expert with all
-// the rows):
-//   N 4096, K 7168  forward 681 (739)  rows' gradient 714 (842)  weights' gradient 804 (1108)
-//   N 7168, K 2048  forward 376        rows' gradient 353        weights' gradient 414
-// 681 is 1412 TFLOP/s.  Counters with uneven experts: matrix cores busy 66% of the time forward, 63%
-// rows' gradient, 58% weights' gradient, at 2.0 GHz of 2.4; waits for loads and barriers 12 to 13%,
-// LDS bank conflicts below 1%.
+// MI355X, bf16, 8 experts of 2048 rows, in loops one after another on one card, us (and a library product
+// of the same kind, of one expert with all the rows, into bf16):
+//   N 4096, K 7168  forward 691 (613 to 629)  rows' gradient 718 (728 to 731)  weights' gradient 798 (986)
+//   N 7168, K 2048  forward 375 (333)         rows' gradient 365 (363 to 365)  weights' gradient 419 (547)
+// (the weights' into fp32; into bf16 752 to 759 and 392).  691 is 1393 TFLOP/s.  Counters with uneven experts:
+// matrix cores busy 66% of the time forward, 63% rows' gradient, 58% weights' gradient, at 2.0 GHz of 2.4;
+// waits for loads and barriers 12 to 13%, LDS bank conflicts below 1%.
+//
+// Known to be slow: results added to what is there (store() with ADD).  Every 16 bytes are a load, a wait for
+// it and a store, 64 times a whole tile: the weights' gradients above take 1210 and 619 so, and 1000 rows of
+// 8 experts, N 4096, K 7168 505 where 180 do without.
 #pragma once
 #include "ops_launch.h"
 #include "gemm_mx4.h"

@@ -188,13 +188,18 @@ MOK_FORMS Form form_of(MmKind kind, const Counts& c, int n, int k, bool may_spli
   return us_small < us_whole ? kSmall : kWhole;
 }
 
-// Which kernels are launched: whole tiles alone where there may be four rounds of them (buffers hold
-// about as many rows as are routed), small ones (and few rows) alone where these make a round at most,
-// otherwise both, one of which returns at once (4 us).  A product of weights has its tiles whatever
-// the rows; with two steps an expert or fewer they are small ones, two of which a CU has in flight: what
-// counts is to write the results.  MI355X, us, into fp32, whole / small: 2 rows of 32 experts, N 3432,
-// K 128 17.6 / 13.1, 25 of 13, N 3048, K 400 20.3 / 17.6, 1000 of 8, N 2048, K 2048 32.6 / 28.9, N 4096,
-// K 7168 188 / 183; with four steps 2000 of 8, N 4096, K 2048 65.8 / 68.1, with eight 94.5 / 114.
+// Which kernels are launched, by the rows that there may be: whole tiles alone where that is four rounds of
+// them (buffers hold about as many rows as are routed), small ones (and few rows) alone where these make a
+// round at most, otherwise both, one of which returns at once (4 us).  In a buffer that is mostly empty
+// whole tiles alone have few rows too; MI355X, forward and rows' gradient, us, of 16,384 rows / of as many
+// as are routed: N 4096, K 7168, 64 rows of one expert 22, 23 / 23, 19, 256 rows 36, 37 / 30, 29, 512 rows
+// of eight 95, 84 / 97, 99 (their one round is split); N 7168, K 2048 (short sums are not split) 64 rows of
+// one expert 22, 25 / 17, 18, 256 rows 41, 29 / 25, 23, 512 rows of eight 37, 54 / 39, 52.
+// A product of weights has its tiles whatever the rows; with two steps an expert or fewer they are small
+// ones, two of which a CU has in flight: what counts is to write the results.  MI355X, us, into fp32,
+// whole / small: 2 rows of 32 experts, N 3432, K 128 17.6 / 13.1, 25 of 13, N 3048, K 400 20.3 / 17.6, 1000
+// of 8, N 2048, K 2048 32.6 / 28.9, N 4096, K 7168 188 / 183; with four steps 2000 of 8, N 4096, K 2048
+// 65.8 / 68.1, with eight 94.5 / 114.
 enum Launched { kOnlySmall, kOnlyWhole, kBoth };
 // Tiles of `tall` x `tall` that a call may have: an expert's rows may start a tile of their own.
 inline int64_t tiles_at_most(MmKind kind, int64_t max_rows, int64_t groups, int64_t n, int64_t k, int64_t tall) {

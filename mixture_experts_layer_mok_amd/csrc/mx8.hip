@@ -3,9 +3,10 @@
 // of 32 along a row, one e8m0 scale each; the shared exponent is the smallest n with
 // amax * 2^-n <= 448 (mx_shared_exp); the codes come from gfx950's conversions, which divide by a
 // power-of-two scale and round to nearest even, and nothing saturates.  All are bound by HBM: one pass,
-// 16 bytes of values a lane, no LDS.  MI355X, 16,384 rows, bf16 (bytes at the 5.27 TB/s of a large copy
-// in brackets): quantise 7168 columns 55 us (67), back 60 (67); SwiGLU of 2048 pairs 43 (51), its
-// backward with the activation again 52 (64).
+// 16 bytes of values a lane, no LDS.  MI355X, 16,384 rows, bf16, in loops over three sets of inputs (bytes at
+// the 5.27 TB/s of a large copy in brackets): quantise 7168 columns 55 us (67), back 66 (67); SwiGLU of 2048
+// pairs 44 (51), its backward with the activation again 52 (64).  Alone under a profiler, with the caches as
+// the other kernels of a pass leave them, 61, 60, 48 and 53 at the least.
 //
 // A chunk is 16 bytes of values, kN elements; the 32 / kN lanes of a group (4 of a 16-bit type,
 // 8 of fp32) hold one block.  Rows are whole blocks, so a group's chunks are of one row, and
