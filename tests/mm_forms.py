@@ -1,4 +1,5 @@
 """Runs csrc/mm_forms_check.cpp: which form a call of the 16-bit grouped product takes (host only)."""
+import functools
 import os
 import shutil
 import subprocess
@@ -13,11 +14,14 @@ def compiler():
     return shutil.which("amdclang++") or "/opt/rocm/bin/amdclang++"
 
 
+@functools.lru_cache(None)
 def program(exe, *flags):
     exe = str(exe)
     os.makedirs(os.path.dirname(exe), exist_ok=True)
-    subprocess.run([compiler(), "-O2", "-std=c++17", "-Wall", "-Werror", *flags, "-o", exe,
+    mine = f"{exe}.{os.getpid()}"  # (another process may be running, or making, the same)
+    subprocess.run([compiler(), "-O2", "-std=c++17", "-Wall", "-Werror", *flags, "-o", mine,
                     os.path.join(build.CSRC, "mm_forms_check.cpp")], check=True)
+    os.replace(mine, exe)
     return exe
 
 

@@ -57,6 +57,16 @@ def test_sums_are_touched_by_mfmas_alone(listings, name):
         assert not other_uses(b), other_uses(b)[:4]
 
 
+@pytest.mark.parametrize("name", [f for f in FILES if f != "grouped_mm_out"])
+def test_no_block_of_mfmas_touches_the_sums_otherwise(listings, name):
+    """Also the blocks that a branch cuts a loop into, of which only one has loads to LDS.  (The forward's
+    form of few rows has MFMAs that the compiler knows and sees to itself.)"""
+    many = [b for b in blocks(listings[name]) if sum(bool(re.match(r"v_mfma\S+ a\[", o)) for o in b) >= 8]
+    assert len(many) >= (8 if "rows" in name else 4)
+    for b in many:
+        assert not other_uses(b), other_uses(b)[:4]
+
+
 @pytest.mark.parametrize("name", FILES)
 def test_nothing_spills_to_memory(listings, name):
     assert set(re.findall(r"\.vgpr_spill_count:\s+(\d+)", listings[name])) == {"0"}
